@@ -22,38 +22,38 @@ DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
 def listed():
     return [
         # one generated token for each of four chats: the conv step of a d_inner 5120 layer, all latency
-        dict(name="conv step, 4 requests", op="conv", form="step", tokens=4, seqs=4, dim=5120, width=4, dtype="bf16"),
+        dict(name="conv step 4", op="conv", form="step", tokens=4, seqs=4, dim=5120, width=4, dtype="bf16"),
         # a prefill batch of ragged prompts through the conv, half of them continuing a cached history
-        dict(name="conv prompts, 16384 tokens", op="conv", form="prompts", tokens=16384, seqs=24, dim=5120, width=4,
+        dict(name="conv prompts 16384", op="conv", form="prompts", tokens=16384, seqs=24, dim=5120, width=4,
              dtype="bf16"),
         # the conv's gradients in a training step of the same layer (x is half of the projection's rows)
-        dict(name="conv gradients, 2x8192x5120", op="conv_grad", batch=2, tokens=8192, dim=5120, width=4, dtype="bf16",
+        dict(name="conv gradients 2x8192x5120", op="conv_grad", batch=2, tokens=8192, dim=5120, width=4, dtype="bf16",
              silu=True),
         # the same for a small odd layer in fp32: nothing divides evenly
-        dict(name="conv gradients, 3x1001x777", op="conv_grad", batch=3, tokens=1001, dim=777, width=3, dtype="fp32",
+        dict(name="conv gradients 3x1001x777", op="conv_grad", batch=3, tokens=1001, dim=777, width=3, dtype="fp32",
              silu=False),
         # one token for each of three chats through the scan's state, fp32
-        dict(name="scan step, 3 requests", op="scan", form="step", tokens=3, seqs=3, dim=2048, dstate=16, dtype="fp32"),
+        dict(name="scan step 3", op="scan", form="step", tokens=3, seqs=3, dim=2048, dstate=16, dtype="fp32"),
         # a full decode batch: 256 requests of a d_inner 5120 layer, bound by moving their states
-        dict(name="scan step, 256 requests", op="scan", form="step", tokens=256, seqs=256, dim=5120, dstate=16,
+        dict(name="scan step 256", op="scan", form="step", tokens=256, seqs=256, dim=5120, dstate=16,
              dtype="bf16"),
         # a ragged prefill batch of a d_inner 2048 layer, odd token count
-        dict(name="scan prompts, 9001 tokens", op="scan", form="prompts", tokens=9001, seqs=40, dim=2048, dstate=16,
+        dict(name="scan prompts 9001", op="scan", form="prompts", tokens=9001, seqs=40, dim=2048, dstate=16,
              dtype="bf16"),
         # few long documents: parallelism has to come from the time axis
-        dict(name="scan prompts, 32768 tokens", op="scan", form="prompts", tokens=32768, seqs=3, dim=5120, dstate=16,
+        dict(name="scan prompts 32768", op="scan", form="prompts", tokens=32768, seqs=3, dim=5120, dstate=16,
              dtype="bf16"),
         # the gated norm of a decode batch, groups of 640 channels, norm before the gate
-        dict(name="gated norm, 256 rows", op="gated_norm", train=False, rows=256, dim=5120, groups=8, norm_first=True,
+        dict(name="gated norm 256", op="gated_norm", train=False, rows=256, dim=5120, groups=8, norm_first=True,
              dtype="bf16"),
         # the gated norm of a training step: fp32 scan output, gate first, forward and gradients
-        dict(name="gated norm training, 16384 rows", op="gated_norm", train=True, rows=16384, dim=5120, groups=1,
+        dict(name="gated norm training 16384", op="gated_norm", train=True, rows=16384, dim=5120, groups=1,
              norm_first=False, dtype="bf16"),
         # residual add and the next block's norm for a decode batch of an odd size
-        dict(name="residual norm, 37 rows", op="residual_norm", train=False, rows=37, dim=2560, post=False,
+        dict(name="residual norm 37", op="residual_norm", train=False, rows=37, dim=2560, post=False,
              dtype="bf16"),
         # norms on both sides of the block with a learned residual scale, forward and gradients
-        dict(name="residual norm training, 16384 rows", op="residual_norm", train=True, rows=16384, dim=2560, post=True,
+        dict(name="residual norm training 16384", op="residual_norm", train=True, rows=16384, dim=2560, post=True,
              dtype="bf16"),
     ]
 
