@@ -1,7 +1,7 @@
 /*
  * sss.h -- C ABI of the MI355X (gfx950) selective-scan library, libsss.so.
  *
- * Five operations, all fully computed by hand-written HIP kernels on the device:
+ * The operations, all fully computed by hand-written HIP kernels on the device:
  *
  *  selective_scan_fwd  -- the selective (input-dependent) state-space recurrence of
  *      "Selective Scan trong Mamba toi uu chuoi dai the nao?" (thecsnote.cc), sections
@@ -26,6 +26,11 @@
  *
  *  causal_conv1d_fwd -- the causal depthwise convolution (+ silu) that produces the
  *      scan's input x in the Mamba block.
+ *
+ *  causal_conv1d_packed_fwd, selective_scan_packed_fwd -- the same convolution and scan over
+ *      packed prompts of any lengths, the history and state of every sequence in cache slots;
+ *      causal_conv1d_update, selective_state_update_slots -- their single-token steps on those
+ *      slots; causal_conv1d_bwd -- the convolution's gradients.
  *
  *  elementwise_scan -- the per-channel form of "15. Selective (Data-Dependent) SSM
  *      Scan" (Reference solution): h = A_t*h + B_t*x_t, y_t = C_t*h.
@@ -243,6 +248,88 @@ int selective_scan_fwd_ex(const void* x, const void* delta, const float* A, cons
  * otherwise).  out may not overlap x, weight or bias.  No workspace.  Returns an sss_status. */
 int causal_conv1d_fwd(const void* x, const float* weight, const float* bias, void* out, int64_t batch,
                       int64_t seqlen, int64_t dim, int64_t width, int io_dtype, int apply_silu, sss_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Serving and training around the scan.  These calls differ from those above in two
+ * conventions: rows may be strided (a row is dim adjacent elements, `*_stride` elements after
+ * the row before it, so that halves of a projection's output are taken as they lie; at least
+ * dim, at most 2^24, SSS_ERR_BAD_DIM otherwise), and pointers need only their element type's
+ * alignment (the workspace 16 bytes).  The memory an argument takes, for the overlap rule, is
+ * that from its first to its last element.
+ *
+ * Packed prompts: `tokens` rows hold the sequences one after the other; sequence s is rows
+ * cu_seqlens[s] .. cu_seqlens[s+1]-1 (nseq + 1 device integers, not decreasing, in [0, tokens]).
+ * A sequence may be empty: its slot is then left alone.  Rows outside every sequence are
+ * neither read nor written.  The device never reads or writes out of range whatever these
+ * integers hold, but the results are only defined as above.
+ *
+ * Cache slots: sequence (or decode row) s keeps its history or state in slot state_indices[s]
+ * of `slots`, or in slot s where state_indices is NULL (then nseq <= slots: SSS_ERR_BAD_DIM).
+ * An index outside 0 .. slots-1, -1 by custom for the padding of a batch, is no slot: the
+ * sequence starts from zero and keeps nothing.  Two sequences of one call may not share a
+ * slot (their results are then undefined).  A call with no tokens or no sequences returns
+ * SSS_OK and does nothing. */
+
+/* causal_conv1d_fwd over packed prompts.  x (tokens, dim) with x_stride; conv_state (slots,
+ * width-1, dim) in io_dtype, nullable (nothing is kept), updated in place: the last width-1
+ * inputs of each sequence's history and tokens.  has_initial (nseq bytes, nullable): the
+ * sequences marked non-zero continue what their slot holds, the others start from zero
+ * history.  out (tokens, dim) contiguous.  Required: x, weight, cu_seqlens, out. */
+int causal_conv1d_packed_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias, void* conv_state,
+                             const int32_t* cu_seqlens, const int32_t* state_indices, const uint8_t* has_initial,
+                             void* out, int64_t tokens, int64_t nseq, int64_t slots, int64_t dim, int64_t width,
+                             int io_dtype, int apply_silu, sss_stream_t stream);
+
+/* The single-token step of the same convolution: x (batch, dim) with x_stride holds one new
+ * input per row, every row continues its slot.  out (batch, dim).  Required: x, weight,
+ * conv_state (unless width is 1), out. */
+int causal_conv1d_update(const void* x, int64_t x_stride, const float* weight, const float* bias, void* conv_state,
+                         const int32_t* state_indices, void* out, int64_t batch, int64_t slots, int64_t dim,
+                         int64_t width, int io_dtype, int apply_silu, sss_stream_t stream);
+
+/* Bytes of workspace causal_conv1d_bwd needs on `device` (0 on invalid sizes). */
+size_t causal_conv1d_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype,
+                                        int device);
+
+/* Gradients of causal_conv1d_fwd: with L = sum(dout * out), dx = dL/dx (batch, seqlen, dim),
+ * dweight (dim, width) and dbias (dim) float32.  The pre-activation is recomputed.  x and dx have a
+ * row and a batch stride (dx's batch rows may not share elements: SSS_ERR_BAD_DIM); dout is
+ * contiguous; dout and dx are each float32 or io_dtype (SSS_ERR_UNSUPPORTED otherwise).
+ * Required: x, weight, dout, dx, dweight; dbias with bias.  The sums over batch and time are
+ * formed in a fixed order: results are deterministic. */
+int causal_conv1d_bwd(const void* x, int64_t x_batch_stride, int64_t x_stride, const float* weight, const float* bias,
+                      const void* dout, void* dx, int64_t dx_batch_stride, int64_t dx_stride, float* dweight,
+                      float* dbias, int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype,
+                      int dout_dtype, int dx_dtype, int apply_silu, void* workspace, size_t workspace_bytes,
+                      sss_stream_t stream);
+
+/* Bytes of workspace selective_scan_packed_fwd needs on `device` (0 on invalid sizes, and where
+ * none is needed); it depends on the token count alone, not on the sequences. */
+size_t selective_scan_packed_fwd_workspace_size(int64_t tokens, int64_t dim, int64_t dstate, int device);
+
+/* selective_scan_fwd over packed prompts, through the delta front end (delta_bias nullable,
+ * flags 0 or SSS_DELTA_SOFTPLUS).  x, delta, z (tokens, dim) in io_dtype, B and C (tokens,
+ * dstate) in bc_dtype, each with its stride; state (slots, dim, dstate) float32, nullable
+ * (every sequence starts from zero and nothing is kept), updated in place to each sequence's
+ * last state; has_initial as above.  y (tokens, dim) contiguous in y_dtype, rounded once.
+ * Required: x, delta, A, B, C, cu_seqlens, y.  dim * dstate must not exceed 2^30. */
+int selective_scan_packed_fwd(const void* x, int64_t x_stride, const void* delta, int64_t delta_stride, const float* A,
+                              const void* B, int64_t b_stride, const void* C, int64_t c_stride, const float* D_skip,
+                              const void* z, int64_t z_stride, const float* delta_bias, unsigned flags, float* state,
+                              const int32_t* cu_seqlens, const int32_t* state_indices, const uint8_t* has_initial,
+                              void* y, int64_t tokens, int64_t nseq, int64_t slots, int64_t dim, int64_t dstate,
+                              int io_dtype, int bc_dtype, int y_dtype, void* workspace, size_t workspace_bytes,
+                              sss_stream_t stream);
+
+/* One decode step on states in cache slots, through the delta front end: selective_state_update
+ * with strided operands, B and C in bc_dtype, y (batch, dim) in y_dtype, and row b's state in
+ * its slot (updated in place).  Required: x, delta, A, B, C, state, y.  No workspace. */
+int selective_state_update_slots(const void* x, int64_t x_stride, const void* delta, int64_t delta_stride,
+                                 const float* A, const void* B, int64_t b_stride, const void* C, int64_t c_stride,
+                                 const float* D_skip, const void* z, int64_t z_stride, const float* delta_bias,
+                                 unsigned flags, float* state, const int32_t* state_indices, void* y, int64_t batch,
+                                 int64_t slots, int64_t dim, int64_t dstate, int io_dtype, int bc_dtype, int y_dtype,
+                                 sss_stream_t stream);
 
 /* Bytes of workspace elementwise_scan needs for these sizes on `device`. */
 size_t elementwise_scan_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int device);

@@ -12,6 +12,11 @@ include/sss.h); this package is its thin Python binding:
   * ``selective_state_update(x, delta, A, B, C, D=None, z=None, state=...)`` -> y (one
     decode step; ``state`` is updated in place)
   * ``causal_conv1d_fwd(x, weight, bias=None, silu=False)`` -> out (the conv front end)
+  * ``causal_conv1d_packed_fwd`` / ``selective_scan_packed_fwd``: the convolution and the scan
+    over packed prompts of any lengths (``cu_seqlens``), each sequence's history or state in a
+    cache slot; ``causal_conv1d_update`` / ``selective_state_update_slots``: one token of each
+    request on the same caches
+  * ``causal_conv1d_bwd(x, weight, bias, dout=..., silu=False)`` -> the convolution's gradients
   * ``elementwise_scan(x, A, B, C, h0=None)`` -> (y, h_last)
   * ``*_workspace_size``, raw-pointer variants ``*_raw`` and ``status_string``.
 
@@ -26,8 +31,13 @@ from ._lib import (EXPORTED, LIB_PATH, SSSError, SSS_BF16, SSS_DELTA_SOFTPLUS, S
                    selective_scan_fwd_workspace_size, selective_scan_fwd_ex_workspace_size,
                    selective_state_update, selective_state_update_raw,
                    status_string)
+from ._block import (causal_conv1d_bwd, causal_conv1d_bwd_workspace_size, causal_conv1d_packed_fwd,
+                     causal_conv1d_update, selective_scan_packed_fwd, selective_scan_packed_fwd_workspace_size,
+                     selective_state_update_slots)
 
-__all__ = ["selective_scan_fwd", "selective_scan_bwd", "selective_scan_bwd_raw", "selective_scan_bwd_ex_raw", "selective_scan_bwd_workspace_size",
+__all__ = ["causal_conv1d_packed_fwd", "causal_conv1d_update", "causal_conv1d_bwd", "causal_conv1d_bwd_workspace_size",
+           "selective_scan_packed_fwd", "selective_scan_packed_fwd_workspace_size", "selective_state_update_slots",
+           "selective_scan_fwd", "selective_scan_bwd", "selective_scan_bwd_raw", "selective_scan_bwd_ex_raw", "selective_scan_bwd_workspace_size",
            "selective_state_update", "causal_conv1d_fwd", "causal_conv1d_fwd_raw", "selective_state_update_raw", "elementwise_scan",
            "selective_scan_fwd_workspace_size",
            "elementwise_scan_workspace_size", "selective_scan_fwd_raw", "elementwise_scan_raw", "status_string",

@@ -1,0 +1,289 @@
+"""Binding of the operators around the scan: the convolution and the scan over packed prompts
+and their single-token steps on cache slots, and the convolution's gradients.
+
+As in ``_lib``, only argument checks, output allocation and the C call: every step of the
+computation runs in the library's HIP kernels.
+"""
+from __future__ import annotations
+
+from . import _lib
+from ._lib import SSS_BF16, SSS_DELTA_SOFTPLUS, SSS_F32, SSSError, load
+
+
+def _rows(t, name, dtype, rows, dim, device):
+    """Checks a (rows, dim) tensor whose rows may be strided; returns (pointer, row stride)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.ndim != 2 or t.shape[0] != rows or t.shape[1] != dim:
+        raise ValueError(f"{name} must have shape {(rows, dim)}, got {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU ({device}), got {t.device}")
+    s0, s1 = t.stride()
+    if s1 != 1 and dim != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent, got strides {(s0, s1)}")
+    if rows > 1 and s0 < dim:
+        raise ValueError(f"{name}: rows must not overlap, got strides {(s0, s1)}")
+    return t.data_ptr(), max(s0, dim)
+
+
+def _dense(t, name, dtype, shape, device):
+    """Checks a contiguous tensor on the call's GPU; returns its pointer (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU ({device}), got {t.device}")
+    return t.data_ptr()
+
+
+def _code(dtype, name):
+    import torch
+    if dtype == torch.bfloat16:
+        return SSS_BF16
+    if dtype == torch.float32:
+        return SSS_F32
+    raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+
+
+def _two_d(t, name):
+    if t.ndim != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _stream(stream, device):
+    if stream is not None:
+        return stream
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _cache(state, name, dtype, tail, device):
+    """A (slots, *tail) cache; returns (pointer, slots)."""
+    if state is None:
+        return 0, 0
+    if state.ndim != 1 + len(tail) or state.shape[0] < 1:
+        raise ValueError(f"{name} must have shape (slots, {', '.join(map(str, tail))}), got {tuple(state.shape)}")
+    slots = state.shape[0]
+    return _dense(state, name, dtype, (slots, *tail), device), slots
+
+
+def _sequences(cu_seqlens, state_indices, has_initial, state, slots, device):
+    """Checks what describes a packed batch; returns (nseq, cu, indices, initial) with pointers."""
+    import torch
+    if cu_seqlens.ndim != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError(f"cu_seqlens must be 1-D with one entry more than sequences, got {tuple(cu_seqlens.shape)}")
+    nseq = cu_seqlens.shape[0] - 1
+    cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), device)
+    idx = _dense(state_indices, "state_indices", torch.int32, (nseq,), device)
+    if state is not None and state_indices is None and nseq > slots:
+        raise ValueError(f"{nseq} sequences need as many slots or state_indices, the cache has {slots}")
+    if state is None and has_initial is not None:
+        raise ValueError("has_initial needs a cache to start from")
+    ini = 0
+    if has_initial is not None:
+        if has_initial.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"has_initial must be bool or uint8, got {has_initial.dtype}")
+        ini = _dense(has_initial, "has_initial", has_initial.dtype, (nseq,), device)
+    return nseq, cu, idx, ini
+
+
+def causal_conv1d_packed_fwd(x, weight, bias=None, *, cu_seqlens, conv_state=None, state_indices=None,
+                             has_initial=None, silu=False, out=None, stream=None):
+    """Causal depthwise convolution over packed prompts: out (tokens, dim) in x's dtype.
+
+    x (tokens, dim) float32 or bfloat16, rows may be strided; weight (dim, width), bias (dim)
+    float32; cu_seqlens (nseq + 1) int32.  conv_state (slots, width-1, dim) in x's dtype keeps
+    each sequence's last width-1 inputs (updated in place) in slot state_indices[s] (int32; None:
+    slot s; -1: none); has_initial (nseq) bool marks the sequences that continue their slot.
+    Rows outside every sequence are left as they are in ``out``."""
+    import torch
+    dev = x.device
+    tokens, dim = _two_d(x, "x")
+    code = _code(x.dtype, "x")
+    xp, xs = _rows(x, "x", x.dtype, tokens, dim, dev)
+    width = _two_d(weight, "weight")[1]
+    wp = _dense(weight, "weight", torch.float32, (dim, width), dev)
+    bp = _dense(bias, "bias", torch.float32, (dim,), dev)
+    sp, slots = _cache(conv_state, "conv_state", x.dtype, (width - 1, dim), dev)
+    nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, conv_state, slots, dev)
+    o = out if out is not None else torch.empty((tokens, dim), dtype=x.dtype, device=dev)
+    op = _dense(o, "out", x.dtype, (tokens, dim), dev)
+    if tokens == 0:
+        return o
+    rc = load().causal_conv1d_packed_fwd(xp, xs, wp, bp, sp, cu, idx, ini, op, tokens, nseq, slots if sp else 0, dim,
+                                         width, code, int(bool(silu)), _stream(stream, dev))
+    if rc != 0:
+        raise SSSError(rc, "causal_conv1d_packed_fwd")
+    return o
+
+
+def causal_conv1d_update(x, weight, bias=None, *, conv_state, state_indices=None, silu=False, out=None, stream=None):
+    """One token of each row through the convolution: out (batch, dim) in x's dtype.
+
+    x (batch, dim), rows may be strided; conv_state (slots, width-1, dim) in x's dtype, updated
+    in place, row b's in slot state_indices[b] (int32; None: slot b; -1: none, the row starts
+    from zeros and keeps nothing)."""
+    import torch
+    dev = x.device
+    batch, dim = _two_d(x, "x")
+    code = _code(x.dtype, "x")
+    xp, xs = _rows(x, "x", x.dtype, batch, dim, dev)
+    width = _two_d(weight, "weight")[1]
+    wp = _dense(weight, "weight", torch.float32, (dim, width), dev)
+    bp = _dense(bias, "bias", torch.float32, (dim,), dev)
+    sp, slots = _cache(conv_state, "conv_state", x.dtype, (width - 1, dim), dev)
+    idx = _dense(state_indices, "state_indices", torch.int32, (batch,), dev)
+    if state_indices is None and batch > slots:
+        raise ValueError(f"{batch} rows need as many slots or state_indices, the cache has {slots}")
+    o = out if out is not None else torch.empty((batch, dim), dtype=x.dtype, device=dev)
+    op = _dense(o, "out", x.dtype, (batch, dim), dev)
+    if batch == 0:
+        return o
+    rc = load().causal_conv1d_update(xp, xs, wp, bp, sp, idx, op, batch, slots, dim, width, code, int(bool(silu)),
+                                     _stream(stream, dev))
+    if rc != 0:
+        raise SSSError(rc, "causal_conv1d_update")
+    return o
+
+
+def causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, io_dtype=SSS_BF16, device=0) -> int:
+    return int(load().causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, io_dtype, device))
+
+
+def _blocks(t, name, shape, device):
+    """Checks a (batch, rows, dim) tensor whose rows and batch entries may be strided; returns
+    (pointer, batch stride, row stride)."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU ({device}), got {t.device}")
+    batch, rows, dim = shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and dim != 1) or (rows > 1 and s1 < dim):
+        raise ValueError(f"{name}: rows must be {dim} adjacent elements, got strides {(s0, s1, s2)}")
+    return t.data_ptr(), s0, max(s1, dim)
+
+
+def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, workspace=None, stream=None):
+    """Gradients of sum(dout * causal_conv1d_fwd(x, weight, bias, silu=silu)).
+
+    x (batch, seqlen, dim) float32 or bfloat16, dense or strided in batch and time; dout (batch,
+    seqlen, dim) float32 or x's dtype, contiguous.  Returns a dict of dx (x's dtype, or that of
+    the given ``dx`` tensor: float32 or x's dtype, strided or not), dweight (dim, width) and,
+    with a bias, dbias (dim), both float32."""
+    import torch
+    dev = x.device
+    if x.ndim != 3:
+        raise ValueError(f"x must be (batch, seqlen, dim), got shape {tuple(x.shape)}")
+    batch, seqlen, dim = x.shape
+    code = _code(x.dtype, "x")
+    width = _two_d(weight, "weight")[1]
+    if dout.dtype not in (torch.float32, x.dtype):
+        raise ValueError(f"dout must be float32 or {x.dtype}, got {dout.dtype}")
+    xp, xb, xr = _blocks(x, "x", (batch, seqlen, dim), dev)
+    wp = _dense(weight, "weight", torch.float32, (dim, width), dev)
+    bp = _dense(bias, "bias", torch.float32, (dim,), dev)
+    dp = _dense(dout, "dout", dout.dtype, (batch, seqlen, dim), dev)
+    g = {"dx": dx if dx is not None else torch.empty((batch, seqlen, dim), dtype=x.dtype, device=dev),
+         "dweight": torch.empty((dim, width), dtype=torch.float32, device=dev)}
+    if g["dx"].dtype not in (torch.float32, x.dtype):
+        raise ValueError(f"dx must be float32 or {x.dtype}, got {g['dx'].dtype}")
+    gp, gb, gr = _blocks(g["dx"], "dx", (batch, seqlen, dim), dev)
+    if bias is not None:
+        g["dbias"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+    if workspace is None:
+        n = causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, code, dev.index or 0)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    wsp, wsn = _lib._workspace(workspace, dev)
+    rc = load().causal_conv1d_bwd(xp, xb, xr, wp, bp, dp, gp, gb, gr, g["dweight"].data_ptr(),
+                                  g["dbias"].data_ptr() if bias is not None else 0, batch, seqlen, dim, width, code,
+                                  _code(dout.dtype, "dout"), _code(g["dx"].dtype, "dx"), int(bool(silu)), wsp, wsn,
+                                  _stream(stream, dev))
+    if rc != 0:
+        raise SSSError(rc, "causal_conv1d_bwd")
+    return g
+
+
+def _scan_operands(x, delta, A, B, C, D, z, delta_bias):
+    """The scan's operands, checked, as the leading arguments of the C calls."""
+    import torch
+    dev = x.device
+    rows, dim = _two_d(x, "x")
+    code = _code(x.dtype, "x")
+    n = _two_d(A, "A")[1]
+    bc = _code(B.dtype, "B")
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
+    dp, ds = _rows(delta, "delta", x.dtype, rows, dim, dev)
+    Ap = _dense(A, "A", torch.float32, (dim, n), dev)
+    Bp, bs = _rows(B, "B", B.dtype, rows, n, dev)
+    Cp, cs = _rows(C, "C", B.dtype, rows, n, dev)
+    zp, zs = _rows(z, "z", x.dtype, rows, dim, dev) if z is not None else (0, 0)
+    Dp = _dense(D, "D", torch.float32, (dim,), dev)
+    bp = _dense(delta_bias, "delta_bias", torch.float32, (dim,), dev)
+    return (xp, xs, dp, ds, Ap, Bp, bs, Cp, cs, Dp, zp, zs, bp), rows, dim, n, code, bc, dev
+
+
+def selective_scan_packed_fwd_workspace_size(tokens, dim, dstate, device=0) -> int:
+    return int(load().selective_scan_packed_fwd_workspace_size(tokens, dim, dstate, device))
+
+
+def selective_scan_packed_fwd(x, delta, A, B, C, D=None, z=None, *, cu_seqlens, state=None, state_indices=None,
+                              has_initial=None, delta_bias=None, delta_softplus=False, out=None, workspace=None,
+                              stream=None):
+    """The selective scan over packed prompts: y (tokens, dim), float32 or ``out``'s dtype.
+
+    x, delta, z (tokens, dim) float32 or bfloat16 (one dtype), B, C (tokens, dstate) float32 or
+    bfloat16 (one dtype), rows may be strided; A (dim, dstate), D, delta_bias (dim) float32;
+    cu_seqlens (nseq + 1) int32.  state (slots, dim, dstate) float32 keeps each sequence's last
+    state (updated in place) in slot state_indices[s] (int32; None: slot s; -1: none);
+    has_initial (nseq) bool marks the sequences that continue their slot.  Rows outside every
+    sequence are left as they are in ``out``."""
+    import torch
+    ops, tokens, dim, n, code, bc, dev = _scan_operands(x, delta, A, B, C, D, z, delta_bias)
+    sp, slots = _cache(state, "state", torch.float32, (dim, n), dev)
+    nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, state, slots, dev)
+    y = out if out is not None else torch.empty((tokens, dim), dtype=torch.float32, device=dev)
+    yc = _code(y.dtype, "out")
+    yp = _dense(y, "out", y.dtype, (tokens, dim), dev)
+    if tokens == 0:
+        return y
+    if workspace is None:
+        nb = selective_scan_packed_fwd_workspace_size(tokens, dim, n, dev.index or 0)
+        workspace = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    wsp, wsn = _lib._workspace(workspace, dev)
+    rc = load().selective_scan_packed_fwd(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, cu, idx, ini, yp,
+                                          tokens, nseq, slots, dim, n, code, bc, yc, wsp, wsn, _stream(stream, dev))
+    if rc != 0:
+        raise SSSError(rc, "selective_scan_packed_fwd")
+    return y
+
+
+def selective_state_update_slots(x, delta, A, B, C, D=None, z=None, *, state, state_indices=None, delta_bias=None,
+                                 delta_softplus=False, out=None, stream=None):
+    """One decode step on cache slots: y (batch, dim), float32 or ``out``'s dtype.
+
+    Operands as selective_scan_packed_fwd with one row per request; state (slots, dim, dstate)
+    float32 updated in place, row b's in slot state_indices[b] (int32; None: slot b; -1: none, the
+    row starts from zero and keeps nothing)."""
+    import torch
+    ops, batch, dim, n, code, bc, dev = _scan_operands(x, delta, A, B, C, D, z, delta_bias)
+    sp, slots = _cache(state, "state", torch.float32, (dim, n), dev)
+    idx = _dense(state_indices, "state_indices", torch.int32, (batch,), dev)
+    if state_indices is None and batch > slots:
+        raise ValueError(f"{batch} rows need as many slots or state_indices, the cache has {slots}")
+    y = out if out is not None else torch.empty((batch, dim), dtype=torch.float32, device=dev)
+    yc = _code(y.dtype, "out")
+    yp = _dense(y, "out", y.dtype, (batch, dim), dev)
+    if batch == 0:
+        return y
+    rc = load().selective_state_update_slots(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, idx, yp, batch,
+                                             slots, dim, n, code, bc, yc, _stream(stream, dev))
+    if rc != 0:
+        raise SSSError(rc, "selective_state_update_slots")
+    return y

@@ -24,7 +24,10 @@ EXPORTED = ("selective_scan_fwd", "selective_scan_fwd_ex", "selective_scan_fwd_w
             "causal_conv1d_fwd", "selective_scan_bwd", "selective_scan_bwd_workspace_size",
             "elementwise_scan", "elementwise_scan_workspace_size", "sss_status_string",
             "selective_scan_fwd_noalloc", "selective_scan_states_size", "selective_scan_fwd_save",
-            "selective_scan_bwd_saved", "selective_scan_bwd_ex")
+            "selective_scan_bwd_saved", "selective_scan_bwd_ex",
+            "causal_conv1d_packed_fwd", "causal_conv1d_update", "causal_conv1d_bwd",
+            "causal_conv1d_bwd_workspace_size", "selective_scan_packed_fwd",
+            "selective_scan_packed_fwd_workspace_size", "selective_state_update_slots")
 
 
 class SSSError(RuntimeError):
@@ -79,6 +82,23 @@ def load() -> ctypes.CDLL:
         lib.selective_scan_bwd_saved.restype = i32
         lib.selective_scan_bwd_ex.argtypes = [vp] * 11 + [ctypes.c_uint] + [vp] * 9 + [i64] * 4 + [i32, vp, sz, vp]
         lib.selective_scan_bwd_ex.restype = i32
+        u32 = ctypes.c_uint
+        lib.causal_conv1d_packed_fwd.argtypes = [vp, i64] + [vp] * 7 + [i64] * 5 + [i32, i32, vp]
+        lib.causal_conv1d_packed_fwd.restype = i32
+        lib.causal_conv1d_update.argtypes = [vp, i64] + [vp] * 5 + [i64] * 4 + [i32, i32, vp]
+        lib.causal_conv1d_update.restype = i32
+        lib.causal_conv1d_bwd.argtypes = ([vp, i64, i64] + [vp] * 4 + [i64, i64] + [vp] * 2 + [i64] * 4 + [i32] * 4
+                                          + [vp, sz, vp])
+        lib.causal_conv1d_bwd.restype = i32
+        lib.causal_conv1d_bwd_workspace_size.argtypes = [i64] * 4 + [i32, i32]
+        lib.causal_conv1d_bwd_workspace_size.restype = sz
+        scan = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp, u32, vp]
+        lib.selective_scan_packed_fwd.argtypes = scan + [vp] * 4 + [i64] * 5 + [i32] * 3 + [vp, sz, vp]
+        lib.selective_scan_packed_fwd.restype = i32
+        lib.selective_scan_packed_fwd_workspace_size.argtypes = [i64] * 3 + [i32]
+        lib.selective_scan_packed_fwd_workspace_size.restype = sz
+        lib.selective_state_update_slots.argtypes = scan + [vp] * 2 + [i64] * 4 + [i32] * 3 + [vp]
+        lib.selective_state_update_slots.restype = i32
         lib.sss_status_string.argtypes = [i32]
         lib.sss_status_string.restype = ctypes.c_char_p
         _lib = lib

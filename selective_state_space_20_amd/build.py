@@ -1,7 +1,7 @@
 """Build libsss.so (gfx950) in-tree with hipcc.  No JIT, no torch extension machinery.
 
-Every source is compiled to an object in parallel (the selective scan once per state
-count, see the explicit instances at the end of csrc/selective_scan.hip), then the objects
+Every source is compiled to an object in parallel (the selective scans once per state
+count, see the explicit instances at the end of csrc/selective_scan.hip and packed_scan.hip), then the objects
 are linked into the shared library.  Objects live in _build/ at the repository root.
 """
 from __future__ import annotations
@@ -41,7 +41,7 @@ def compile_jobs():
     jobs = []
     for src in sources():
         stem = os.path.splitext(os.path.basename(src))[0]
-        if stem == "selective_scan":
+        if stem in ("selective_scan", "packed_scan"):
             jobs.append((os.path.join(OBJ, f"{stem}_host.o"), [], src))
             for n in STATE_COUNTS:
                 jobs.append((os.path.join(OBJ, f"{stem}_n{n}.o"), [f"-DSSS_INST_NS={n}"], src))

@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "api_util.h"
 #include "kernels.h"
 
 namespace sss {
@@ -20,10 +21,8 @@ int env_int(const char* name, int dflt) {
   return std::atoi(v);
 }
 
-namespace {
-
 constexpr int kMaxDevices = 64;
-std::atomic<int> g_cus[kMaxDevices];  // 0 = unknown
+static std::atomic<int> g_cus[kMaxDevices];  // 0 = unknown
 
 // Compute units of `device` (cached); -1 if it cannot be queried.
 int device_cus(int device) {
@@ -48,27 +47,6 @@ int current_device_cus() {
   return device_cus(dev);
 }
 
-// Sizes in bytes with overflow checks; false when a product leaves [0, 2^62).
-bool mul_ok(int64_t a, int64_t b, int64_t* out) {
-  if (a < 0 || b < 0) return false;
-  if (a != 0 && b > (int64_t(1) << 62) / a) return false;
-  *out = a * b;
-  return true;
-}
-
-struct Range {
-  uintptr_t lo, hi;
-};
-
-bool overlap(const void* p, int64_t bytes, const void* q, int64_t qbytes) {
-  if (p == nullptr || q == nullptr || bytes <= 0 || qbytes <= 0) return false;
-  uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + (uintptr_t)qbytes && b < a + (uintptr_t)bytes;
-}
-
-bool aligned16(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-}  // namespace
 }  // namespace sss
 
 using namespace sss;

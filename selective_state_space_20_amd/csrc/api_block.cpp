@@ -1,0 +1,295 @@
+// api_block.cpp -- the C ABI of the operators around the scan (declared in include/sss.h): the
+// packed convolution, scan and their token steps, and the convolution's gradients.
+#include "sss.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdio>
+
+#include "api_util.h"
+#include "kernels.h"
+
+using namespace sss;
+
+namespace {
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // token numbers are 32-bit on the device
+constexpr int64_t kMaxRowDim = (int64_t)1 << 24;  // as the scan's dim; also the largest row stride
+
+bool dtype_ok(int t) { return t == SSS_F32 || t == SSS_BF16; }
+int64_t dtype_size(int t) { return t == SSS_BF16 ? 2 : 4; }
+bool stride_ok(int64_t stride, int64_t dim) { return stride >= dim && stride <= kMaxRowDim; }
+int status_of(hipError_t e) { return e == hipSuccess ? SSS_OK : SSS_ERR_HIP; }
+
+int conv_impl(const void* x, int64_t x_stride, const float* weight, const float* bias, void* conv_state,
+              const int32_t* cu_seqlens, const int32_t* state_indices, const uint8_t* has_initial, void* out,
+              int64_t tokens, int64_t nseq, int64_t slots, int64_t dim, int64_t width, int io_dtype, int apply_silu,
+              bool step, sss_stream_t stream) {
+  if (!x || !weight || !out || (step ? !conv_state && width != 1 : !cu_seqlens)) return SSS_ERR_NULL_ARG;
+  if (tokens < 0 || nseq < 0 || slots < 0 || dim < 1 || tokens > kMaxTokens || nseq > kMaxTokens ||
+      slots > kMaxTokens || dim > kMaxRowDim ||
+      (conv_state && (slots < 1 || (!state_indices && nseq > slots))))
+    return SSS_ERR_BAD_DIM;
+  if (width < 1 || width > 8 || !dtype_ok(io_dtype)) return SSS_ERR_UNSUPPORTED;
+  if (!stride_ok(x_stride, dim)) return SSS_ERR_BAD_DIM;
+  // threads of the launch: 256 per row and 512 channels, or 64 per 32 tokens and 128 channels
+  const double threads = step ? (double)tokens * (double)((dim + 511) / 512) * 256.0
+                              : (double)(tokens / 32 + 1) * (double)((dim + 127) / 128) * 64.0;
+  if (threads > 2147483647.0) return SSS_ERR_BAD_DIM;
+  const int64_t es = dtype_size(io_dtype);
+  Regions r;
+  r.in(x, span(tokens, x_stride, dim, es), es);
+  r.in(weight, dim * width * 4, 4);
+  r.in(bias, dim * 4, 4);
+  r.in(cu_seqlens, (nseq + 1) * 4, 4);
+  r.in(state_indices, nseq * 4, 4);
+  r.in(has_initial, nseq, 1);
+  r.output(conv_state, slots * (width - 1) * dim * es, es);
+  r.output(out, tokens * dim * es, es);
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  if (tokens == 0 || nseq == 0) return SSS_OK;
+  const int cus = current_device_cus();
+  if (cus <= 0) return SSS_ERR_HIP;
+  PackedConvArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.w = weight;
+  a.bias = bias;
+  a.state = width > 1 ? conv_state : nullptr;  // one tap: nothing to keep
+  a.cu = cu_seqlens;
+  a.sidx = state_indices;
+  a.init = has_initial;
+  a.out = out;
+  a.tokens = tokens;
+  a.nseq = nseq;
+  a.slots = width > 1 ? slots : 0;
+  a.dim = dim;
+  a.width = (int)width;
+  a.bf16 = io_dtype == SSS_BF16;
+  a.silu = apply_silu != 0;
+  a.step = step;
+  return status_of(launch_packed_conv(a, cus, reinterpret_cast<hipStream_t>(stream)));
+}
+
+bool conv_bwd_dims_ok(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {
+  return batch >= 1 && seqlen >= 1 && dim >= 1 && width >= 1 && width <= 8 && batch <= kMaxTokens &&
+         seqlen <= kMaxTokens && dim <= kMaxRowDim &&
+         (double)batch * (double)seqlen * (double)((dim + 63) / 64) <= (double)((int64_t)1 << 36);
+}
+
+int scan_dims(int64_t tokens, int64_t nseq, int64_t slots, int64_t dim, int64_t dstate) {
+  if (tokens < 0 || nseq < 0 || slots < 0 || dim < 1 || dstate < 1 || tokens > kMaxTokens || nseq > kMaxTokens ||
+      slots > kMaxTokens || dim > kMaxRowDim)
+    return SSS_ERR_BAD_DIM;
+  if (dstate > 64 || (dstate & (dstate - 1)) != 0) return SSS_ERR_UNSUPPORTED;
+  if (dim * dstate > ((int64_t)1 << 30)) return SSS_ERR_BAD_DIM;
+  if ((double)tokens * (double)dim > 1.8e18) return SSS_ERR_BAD_DIM;
+  return SSS_OK;
+}
+
+int scan_impl(const void* x, int64_t x_stride, const void* delta, int64_t delta_stride, const float* A, const void* B,
+              int64_t b_stride, const void* C, int64_t c_stride, const float* D_skip, const void* z, int64_t z_stride,
+              const float* delta_bias, unsigned flags, float* state, const int32_t* cu_seqlens,
+              const int32_t* state_indices, const uint8_t* has_initial, void* y, int64_t tokens, int64_t nseq,
+              int64_t slots, int64_t dim, int64_t dstate, int io_dtype, int bc_dtype, int y_dtype, void* workspace,
+              size_t workspace_bytes, bool step, sss_stream_t stream) {
+  if (!x || !delta || !A || !B || !C || !y || (step ? !state : !cu_seqlens)) return SSS_ERR_NULL_ARG;
+  const int st = scan_dims(tokens, nseq, slots, dim, dstate);
+  if (st != SSS_OK) return st;
+  if (state && (slots < 1 || (!state_indices && nseq > slots))) return SSS_ERR_BAD_DIM;
+  if (!dtype_ok(io_dtype) || !dtype_ok(bc_dtype) || !dtype_ok(y_dtype)) return SSS_ERR_UNSUPPORTED;
+  if ((flags & ~(unsigned)SSS_DELTA_SOFTPLUS) != 0) return SSS_ERR_UNSUPPORTED;
+  if (!stride_ok(x_stride, dim) || !stride_ok(delta_stride, dim) || (z && !stride_ok(z_stride, dim)) ||
+      !stride_ok(b_stride, dstate) || !stride_ok(c_stride, dstate))
+    return SSS_ERR_BAD_DIM;
+  const int64_t es = dtype_size(io_dtype), bs = dtype_size(bc_dtype), ys = dtype_size(y_dtype);
+  Regions r;
+  r.in(x, span(tokens, x_stride, dim, es), es);
+  r.in(delta, span(tokens, delta_stride, dim, es), es);
+  r.in(A, dim * dstate * 4, 4);
+  r.in(B, span(tokens, b_stride, dstate, bs), bs);
+  r.in(C, span(tokens, c_stride, dstate, bs), bs);
+  r.in(D_skip, dim * 4, 4);
+  r.in(z, span(tokens, z_stride, dim, es), es);
+  r.in(delta_bias, dim * 4, 4);
+  r.in(cu_seqlens, (nseq + 1) * 4, 4);
+  r.in(state_indices, nseq * 4, 4);
+  r.in(has_initial, nseq, 1);
+  r.output(state, slots * dim * dstate * 4, 4);
+  r.output(y, tokens * dim * ys, ys);
+  if (workspace && !aligned16(workspace)) return SSS_ERR_UNSUPPORTED;
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  if (tokens == 0 || nseq == 0) return SSS_OK;
+  const int cus = current_device_cus();
+  if (cus <= 0) return SSS_ERR_HIP;
+  PackedScanArgs a{};
+  a.x = x;
+  a.delta = delta;
+  a.A = A;
+  a.B = B;
+  a.C = C;
+  a.Dsk = D_skip;
+  a.z = z;
+  a.delta_bias = delta_bias;
+  a.state = state;
+  a.cu = cu_seqlens;
+  a.sidx = state_indices;
+  a.init = has_initial;
+  a.y = y;
+  a.sx = x_stride;
+  a.sd = delta_stride;
+  a.sz = z ? z_stride : 0;
+  a.sb = b_stride;
+  a.sc = c_stride;
+  a.tokens = tokens;
+  a.nseq = nseq;
+  a.slots = slots;
+  a.dim = dim;
+  a.dstate = (int)dstate;
+  a.bf16 = io_dtype == SSS_BF16;
+  a.bc_bf16 = bc_dtype == SSS_BF16;
+  a.y_bf16 = y_dtype == SSS_BF16;
+  a.softplus = (flags & SSS_DELTA_SOFTPLUS) != 0;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (step) {
+    // one workgroup of 256 lanes per 256 pieces of four states; 32-bit grid
+    if ((double)tokens * ((double)dim * (double)dstate / 256.0 + 1.0) > 2147483647.0) return SSS_ERR_BAD_DIM;
+    return status_of(launch_slot_update(a, s));
+  }
+  const PackedScanPlan pl = plan_packed_scan(tokens, dim, dstate, cus);
+  if ((double)pl.chunks * (double)((dim + 63) / 64) > (double)((int64_t)1 << 24)) return SSS_ERR_BAD_DIM;
+  if (pl.ws_total > 0) {
+    if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
+    r.output(workspace, (int64_t)pl.ws_total, 16);
+    if (!r.ok()) return SSS_ERR_ALIAS;
+  }
+  a.workspace = workspace;
+  if (env_int("SSS_LOG", 0))
+    std::fprintf(stderr, "[sss] selective_scan_packed_fwd T=%lld seqs=%lld D=%lld N=%lld %s: chunks=%d of %lld ws=%zu\n",
+                 (long long)tokens, (long long)nseq, (long long)dim, (long long)dstate,
+                 io_dtype == SSS_BF16 ? "bf16" : "f32", pl.chunks, (long long)pl.K, pl.ws_total);
+  return status_of(launch_packed_scan(a, pl, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+int causal_conv1d_packed_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias, void* conv_state,
+                             const int32_t* cu_seqlens, const int32_t* state_indices, const uint8_t* has_initial,
+                             void* out, int64_t tokens, int64_t nseq, int64_t slots, int64_t dim, int64_t width,
+                             int io_dtype, int apply_silu, sss_stream_t stream) {
+  return conv_impl(x, x_stride, weight, bias, conv_state, cu_seqlens, state_indices, has_initial, out, tokens, nseq,
+                   slots, dim, width, io_dtype, apply_silu, false, stream);
+}
+
+int causal_conv1d_update(const void* x, int64_t x_stride, const float* weight, const float* bias, void* conv_state,
+                         const int32_t* state_indices, void* out, int64_t batch, int64_t slots, int64_t dim,
+                         int64_t width, int io_dtype, int apply_silu, sss_stream_t stream) {
+  return conv_impl(x, x_stride, weight, bias, conv_state, nullptr, state_indices, nullptr, out, batch, batch, slots,
+                   dim, width, io_dtype, apply_silu, true, stream);
+}
+
+size_t causal_conv1d_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype,
+                                        int device) {
+  if (!conv_bwd_dims_ok(batch, seqlen, dim, width) || !dtype_ok(io_dtype)) return 0;
+  int cus = device_cus(device);
+  if (cus <= 0) cus = 256;
+  return plan_conv_bwd(batch, seqlen, dim, width, io_dtype == SSS_BF16, cus).ws_total;
+}
+
+int causal_conv1d_bwd(const void* x, int64_t x_batch_stride, int64_t x_stride, const float* weight, const float* bias,
+                      const void* dout, void* dx, int64_t dx_batch_stride, int64_t dx_stride, float* dweight,
+                      float* dbias, int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int io_dtype,
+                      int dout_dtype, int dx_dtype, int apply_silu, void* workspace, size_t workspace_bytes,
+                      sss_stream_t stream) {
+  if (!x || !weight || !dout || !dx || !dweight || (bias && !dbias)) return SSS_ERR_NULL_ARG;
+  if (width < 1 || width > 8) return batch < 1 || seqlen < 1 || dim < 1 ? SSS_ERR_BAD_DIM : SSS_ERR_UNSUPPORTED;
+  if (!conv_bwd_dims_ok(batch, seqlen, dim, width)) return SSS_ERR_BAD_DIM;
+  // each of the gradients in fp32 or in x's type
+  if (!dtype_ok(io_dtype) || (dout_dtype != SSS_F32 && dout_dtype != io_dtype) ||
+      (dx_dtype != SSS_F32 && dx_dtype != io_dtype))
+    return SSS_ERR_UNSUPPORTED;
+  const int64_t kMaxBatchStride = (int64_t)1 << 46;
+  if (!stride_ok(x_stride, dim) || !stride_ok(dx_stride, dim) || x_batch_stride < 0 || dx_batch_stride < 0 ||
+      x_batch_stride > kMaxBatchStride || dx_batch_stride > kMaxBatchStride)
+    return SSS_ERR_BAD_DIM;
+  // batch rows may not share elements of dx
+  if (batch > 1 && dx_batch_stride < (seqlen - 1) * dx_stride + dim) return SSS_ERR_BAD_DIM;
+  const int64_t es = dtype_size(io_dtype), dos = dtype_size(dout_dtype), dxs = dtype_size(dx_dtype);
+  Regions r;
+  r.in(x, (batch - 1) * x_batch_stride * es + span(seqlen, x_stride, dim, es), es);
+  r.in(weight, dim * width * 4, 4);
+  r.in(bias, dim * 4, 4);
+  r.in(dout, batch * seqlen * dim * dos, dos);
+  r.output(dx, (batch - 1) * dx_batch_stride * dxs + span(seqlen, dx_stride, dim, dxs), dxs);
+  r.output(dweight, dim * width * 4, 4);
+  r.output(bias ? dbias : nullptr, dim * 4, 4);
+  if (workspace && !aligned16(workspace)) return SSS_ERR_UNSUPPORTED;
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  const int cus = current_device_cus();
+  if (cus <= 0) return SSS_ERR_HIP;
+  const ConvBwdPlan pl = plan_conv_bwd(batch, seqlen, dim, width, io_dtype == SSS_BF16, cus);
+  if ((double)pl.segments * (double)batch * (double)((dim + 63) / 64) > (double)((int64_t)1 << 24) * 2) return SSS_ERR_BAD_DIM;
+  if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
+  r.output(workspace, (int64_t)pl.ws_total, 16);
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  ConvBwdArgs a{};
+  a.x = x;
+  a.x_row = x_stride;
+  a.x_batch = x_batch_stride;
+  a.w = weight;
+  a.bias = bias;
+  a.dout = dout;
+  a.dx = dx;
+  a.dx_row = dx_stride;
+  a.dx_batch = dx_batch_stride;
+  a.dw = dweight;
+  a.db = bias ? dbias : nullptr;
+  a.workspace = workspace;
+  a.batch = batch;
+  a.seqlen = seqlen;
+  a.dim = dim;
+  a.width = (int)width;
+  a.bf16 = io_dtype == SSS_BF16;
+  a.dout_bf16 = dout_dtype == SSS_BF16;
+  a.dx_bf16 = dx_dtype == SSS_BF16;
+  a.silu = apply_silu != 0;
+  return status_of(launch_conv_bwd(a, pl, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t selective_scan_packed_fwd_workspace_size(int64_t tokens, int64_t dim, int64_t dstate, int device) {
+  if (scan_dims(tokens, 0, 0, dim, dstate) != SSS_OK || tokens < 1) return 0;
+  int cus = device_cus(device);
+  if (cus <= 0) cus = 256;
+  return plan_packed_scan(tokens, dim, dstate, cus).ws_total;
+}
+
+int selective_scan_packed_fwd(const void* x, int64_t x_stride, const void* delta, int64_t delta_stride, const float* A,
+                              const void* B, int64_t b_stride, const void* C, int64_t c_stride, const float* D_skip,
+                              const void* z, int64_t z_stride, const float* delta_bias, unsigned flags, float* state,
+                              const int32_t* cu_seqlens, const int32_t* state_indices, const uint8_t* has_initial,
+                              void* y, int64_t tokens, int64_t nseq, int64_t slots, int64_t dim, int64_t dstate,
+                              int io_dtype, int bc_dtype, int y_dtype, void* workspace, size_t workspace_bytes,
+                              sss_stream_t stream) {
+  return scan_impl(x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D_skip, z, z_stride, delta_bias,
+                   flags, state, cu_seqlens, state_indices, has_initial, y, tokens, nseq, slots, dim, dstate, io_dtype,
+                   bc_dtype, y_dtype, workspace, workspace_bytes, false, stream);
+}
+
+int selective_state_update_slots(const void* x, int64_t x_stride, const void* delta, int64_t delta_stride,
+                                 const float* A, const void* B, int64_t b_stride, const void* C, int64_t c_stride,
+                                 const float* D_skip, const void* z, int64_t z_stride, const float* delta_bias,
+                                 unsigned flags, float* state, const int32_t* state_indices, void* y, int64_t batch,
+                                 int64_t slots, int64_t dim, int64_t dstate, int io_dtype, int bc_dtype, int y_dtype,
+                                 sss_stream_t stream) {
+  return scan_impl(x, x_stride, delta, delta_stride, A, B, b_stride, C, c_stride, D_skip, z, z_stride, delta_bias,
+                   flags, state, nullptr, state_indices, nullptr, y, batch, batch, slots, dim, dstate, io_dtype,
+                   bc_dtype, y_dtype, nullptr, 0, true, stream);
+}
+
+}  // extern "C"

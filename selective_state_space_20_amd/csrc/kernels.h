@@ -6,6 +6,10 @@
 
 namespace sss {
 
+// Compute units of `device` / of the current device, cached (api.cpp); -1 if it cannot be queried.
+int device_cus(int device);
+int current_device_cus();
+
 // Launch plan of the selective scan (chosen on the host, see selective_scan.hip).
 struct SelPlan {
   int segments;      // time segments S (S > 1: segment states, carry, then outputs)
@@ -154,6 +158,84 @@ struct ConvArgs {
 
 ConvPlan plan_conv1d(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, int num_cus);
 hipError_t launch_conv1d(const ConvArgs& a, const ConvPlan& plan, hipStream_t stream);
+
+// Causal convolution over packed prompts, or one token per row (step), with the inputs before
+// them in cache slots (packed_conv.hip).
+struct PackedConvArgs {
+  const void* x;
+  int64_t x_stride;  // elements between tokens
+  const float* w;
+  const float* bias;
+  void* state;           // (slots, width-1, dim), nullable for prompts
+  const int32_t* cu;     // nseq + 1 boundaries (prompts)
+  const int32_t* sidx;   // nullable: slot of each sequence or row
+  const uint8_t* init;   // nullable (prompts): sequences that continue their slot
+  void* out;
+  int64_t tokens, nseq, slots, dim;
+  int width, bf16, silu, step;
+};
+
+hipError_t launch_packed_conv(const PackedConvArgs& a, int num_cus, hipStream_t stream);
+
+// Gradients of the causal convolution (conv_bwd.hip).
+struct ConvBwdPlan {
+  int segments;
+  int64_t seg_len;
+  int cpl;  // channels per lane
+  size_t ws_total;
+};
+
+struct ConvBwdArgs {
+  const void* x;
+  int64_t x_row, x_batch;  // strides in elements
+  const float* w;
+  const float* bias;
+  const void* dout;
+  void* dx;
+  int64_t dx_row, dx_batch;
+  float* dw;
+  float* db;
+  void* workspace;
+  int64_t batch, seqlen, dim;
+  int width, bf16, dout_bf16, dx_bf16, silu;
+};
+
+ConvBwdPlan plan_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, bool bf16, int num_cus);
+hipError_t launch_conv_bwd(const ConvBwdArgs& a, const ConvBwdPlan& plan, hipStream_t stream);
+
+// Selective scan over packed prompts (packed_scan.hip) and the decode step on cache slots
+// (slot_update.hip; tokens = rows, no boundaries).
+struct PackedScanPlan {
+  int64_t K;   // tokens per chunk
+  int chunks;
+  size_t off_end, off_init, off_enter, off_sum, off_flag, ws_total;
+};
+
+struct PackedScanArgs {
+  const void* x;
+  const void* delta;
+  const float* A;
+  const void* B;
+  const void* C;
+  const float* Dsk;
+  const void* z;
+  const float* delta_bias;
+  float* state;
+  const int32_t* cu;
+  const int32_t* sidx;
+  const uint8_t* init;
+  void* y;
+  int64_t sx, sd, sz, sb, sc;  // elements between tokens
+  int64_t tokens, nseq, slots, dim;
+  int dstate, bf16, bc_bf16, y_bf16, softplus;
+  void* workspace;
+};
+
+PackedScanPlan plan_packed_scan(int64_t tokens, int64_t dim, int64_t dstate, int num_cus);
+hipError_t launch_packed_scan(const PackedScanArgs& a, const PackedScanPlan& plan, hipStream_t stream);
+hipError_t launch_pscan_carry(const float* A, const float* ends, const float* sums, const int32_t* flags, float* enter,
+                              int dstate, int dim, int chunks, hipStream_t stream);
+hipError_t launch_slot_update(const PackedScanArgs& a, hipStream_t stream);
 
 int env_int(const char* name, int dflt);
 

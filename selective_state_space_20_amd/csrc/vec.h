@@ -1,0 +1,137 @@
+// vec.h -- V adjacent elements of one lane, bf16 or fp32, moved as one wide access, and the
+// search of a packed batch's sequence boundaries (HIP, gfx950).
+#pragma once
+#include "common.h"
+
+namespace sss {
+
+// Wide accesses at element alignment: rows of an odd length, or halves of a projection's rows,
+// start at any element.  gfx950 runs with unaligned global accesses enabled (the compiler
+// emits one wide load or store for these types), so that no narrower path is needed.
+typedef uint32_t vec_u1 __attribute__((aligned(2)));
+typedef uint32_t vec_u2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t vec_u4 __attribute__((ext_vector_type(4), aligned(2)));
+
+typedef __bf16 vec_bf2 __attribute__((ext_vector_type(2)));
+typedef float vec_f2 __attribute__((ext_vector_type(2)));
+
+// two fp32 -> two bf16 in one dword (low half = a), rounded to nearest even (v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint32_t vec_bf16_pair(float a, float b) {
+  const vec_f2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, vec_bf2));
+}
+
+template <bool BF16, int V>
+struct Vec {
+  static constexpr int ES = BF16 ? 2 : 4;       // bytes per element
+  static constexpr int VB = V * ES;             // bytes per lane
+  static constexpr int ND = VB >= 4 ? VB / 4 : 1;
+  uint32_t w[ND];  // raw bits: widened only when read, so that loads stay in flight
+
+  // NT: streamed data that nothing reads again soon
+  template <bool NT = false>
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (VB == 2) {
+      w[0] = NT ? __builtin_nontemporal_load((const uint16_t*)p) : *(const uint16_t*)p;
+    } else if constexpr (VB == 4) {
+      w[0] = NT ? __builtin_nontemporal_load((const vec_u1*)p) : *(const vec_u1*)p;
+    } else if constexpr (VB == 8) {
+      const vec_u2 v = NT ? __builtin_nontemporal_load((const vec_u2*)p) : *(const vec_u2*)p;
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+      static_assert(VB % 16 == 0 || VB < 16, "vector bytes");
+#pragma unroll
+      for (int i = 0; i < VB / 16; ++i) {
+        const vec_u4 v = NT ? __builtin_nontemporal_load((const vec_u4*)p + i) : *((const vec_u4*)p + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < ND; ++i) w[i] = 0u;
+  }
+  // element c widened to fp32
+  __device__ __forceinline__ float get(int c) const {
+    if constexpr (BF16) {
+      const uint32_t d = w[c >> 1];
+      return __builtin_bit_cast(float, (c & 1) ? (d & 0xFFFF0000u) : (d << 16));
+    } else {
+      return __builtin_bit_cast(float, w[c]);
+    }
+  }
+  // from fp32, rounded once to nearest even in bf16
+  __device__ __forceinline__ void set(const float (&v)[V]) {
+    if constexpr (BF16) {
+      if constexpr (V == 1) {
+        w[0] = vec_bf16_pair(v[0], 0.0f) & 0xFFFFu;
+      } else {
+#pragma unroll
+        for (int c = 0; c < V; c += 2) w[c >> 1] = vec_bf16_pair(v[c], v[c + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) w[c] = __builtin_bit_cast(uint32_t, v[c]);
+    }
+  }
+  template <bool NT = false>
+  __device__ __forceinline__ void store(void* p) const {
+    if constexpr (VB == 2) {
+      if constexpr (NT) __builtin_nontemporal_store((uint16_t)w[0], (uint16_t*)p);
+      else *(uint16_t*)p = (uint16_t)w[0];
+    } else if constexpr (VB == 4) {
+      if constexpr (NT) __builtin_nontemporal_store(w[0], (vec_u1*)p);
+      else *(vec_u1*)p = w[0];
+    } else if constexpr (VB == 8) {
+      const vec_u2 v = {w[0], w[1]};
+      if constexpr (NT) __builtin_nontemporal_store(v, (vec_u2*)p);
+      else *(vec_u2*)p = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VB / 16; ++i) {
+        const vec_u4 v = {w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+        if constexpr (NT) __builtin_nontemporal_store(v, (vec_u4*)p + i);
+        else *((vec_u4*)p + i) = v;
+      }
+    }
+  }
+  // elements skip..V-1 only (skip 0: one wide store; skip V: nothing)
+  template <bool NT = false>
+  __device__ __forceinline__ void store_from(void* p, int skip) const {
+    if (skip == 0) {
+      store<NT>(p);
+    } else {
+#pragma unroll
+      for (int c = 1; c < V; ++c) {
+        if (c < skip) continue;
+        if constexpr (BF16) ((uint16_t*)p)[c] = (uint16_t)((c & 1) ? w[c >> 1] >> 16 : w[c >> 1]);
+        else ((uint32_t*)p)[c] = w[c];
+      }
+    }
+  }
+};
+
+// Packed sequences: the sequence that token t belongs to, i.e. the last s with cu[s] <= t
+// among cu[0..nseq] (-1: before the first).  The whole wave searches: 64 boundaries per load,
+// so that 64 sequences take one load and 4096 two.  Any contents of cu give a number in
+// [-1, nseq].
+__device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int nseq, int t, int lane) {
+  int lo = 0, cnt = nseq + 1;
+  while (cnt > 64) {
+    const int step = (cnt + 63) >> 6;
+    const int i = lane * step;
+    const bool le = i < cnt && cu[lo + i] <= t;
+    const int k = __builtin_popcountll(__builtin_amdgcn_ballot_w64(le));
+    if (k == 0) return lo - 1;
+    lo += (k - 1) * step;
+    cnt = min(step, cnt - (k - 1) * step);
+  }
+  const bool le = lane < cnt && cu[lo + lane] <= t;
+  return lo - 1 + __builtin_popcountll(__builtin_amdgcn_ballot_w64(le));
+}
+
+}  // namespace sss

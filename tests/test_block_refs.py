@@ -1,0 +1,76 @@
+"""The plain references of the operators around the scan against things other than themselves:
+library convolutions, hand-worked values and central differences (CPU only)."""
+import numpy as np
+import pytest
+
+from . import block_ref as ref
+
+
+def test_packed_conv_is_numpy_convolve_per_sequence():
+    rng = np.random.default_rng(1)
+    x, w = rng.standard_normal((11, 3)), rng.standard_normal((3, 4))
+    cu = [0, 4, 4, 11]
+    out, _, _ = ref.packed_conv(x, w, None, cu, None, None, None, False)
+    for lo, hi in ((0, 4), (4, 11)):
+        for d in range(3):
+            full = np.convolve(x[lo:hi, d], w[d, ::-1])[:hi - lo]
+            np.testing.assert_allclose(out[lo:hi, d], full, rtol=1e-12, atol=1e-12)
+
+
+def test_packed_conv_split_anywhere_continues_from_its_state():
+    rng = np.random.default_rng(2)
+    x, w, b = rng.standard_normal((9, 2)), rng.standard_normal((2, 4)), rng.standard_normal(2)
+    whole, _, _ = ref.packed_conv(x, w, b, [0, 9], np.zeros((1, 3, 2)), None, [0], True)
+    for cut in range(10):
+        st = np.zeros((1, 3, 2))
+        first, st1, _ = ref.packed_conv(x[:cut], w, b, [0, cut], st, None, [0], True)
+        second, _, _ = ref.packed_conv(x[cut:], w, b, [0, 9 - cut], st1 if cut else st, None, [cut > 0], True)
+        np.testing.assert_allclose(np.concatenate([first, second]), whole, rtol=1e-12)
+
+
+@pytest.mark.parametrize("act", [False, True])
+@pytest.mark.parametrize("shape", [(2, 5, 3, 4), (1, 2, 2, 4), (1, 1, 1, 1), (2, 7, 1, 2)])
+def test_conv_gradient_formulas_against_differences(shape, act):
+    bt, length, d, width = shape
+    rng = np.random.default_rng(3)
+    x, w, b = rng.standard_normal((bt, length, d)), rng.standard_normal((d, width)), rng.standard_normal(d)
+    dout = rng.standard_normal((bt, length, d))
+    grads, _ = ref.conv_backward(x, w, b, dout, act)
+    loss = lambda: float((dout * ref.conv_forward(x, w, b, act)).sum())
+    eps = 1e-5  # central differences of a smooth function: error about eps^2 |f'''| / 6
+    for arr, g in zip((x, w, b), grads):
+        for i in np.ndindex(arr.shape):
+            keep = arr[i]
+            arr[i] = keep + eps
+            up = loss()
+            arr[i] = keep - eps
+            down = loss()
+            arr[i] = keep
+            assert abs((up - down) / (2 * eps) - g[i]) <= 1e-7 * (1 + abs(g[i]))
+
+
+def test_packed_scan_hand_worked():
+    """One channel, one state, A = 0: the state is a running sum of step * B * x."""
+    x = np.array([[1.0], [2.0], [3.0], [5.0]])
+    delta = np.array([[1.0], [0.5], [2.0], [1.0]])
+    B, C = np.array([[2.0], [4.0], [1.0], [1.0]]), np.array([[1.0], [1.0], [3.0], [2.0]])
+    y, st = ref.packed_scan(x, delta, np.zeros((1, 1)), B, C, None, None, [0, 2, 4], np.array([[[10.0]], [[7.0]]]),
+                            None, [False, True], None, False)
+    np.testing.assert_array_equal(y[:, 0], [2.0, 6.0, 39.0, 36.0])
+    np.testing.assert_array_equal(st[:, 0, 0], [6.0, 18.0])
+
+
+def test_packed_scan_agrees_with_the_oracle(oracle_lib):
+    """Each packed sequence is a dense scan of its own."""
+    rng = np.random.default_rng(4)
+    f = lambda *s: rng.standard_normal(s).astype(np.float32)
+    t, d, n, cu = 12, 3, 4, [0, 5, 5, 12]
+    x, delta, z, A, B, C, D = f(t, d), np.abs(f(t, d)) * 0.3, f(t, d), -np.abs(f(d, n)), f(t, n), f(t, n), f(d)
+    state = f(3, d, n)
+    y, st = ref.packed_scan(x, delta, A, B, C, D, z, cu, state, [2, 1, 0], [True, True, False], None, False)
+    for s, h0, slot in ((0, state[2:3], 2), (2, None, 0)):
+        r = slice(cu[s], cu[s + 1])
+        yo, ho = oracle_lib.selective_scan(x[None, r], delta[None, r], A, B[None, r], C[None, r], D, z[None, r], h0)
+        np.testing.assert_allclose(y[r], np.asarray(yo)[0], rtol=1e-12, atol=1e-12)
+        np.testing.assert_allclose(st[slot], np.asarray(ho)[0], rtol=1e-12, atol=1e-12)
+    np.testing.assert_array_equal(st[1], state[1].astype(np.float64))
