@@ -32,6 +32,10 @@
  *      causal_conv1d_update, selective_state_update_slots -- their single-token steps on those
  *      slots; causal_conv1d_bwd -- the convolution's gradients.
  *
+ *  rms_norm_gated_fwd / _bwd, rms_norm_residual_fwd / _bwd -- the norms around the block: after
+ *      the scan, fused with the gate, and between blocks, fused with the residual addition, a
+ *      norm of the block's output and its scale.
+ *
  *  elementwise_scan -- the per-channel form of "15. Selective (Data-Dependent) SSM
  *      Scan" (Reference solution): h = A_t*h + B_t*x_t, y_t = C_t*h.
  *
@@ -330,6 +334,61 @@ int selective_state_update_slots(const void* x, int64_t x_stride, const void* de
                                  unsigned flags, float* state, const int32_t* state_indices, void* y, int64_t batch,
                                  int64_t slots, int64_t dim, int64_t dstate, int io_dtype, int bc_dtype, int y_dtype,
                                  sss_stream_t stream);
+
+/* Option of the gated norm. */
+#define SSS_NORM_BEFORE_GATE 1u /* the norm is applied to x and its result gated, instead of the
+                                   gated x being normed */
+
+/* Norm after the scan, fused with the block's gate; over groups of `group` adjacent channels (a
+ * divisor of dim, at most 32768: SSS_ERR_UNSUPPORTED otherwise), with
+ * rstd(v) = (mean(v^2) + eps)^-1/2:
+ *   out = u rstd(u) weight,  u = x silu(z);  with SSS_NORM_BEFORE_GATE  out = x rstd(x) weight silu(z).
+ * x (rows, dim) in x_dtype, z (rows, dim) and out (rows, dim, contiguous) in out_dtype; weight
+ * (dim) float32; z nullable (no gate); rstd (rows, dim / group) float32, nullable output that
+ * the gradients call takes.  Required: x, weight, out.  rows may be 0. */
+int rms_norm_gated_fwd(const void* x, int64_t x_stride, const float* weight, const void* z, int64_t z_stride, void* out,
+                       float* rstd, int64_t rows, int64_t dim, int64_t group, float eps, unsigned flags, int x_dtype,
+                       int out_dtype, sss_stream_t stream);
+
+/* Bytes of workspace rms_norm_gated_bwd needs on `device` (0 on invalid sizes). */
+size_t rms_norm_gated_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, int device);
+
+/* Its gradients for L = sum(dout * out): dx (rows, dim) in x_dtype, dz (rows, dim) with
+ * dz_stride in out_dtype (with z), dweight (dim) float32; dout (rows, dim) in out_dtype; rstd
+ * as the forward call left it.  dx and dout are contiguous.  dweight is summed over the rows
+ * in a fixed order; with no rows it is zero. */
+int rms_norm_gated_bwd(const void* dout, const void* x, int64_t x_stride, const float* weight, const void* z,
+                       int64_t z_stride, const float* rstd, void* dx, void* dz, int64_t dz_stride, float* dweight,
+                       int64_t rows, int64_t dim, int64_t group, unsigned flags, int x_dtype, int out_dtype,
+                       void* workspace, size_t workspace_bytes, sss_stream_t stream);
+
+/* Between two blocks: the block's output x, normed (with post_weight) and scaled, joins the
+ * residual stream, whose norm is the next block's input:
+ *   v = x rstd(x) post_weight  (or x),  residual_out = residual + alpha * scale * v,
+ *   out = residual_out rstd(residual_out) weight.
+ * x (rows, dim) and out in io_dtype, residual and residual_out in residual_dtype; post_weight,
+ * scale, weight (dim) float32; residual (zero), post_weight and scale (one) nullable.  out is
+ * of the sum before it is rounded to residual_dtype.  residual_out may be residual itself
+ * (contiguous), no other overlap.  rstd_post, rstd (rows) float32: nullable outputs for the
+ * gradients call.  dim at most 32768 (SSS_ERR_UNSUPPORTED).  Required: x, weight, out, residual_out. */
+int rms_norm_residual_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                          const float* post_weight, const float* scale, const float* weight, void* out,
+                          void* residual_out, float* rstd_post, float* rstd, int64_t rows, int64_t dim, float alpha,
+                          float eps, int io_dtype, int residual_dtype, sss_stream_t stream);
+
+/* Bytes of workspace rms_norm_residual_bwd needs on `device` (0 on invalid sizes). */
+size_t rms_norm_residual_bwd_workspace_size(int64_t rows, int64_t dim, int device);
+
+/* Its gradients for L = sum(dout * out) + sum(dresidual_out * residual_out) (dresidual_out
+ * nullable: zero): dx (io_dtype), dresidual (residual_dtype, nullable), dweight, and
+ * dpost_weight / dscale (with post_weight / scale), float32.  residual_out, rstd_post, rstd as
+ * the forward call left them; x is needed with post_weight or scale only.  All contiguous but
+ * x.  Parameter gradients are summed over the rows in a fixed order; with no rows they are zero. */
+int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const void* x, int64_t x_stride,
+                          const void* residual_out, const float* post_weight, const float* scale, const float* weight,
+                          const float* rstd_post, const float* rstd, void* dx, void* dresidual, float* dweight,
+                          float* dpost_weight, float* dscale, int64_t rows, int64_t dim, float alpha, int io_dtype,
+                          int residual_dtype, void* workspace, size_t workspace_bytes, sss_stream_t stream);
 
 /* Bytes of workspace elementwise_scan needs for these sizes on `device`. */
 size_t elementwise_scan_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int device);

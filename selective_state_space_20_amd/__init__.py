@@ -17,12 +17,16 @@ include/sss.h); this package is its thin Python binding:
     cache slot; ``causal_conv1d_update`` / ``selective_state_update_slots``: one token of each
     request on the same caches
   * ``causal_conv1d_bwd(x, weight, bias, dout=..., silu=False)`` -> the convolution's gradients
+  * ``rms_norm_gated_fwd`` / ``rms_norm_gated_bwd``: the norm after the scan, fused with the gate;
+    ``rms_norm_residual_fwd`` / ``rms_norm_residual_bwd``: the residual addition between blocks,
+    fused with a norm of the block's output, its scale and the next block's norm
   * ``elementwise_scan(x, A, B, C, h0=None)`` -> (y, h_last)
   * ``*_workspace_size``, raw-pointer variants ``*_raw`` and ``status_string``.
 
 ``inputs`` holds the seeded synthetic workload generators.
 """
 from ._lib import (EXPORTED, LIB_PATH, SSSError, SSS_BF16, SSS_DELTA_SOFTPLUS, SSS_EXACT_ZOH, SSS_F32, SSS_LAYOUT_BDL,
+                   SSS_NORM_BEFORE_GATE,
                    causal_conv1d_fwd, causal_conv1d_fwd_raw, elementwise_scan, elementwise_scan_raw,
                    selective_scan_bwd, selective_scan_bwd_raw, selective_scan_bwd_ex_raw, selective_scan_bwd_workspace_size,
                    selective_scan_fwd_ex_raw, selective_scan_fwd_noalloc_raw, selective_scan_states_size,
@@ -32,11 +36,15 @@ from ._lib import (EXPORTED, LIB_PATH, SSSError, SSS_BF16, SSS_DELTA_SOFTPLUS, S
                    selective_state_update, selective_state_update_raw,
                    status_string)
 from ._block import (causal_conv1d_bwd, causal_conv1d_bwd_workspace_size, causal_conv1d_packed_fwd,
-                     causal_conv1d_update, selective_scan_packed_fwd, selective_scan_packed_fwd_workspace_size,
+                     causal_conv1d_update, rms_norm_gated_bwd, rms_norm_gated_bwd_workspace_size, rms_norm_gated_fwd,
+                     rms_norm_residual_bwd, rms_norm_residual_bwd_workspace_size, rms_norm_residual_fwd,
+                     selective_scan_packed_fwd, selective_scan_packed_fwd_workspace_size,
                      selective_state_update_slots)
 
 __all__ = ["causal_conv1d_packed_fwd", "causal_conv1d_update", "causal_conv1d_bwd", "causal_conv1d_bwd_workspace_size",
            "selective_scan_packed_fwd", "selective_scan_packed_fwd_workspace_size", "selective_state_update_slots",
+           "rms_norm_gated_fwd", "rms_norm_gated_bwd", "rms_norm_gated_bwd_workspace_size", "rms_norm_residual_fwd",
+           "rms_norm_residual_bwd", "rms_norm_residual_bwd_workspace_size", "SSS_NORM_BEFORE_GATE",
            "selective_scan_fwd", "selective_scan_bwd", "selective_scan_bwd_raw", "selective_scan_bwd_ex_raw", "selective_scan_bwd_workspace_size",
            "selective_state_update", "causal_conv1d_fwd", "causal_conv1d_fwd_raw", "selective_state_update_raw", "elementwise_scan",
            "selective_scan_fwd_workspace_size",

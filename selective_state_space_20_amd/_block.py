@@ -1,5 +1,6 @@
 """Binding of the operators around the scan: the convolution and the scan over packed prompts
-and their single-token steps on cache slots, and the convolution's gradients.
+and their single-token steps on cache slots, the convolution's gradients, and the norms around
+the block.
 
 As in ``_lib``, only argument checks, output allocation and the C call: every step of the
 computation runs in the library's HIP kernels.
@@ -7,7 +8,7 @@ computation runs in the library's HIP kernels.
 from __future__ import annotations
 
 from . import _lib
-from ._lib import SSS_BF16, SSS_DELTA_SOFTPLUS, SSS_F32, SSSError, load
+from ._lib import SSS_BF16, SSS_DELTA_SOFTPLUS, SSS_F32, SSS_NORM_BEFORE_GATE, SSSError, load
 
 
 def _rows(t, name, dtype, rows, dim, device):
@@ -287,3 +288,169 @@ def selective_state_update_slots(x, delta, A, B, C, D=None, z=None, *, state, st
     if rc != 0:
         raise SSSError(rc, "selective_state_update_slots")
     return y
+
+
+def _group(dim, group_size):
+    g = dim if group_size is None else int(group_size)
+    if g < 1 or dim % g != 0:
+        raise ValueError(f"group_size must divide {dim}, got {group_size}")
+    return g
+
+
+def rms_norm_gated_fwd(x, weight, z=None, *, eps=1e-5, group_size=None, norm_before_gate=False, out=None,
+                       return_rstd=False, stream=None):
+    """Norm after the scan, fused with the gate: rmsnorm(x * silu(z)) * weight, or
+    rmsnorm(x) * weight * silu(z) with norm_before_gate; over groups of group_size channels.
+
+    x (rows, dim) float32 or bfloat16 (the scan's output), z (rows, dim) float32 or bfloat16, rows
+    may be strided; weight (dim) float32.  Returns out (rows, dim) in z's dtype (x's without z),
+    and with return_rstd the (rows, groups) float32 factors that rms_norm_gated_bwd takes."""
+    import torch
+    dev = x.device
+    rows, dim = _two_d(x, "x")
+    xc = _code(x.dtype, "x")
+    g = _group(dim, group_size)
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
+    od = z.dtype if z is not None else x.dtype
+    oc = _code(od, "z")
+    zp, zs = _rows(z, "z", od, rows, dim, dev) if z is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
+    o = out if out is not None else torch.empty((rows, dim), dtype=od, device=dev)
+    op = _dense(o, "out", od, (rows, dim), dev)
+    rstd = torch.empty((rows, dim // g), dtype=torch.float32, device=dev) if return_rstd else None
+    if rows > 0:
+        rc = load().rms_norm_gated_fwd(xp, xs, wp, zp, zs, op, rstd.data_ptr() if return_rstd else 0, rows, dim, g,
+                                       float(eps), SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc,
+                                       _stream(stream, dev))
+        if rc != 0:
+            raise SSSError(rc, "rms_norm_gated_fwd")
+    return (o, rstd) if return_rstd else o
+
+
+def rms_norm_gated_bwd_workspace_size(rows, dim, group_size=None, device=0) -> int:
+    return int(load().rms_norm_gated_bwd_workspace_size(rows, dim, _group(dim, group_size), device))
+
+
+def rms_norm_gated_bwd(dout, x, weight, z=None, *, rstd, group_size=None, norm_before_gate=False, dz=None,
+                       workspace=None, stream=None):
+    """Gradients of sum(dout * rms_norm_gated_fwd(...)): a dict of dx (x's dtype), dz (z's dtype,
+    with z; into the given ``dz``, strided or not) and dweight float32.  dout (rows, dim) in the
+    forward output's dtype, contiguous; rstd as the forward returned it."""
+    import torch
+    dev = x.device
+    rows, dim = _two_d(x, "x")
+    xc = _code(x.dtype, "x")
+    g = _group(dim, group_size)
+    od = z.dtype if z is not None else x.dtype
+    oc = _code(od, "z")
+    dp = _dense(dout, "dout", od, (rows, dim), dev)
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
+    zp, zs = _rows(z, "z", od, rows, dim, dev) if z is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
+    rp = _dense(rstd, "rstd", torch.float32, (rows, dim // g), dev)
+    res = {"dx": torch.empty((rows, dim), dtype=x.dtype, device=dev),
+           "dweight": torch.empty((dim,), dtype=torch.float32, device=dev)}
+    gp, gs = 0, 0
+    if z is not None:
+        res["dz"] = dz if dz is not None else torch.empty((rows, dim), dtype=od, device=dev)
+        gp, gs = _rows(res["dz"], "dz", od, rows, dim, dev)
+    if workspace is None:
+        workspace = torch.empty(rms_norm_gated_bwd_workspace_size(rows, dim, g, dev.index or 0), dtype=torch.uint8,
+                                device=dev)
+    wsp, wsn = _lib._workspace(workspace, dev)
+    rc = load().rms_norm_gated_bwd(dp, xp, xs, wp, zp, zs, rp, res["dx"].data_ptr(), gp, gs, res["dweight"].data_ptr(),
+                                   rows, dim, g, SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc, wsp, wsn,
+                                   _stream(stream, dev))
+    if rc != 0:
+        raise SSSError(rc, "rms_norm_gated_bwd")
+    return res
+
+
+def rms_norm_residual_fwd(x, weight, residual=None, *, post_weight=None, scale=None, alpha=1.0, eps=1e-5, out=None,
+                          residual_out=None, return_rstd=False, stream=None):
+    """Between two blocks: residual_out = residual + alpha * scale * v with v = x, or
+    rmsnorm(x) * post_weight, and out = rmsnorm(residual_out) * weight.
+
+    x (rows, dim) float32 or bfloat16, residual (rows, dim) float32 or bfloat16, rows may be
+    strided; weight, post_weight, scale (dim) float32.  Returns (out in x's dtype, residual_out in
+    the residual's dtype, float32 without one), and with return_rstd also the (rows,) float32
+    factors rstd and rstd_post (None without post_weight).  residual_out may be the residual."""
+    import torch
+    dev = x.device
+    rows, dim = _two_d(x, "x")
+    xc = _code(x.dtype, "x")
+    hd = (residual.dtype if residual is not None else residual_out.dtype if residual_out is not None
+          else torch.float32)
+    hc = _code(hd, "residual")
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
+    hp, hs = _rows(residual, "residual", hd, rows, dim, dev) if residual is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
+    pp = _dense(post_weight, "post_weight", torch.float32, (dim,), dev)
+    sp = _dense(scale, "scale", torch.float32, (dim,), dev)
+    o = out if out is not None else torch.empty((rows, dim), dtype=x.dtype, device=dev)
+    op = _dense(o, "out", x.dtype, (rows, dim), dev)
+    h = residual_out if residual_out is not None else torch.empty((rows, dim), dtype=hd, device=dev)
+    ho = _dense(h, "residual_out", hd, (rows, dim), dev)
+    rstd = rstd_post = None
+    if return_rstd:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd_post = torch.empty((rows,), dtype=torch.float32, device=dev) if post_weight is not None else None
+    if rows > 0:
+        rc = load().rms_norm_residual_fwd(xp, xs, hp, hs, pp, sp, wp, op, ho,
+                                          0 if rstd_post is None else rstd_post.data_ptr(),
+                                          0 if rstd is None else rstd.data_ptr(), rows, dim, float(alpha), float(eps),
+                                          xc, hc, _stream(stream, dev))
+        if rc != 0:
+            raise SSSError(rc, "rms_norm_residual_fwd")
+    return (o, h, rstd, rstd_post) if return_rstd else (o, h)
+
+
+def rms_norm_residual_bwd_workspace_size(rows, dim, device=0) -> int:
+    return int(load().rms_norm_residual_bwd_workspace_size(rows, dim, device))
+
+
+def rms_norm_residual_bwd(dout, dresidual_out=None, *, residual_out, weight, rstd, x=None, post_weight=None, scale=None,
+                          rstd_post=None, alpha=1.0, want_dresidual=True, workspace=None, stream=None):
+    """Gradients of sum(dout * out) + sum(dresidual_out * residual_out) of rms_norm_residual_fwd.
+
+    dout (rows, dim) in x's dtype and dresidual_out (or None) and residual_out in the residual's,
+    contiguous; rstd, rstd_post as the forward returned them; x is needed with post_weight or
+    scale.  Returns a dict of dx (x's dtype), dresidual (the residual's, unless not wanted),
+    dweight, and dpost_weight / dscale with post_weight / scale, float32."""
+    import torch
+    dev = dout.device
+    rows, dim = _two_d(dout, "dout")
+    xd, hd = dout.dtype, residual_out.dtype
+    xc, hc = _code(xd, "dout"), _code(hd, "residual_out")
+    if x is None and (post_weight is not None or scale is not None):
+        raise ValueError("x is needed for the gradients through post_weight or scale")
+    if post_weight is not None and rstd_post is None:
+        raise ValueError("rstd_post is needed with post_weight")
+    dp = _dense(dout, "dout", xd, (rows, dim), dev)
+    ep = _dense(dresidual_out, "dresidual_out", hd, (rows, dim), dev)
+    hp = _dense(residual_out, "residual_out", hd, (rows, dim), dev)
+    xp, xs = _rows(x, "x", xd, rows, dim, dev) if x is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
+    pp = _dense(post_weight, "post_weight", torch.float32, (dim,), dev)
+    sp = _dense(scale, "scale", torch.float32, (dim,), dev)
+    rp = _dense(rstd, "rstd", torch.float32, (rows,), dev)
+    rpp = _dense(rstd_post, "rstd_post", torch.float32, (rows,), dev) if post_weight is not None else 0
+    vec = lambda: torch.empty((dim,), dtype=torch.float32, device=dev)
+    res = {"dx": torch.empty((rows, dim), dtype=xd, device=dev), "dweight": vec()}
+    if want_dresidual:
+        res["dresidual"] = torch.empty((rows, dim), dtype=hd, device=dev)
+    if post_weight is not None:
+        res["dpost_weight"] = vec()
+    if scale is not None:
+        res["dscale"] = vec()
+    ptr = lambda k: res[k].data_ptr() if k in res else 0
+    if workspace is None:
+        workspace = torch.empty(rms_norm_residual_bwd_workspace_size(rows, dim, dev.index or 0), dtype=torch.uint8,
+                                device=dev)
+    wsp, wsn = _lib._workspace(workspace, dev)
+    rc = load().rms_norm_residual_bwd(dp, ep, xp, xs, hp, pp, sp, wp, rpp, rp, ptr("dx"), ptr("dresidual"),
+                                      ptr("dweight"), ptr("dpost_weight"), ptr("dscale"), rows, dim, float(alpha), xc,
+                                      hc, wsp, wsn, _stream(stream, dev))
+    if rc != 0:
+        raise SSSError(rc, "rms_norm_residual_bwd")
+    return res

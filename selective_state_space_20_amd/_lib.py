@@ -18,6 +18,7 @@ STATUS = {0: "SSS_OK", -1: "SSS_ERR_NULL_ARG", -2: "SSS_ERR_BAD_DIM", -3: "SSS_E
           -4: "SSS_ERR_WORKSPACE", -5: "SSS_ERR_ALIAS", -6: "SSS_ERR_HIP"}
 
 SSS_EXACT_ZOH, SSS_DELTA_SOFTPLUS, SSS_LAYOUT_BDL = 1, 2, 4
+SSS_NORM_BEFORE_GATE = 1
 
 EXPORTED = ("selective_scan_fwd", "selective_scan_fwd_ex", "selective_scan_fwd_workspace_size",
             "selective_scan_fwd_ex_workspace_size", "selective_state_update",
@@ -27,7 +28,9 @@ EXPORTED = ("selective_scan_fwd", "selective_scan_fwd_ex", "selective_scan_fwd_w
             "selective_scan_bwd_saved", "selective_scan_bwd_ex",
             "causal_conv1d_packed_fwd", "causal_conv1d_update", "causal_conv1d_bwd",
             "causal_conv1d_bwd_workspace_size", "selective_scan_packed_fwd",
-            "selective_scan_packed_fwd_workspace_size", "selective_state_update_slots")
+            "selective_scan_packed_fwd_workspace_size", "selective_state_update_slots",
+            "rms_norm_gated_fwd", "rms_norm_gated_bwd", "rms_norm_gated_bwd_workspace_size", "rms_norm_residual_fwd",
+            "rms_norm_residual_bwd", "rms_norm_residual_bwd_workspace_size")
 
 
 class SSSError(RuntimeError):
@@ -99,6 +102,21 @@ def load() -> ctypes.CDLL:
         lib.selective_scan_packed_fwd_workspace_size.restype = sz
         lib.selective_state_update_slots.argtypes = scan + [vp] * 2 + [i64] * 4 + [i32] * 3 + [vp]
         lib.selective_state_update_slots.restype = i32
+        f32 = ctypes.c_float
+        lib.rms_norm_gated_fwd.argtypes = [vp, i64, vp, vp, i64, vp, vp] + [i64] * 3 + [f32, u32, i32, i32, vp]
+        lib.rms_norm_gated_fwd.restype = i32
+        lib.rms_norm_gated_bwd.argtypes = ([vp, vp, i64, vp, vp, i64] + [vp] * 3 + [i64, vp] + [i64] * 3
+                                           + [u32, i32, i32, vp, sz, vp])
+        lib.rms_norm_gated_bwd.restype = i32
+        lib.rms_norm_gated_bwd_workspace_size.argtypes = [i64] * 3 + [i32]
+        lib.rms_norm_gated_bwd_workspace_size.restype = sz
+        lib.rms_norm_residual_fwd.argtypes = ([vp, i64, vp, i64] + [vp] * 7 + [i64] * 2
+                                              + [f32, f32, i32, i32, vp])
+        lib.rms_norm_residual_fwd.restype = i32
+        lib.rms_norm_residual_bwd.argtypes = [vp] * 3 + [i64] + [vp] * 11 + [i64] * 2 + [f32, i32, i32, vp, sz, vp]
+        lib.rms_norm_residual_bwd.restype = i32
+        lib.rms_norm_residual_bwd_workspace_size.argtypes = [i64] * 2 + [i32]
+        lib.rms_norm_residual_bwd_workspace_size.restype = sz
         lib.sss_status_string.argtypes = [i32]
         lib.sss_status_string.restype = ctypes.c_char_p
         _lib = lib

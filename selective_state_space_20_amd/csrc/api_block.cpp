@@ -1,5 +1,6 @@
 // api_block.cpp -- the C ABI of the operators around the scan (declared in include/sss.h): the
-// packed convolution, scan and their token steps, and the convolution's gradients.
+// packed convolution, scan and their token steps, the convolution's gradients, and the norms
+// around the block.
 #include "sss.h"
 
 #include <hip/hip_runtime.h>
@@ -174,9 +175,231 @@ int scan_impl(const void* x, int64_t x_stride, const void* delta, int64_t delta_
   return status_of(launch_packed_scan(a, pl, s));
 }
 
+// rows of a norm: at most one workgroup of 256 to 1024 threads per row and group, 2^31 threads
+int norm_dims(int64_t rows, int64_t dim, int64_t group) {
+  if (rows < 0 || dim < 1 || group < 1 || rows > kMaxTokens || dim > kMaxRowDim || dim % group != 0)
+    return SSS_ERR_BAD_DIM;
+  if (group > kMaxNormDim) return SSS_ERR_UNSUPPORTED;
+  const double threads = group <= 1024 ? 64.0 : group <= 8192 ? 256.0 : group <= 16384 ? 512.0 : 1024.0;
+  if (((double)rows * (double)(dim / group) + 4.0) * threads > 2147483647.0) return SSS_ERR_BAD_DIM;
+  return SSS_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int rms_norm_gated_fwd(const void* x, int64_t x_stride, const float* weight, const void* z, int64_t z_stride, void* out,
+                       float* rstd, int64_t rows, int64_t dim, int64_t group, float eps, unsigned flags, int x_dtype,
+                       int out_dtype, sss_stream_t stream) {
+  if (!x || !weight || !out) return SSS_ERR_NULL_ARG;
+  const int st = norm_dims(rows, dim, group);
+  if (st != SSS_OK) return st;
+  if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype) || (flags & ~(unsigned)SSS_NORM_BEFORE_GATE) != 0)
+    return SSS_ERR_UNSUPPORTED;
+  if (!stride_ok(x_stride, dim) || (z && !stride_ok(z_stride, dim))) return SSS_ERR_BAD_DIM;
+  const int64_t xs = dtype_size(x_dtype), os = dtype_size(out_dtype);
+  Regions r;
+  r.in(x, span(rows, x_stride, dim, xs), xs);
+  r.in(weight, dim * 4, 4);
+  r.in(z, span(rows, z_stride, dim, os), os);
+  r.output(out, rows * dim * os, os);
+  r.output(rstd, rows * (dim / group) * 4, 4);
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  if (rows == 0) return SSS_OK;
+  GatedNormArgs a{};
+  a.x = x;
+  a.z = z;
+  a.w = weight;
+  a.out = out;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.group = group;
+  a.groups = dim / group;
+  a.sx = x_stride;
+  a.sz = z ? z_stride : 0;
+  a.eps = eps;
+  a.x_bf16 = x_dtype == SSS_BF16;
+  a.z_bf16 = out_dtype == SSS_BF16;
+  a.norm_first = (flags & SSS_NORM_BEFORE_GATE) != 0;
+  return status_of(launch_gated_norm_fwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t rms_norm_gated_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, int device) {
+  if (norm_dims(rows, dim, group) != SSS_OK) return 0;
+  int cus = device_cus(device);
+  if (cus <= 0) cus = 256;
+  return plan_norm_bwd(rows, group, dim / group, 1, cus).ws_total;
+}
+
+int rms_norm_gated_bwd(const void* dout, const void* x, int64_t x_stride, const float* weight, const void* z,
+                       int64_t z_stride, const float* rstd, void* dx, void* dz, int64_t dz_stride, float* dweight,
+                       int64_t rows, int64_t dim, int64_t group, unsigned flags, int x_dtype, int out_dtype,
+                       void* workspace, size_t workspace_bytes, sss_stream_t stream) {
+  if (!dweight || (rows != 0 && (!dout || !x || !weight || !rstd || !dx || (z && !dz)))) return SSS_ERR_NULL_ARG;
+  const int st = norm_dims(rows, dim, group);
+  if (st != SSS_OK) return st;
+  if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype) || (flags & ~(unsigned)SSS_NORM_BEFORE_GATE) != 0)
+    return SSS_ERR_UNSUPPORTED;
+  if (!stride_ok(x_stride, dim) || (z && (!stride_ok(z_stride, dim) || !stride_ok(dz_stride, dim))))
+    return SSS_ERR_BAD_DIM;
+  const int64_t xs = dtype_size(x_dtype), os = dtype_size(out_dtype);
+  Regions r;
+  r.in(dout, rows * dim * os, os);
+  r.in(x, span(rows, x_stride, dim, xs), xs);
+  r.in(weight, dim * 4, 4);
+  r.in(z, span(rows, z_stride, dim, os), os);
+  r.in(rstd, rows * (dim / group) * 4, 4);
+  r.output(dx, rows * dim * xs, xs);
+  r.output(z ? dz : nullptr, span(rows, dz_stride, dim, os), os);
+  r.output(dweight, dim * 4, 4);
+  if (workspace && !aligned16(workspace)) return SSS_ERR_UNSUPPORTED;
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  const int cus = current_device_cus();
+  if (cus <= 0) return SSS_ERR_HIP;
+  const NormPlan pl = plan_norm_bwd(rows, group, dim / group, 1, cus);
+  if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
+  r.output(workspace, (int64_t)pl.ws_total, 16);
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  GatedNormArgs a{};
+  a.x = x;
+  a.z = z;
+  a.w = weight;
+  a.rstd = const_cast<float*>(rstd);
+  a.dout = dout;
+  a.dx = dx;
+  a.dz = z ? dz : nullptr;
+  a.dw = dweight;
+  a.workspace = workspace;
+  a.rows = rows;
+  a.group = group;
+  a.groups = dim / group;
+  a.sx = x_stride;
+  a.sz = z ? z_stride : 0;
+  a.sdz = z ? dz_stride : 0;
+  a.x_bf16 = x_dtype == SSS_BF16;
+  a.z_bf16 = out_dtype == SSS_BF16;
+  a.norm_first = (flags & SSS_NORM_BEFORE_GATE) != 0;
+  return status_of(launch_gated_norm_bwd(a, pl, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int rms_norm_residual_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                          const float* post_weight, const float* scale, const float* weight, void* out,
+                          void* residual_out, float* rstd_post, float* rstd, int64_t rows, int64_t dim, float alpha,
+                          float eps, int io_dtype, int residual_dtype, sss_stream_t stream) {
+  if (!x || !weight || !out || !residual_out) return SSS_ERR_NULL_ARG;
+  const int st = norm_dims(rows, dim, dim);
+  if (st != SSS_OK) return st;
+  if (!dtype_ok(io_dtype) || !dtype_ok(residual_dtype)) return SSS_ERR_UNSUPPORTED;
+  if (!stride_ok(x_stride, dim) || (residual && !stride_ok(residual_stride, dim))) return SSS_ERR_BAD_DIM;
+  const int64_t es = dtype_size(io_dtype), hs = dtype_size(residual_dtype);
+  // the residual stream may be updated in place: the same rows, or no shared memory at all
+  const bool in_place = residual == residual_out && (residual_stride == dim || rows <= 1);
+  Regions r;
+  r.in(x, span(rows, x_stride, dim, es), es);
+  if (!in_place) r.in(residual, span(rows, residual_stride, dim, hs), hs);
+  r.in(post_weight, dim * 4, 4);
+  r.in(scale, dim * 4, 4);
+  r.in(weight, dim * 4, 4);
+  r.output(out, rows * dim * es, es);
+  r.output(residual_out, rows * dim * hs, hs);
+  r.output(post_weight ? rstd_post : nullptr, rows * 4, 4);
+  r.output(rstd, rows * 4, 4);
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  if (rows == 0) return SSS_OK;
+  ResNormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.wp = post_weight;
+  a.scale = scale;
+  a.w = weight;
+  a.out = out;
+  a.residual_out = residual_out;
+  a.rstd_post = rstd_post;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.dim = dim;
+  a.sx = x_stride;
+  a.sr = residual ? residual_stride : 0;
+  a.eps = eps;
+  a.alpha = alpha;
+  a.x_bf16 = io_dtype == SSS_BF16;
+  a.h_bf16 = residual_dtype == SSS_BF16;
+  return status_of(launch_res_norm_fwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t rms_norm_residual_bwd_workspace_size(int64_t rows, int64_t dim, int device) {
+  if (norm_dims(rows, dim, dim) != SSS_OK) return 0;
+  int cus = device_cus(device);
+  if (cus <= 0) cus = 256;
+  return plan_norm_bwd(rows, dim, 1, 3, cus).ws_total;
+}
+
+int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const void* x, int64_t x_stride,
+                          const void* residual_out, const float* post_weight, const float* scale, const float* weight,
+                          const float* rstd_post, const float* rstd, void* dx, void* dresidual, float* dweight,
+                          float* dpost_weight, float* dscale, int64_t rows, int64_t dim, float alpha, int io_dtype,
+                          int residual_dtype, void* workspace, size_t workspace_bytes, sss_stream_t stream) {
+  if (!dweight || (post_weight && !dpost_weight) || (scale && !dscale)) return SSS_ERR_NULL_ARG;
+  if (rows != 0 && (!dout || !residual_out || !weight || !rstd || !dx || (post_weight && !rstd_post) ||
+                    ((post_weight || scale) && !x)))
+    return SSS_ERR_NULL_ARG;
+  const int st = norm_dims(rows, dim, dim);
+  if (st != SSS_OK) return st;
+  if (!dtype_ok(io_dtype) || !dtype_ok(residual_dtype)) return SSS_ERR_UNSUPPORTED;
+  if (x && !stride_ok(x_stride, dim)) return SSS_ERR_BAD_DIM;
+  const int64_t es = dtype_size(io_dtype), hs = dtype_size(residual_dtype);
+  Regions r;
+  r.in(dout, rows * dim * es, es);
+  r.in(dresidual_out, rows * dim * hs, hs);
+  r.in(x, span(rows, x_stride, dim, es), es);
+  r.in(residual_out, rows * dim * hs, hs);
+  r.in(post_weight, dim * 4, 4);
+  r.in(scale, dim * 4, 4);
+  r.in(weight, dim * 4, 4);
+  r.in(post_weight ? rstd_post : nullptr, rows * 4, 4);
+  r.in(rstd, rows * 4, 4);
+  r.output(dx, rows * dim * es, es);
+  r.output(dresidual, rows * dim * hs, hs);
+  r.output(dweight, dim * 4, 4);
+  r.output(post_weight ? dpost_weight : nullptr, dim * 4, 4);
+  r.output(scale ? dscale : nullptr, dim * 4, 4);
+  if (workspace && !aligned16(workspace)) return SSS_ERR_UNSUPPORTED;
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  const int cus = current_device_cus();
+  if (cus <= 0) return SSS_ERR_HIP;
+  const NormPlan pl = plan_norm_bwd(rows, dim, 1, 3, cus);
+  if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
+  r.output(workspace, (int64_t)pl.ws_total, 16);
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  ResNormArgs a{};
+  a.x = x;
+  a.wp = post_weight;
+  a.scale = scale;
+  a.w = weight;
+  a.residual_out = const_cast<void*>(residual_out);
+  a.rstd_post = const_cast<float*>(rstd_post);
+  a.rstd = const_cast<float*>(rstd);
+  a.dout = dout;
+  a.dres_out = dresidual_out;
+  a.dx = dx;
+  a.dres = dresidual;
+  a.dw = dweight;
+  a.dwp = dpost_weight;
+  a.dscale = dscale;
+  a.workspace = workspace;
+  a.rows = rows;
+  a.dim = dim;
+  a.sx = x ? x_stride : 0;
+  a.alpha = alpha;
+  a.x_bf16 = io_dtype == SSS_BF16;
+  a.h_bf16 = residual_dtype == SSS_BF16;
+  return status_of(launch_res_norm_bwd(a, pl, reinterpret_cast<hipStream_t>(stream)));
+}
 
 int causal_conv1d_packed_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias, void* conv_state,
                              const int32_t* cu_seqlens, const int32_t* state_indices, const uint8_t* has_initial,

@@ -237,6 +237,61 @@ hipError_t launch_pscan_carry(const float* A, const float* ends, const float* su
                               int dstate, int dim, int chunks, hipStream_t stream);
 hipError_t launch_slot_update(const PackedScanArgs& a, hipStream_t stream);
 
+// Norms around the block (norms.hip).  Pointers marked nullable may be null.
+constexpr int64_t kMaxNormDim = 32768;  // elements of a normed row: 1024 lanes of 32
+struct NormPlan {
+  int nblk;       // workgroups per group of the gradients kernel
+  int part_rows;  // rows of partial parameter gradients
+  size_t ws_total;
+};
+
+struct GatedNormArgs {
+  const void* x;
+  const void* z;  // nullable: no gate
+  const float* w;
+  void* out;
+  float* rstd;  // (rows, groups): nullable output of the forward, input of the backward
+  const void* dout;
+  void* dx;
+  void* dz;
+  float* dw;
+  void* workspace;
+  int64_t rows, group, groups;
+  int64_t sx, sz, sdz;  // elements between rows
+  float eps;
+  int x_bf16, z_bf16, norm_first;  // out and dout have z's type
+};
+
+struct ResNormArgs {
+  const void* x;         // backward: nullable without post norm and scale
+  const void* residual;  // nullable: zero
+  const float* wp;       // nullable: no post norm
+  const float* scale;    // nullable: one
+  const float* w;
+  void* out;
+  void* residual_out;  // backward: input
+  float* rstd_post;    // nullable in the forward
+  float* rstd;
+  const void* dout;
+  const void* dres_out;  // nullable: zero
+  void* dx;
+  void* dres;  // nullable
+  float* dw;
+  float* dwp;
+  float* dscale;
+  void* workspace;
+  int64_t rows, dim;
+  int64_t sx, sr;
+  float eps, alpha;
+  int x_bf16, h_bf16;
+};
+
+NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, int num_cus);
+hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t stream);
+hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, const NormPlan& plan, hipStream_t stream);
+hipError_t launch_res_norm_fwd(const ResNormArgs& a, hipStream_t stream);
+hipError_t launch_res_norm_bwd(const ResNormArgs& a, const NormPlan& plan, hipStream_t stream);
+
 int env_int(const char* name, int dflt);
 
 }  // namespace sss

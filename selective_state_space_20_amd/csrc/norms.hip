@@ -1,0 +1,628 @@
+// norms.hip -- gfx950 kernels of the root-mean-square norms around the block, forward and
+// gradients.  With rstd(v) = (mean(v^2) + eps)^-1/2 over a group of G adjacent channels:
+//
+// Gated norm, after the scan (x: the scan's output, z: the block's gate):
+//   gate first   u = x silu(z),  out = u rstd(u) w
+//   norm first   out = x rstd(x) w silu(z)
+// Residual norm, after a block and before the next one (x: the block's output, h: the residual
+// stream):
+//   v = x rstd(x) wp  (or x),  h' = h + alpha s v,  out = h' rstd(h') w
+// Gradients, with hat = u rstd(u) and g the gradient of hat:  du = rstd (g - hat mean(g hat)).
+//
+// Streaming: each element read once and each result written once.  A row (of a group) is held in
+// the registers of one wave, of one workgroup of 256, 512 or 1024 lanes, whichever is the
+// smallest that holds it: 8 adjacent elements per lane and piece (16 bytes in bf16), M pieces.
+// Sums are fp32: lanes of a wave by DPP, waves through LDS.
+#include "vec.h"
+#include "kernels.h"
+
+#include <algorithm>
+
+namespace sss {
+
+template <int CTRL>
+__device__ __forceinline__ float norm_dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float norm_lane(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+// sum over a wave, the same in every lane
+__device__ __forceinline__ float wave_sum(float v) {
+  v += norm_dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+  v += norm_dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+  v += norm_dpp<0x141>(v);  // row_half_mirror
+  v += norm_dpp<0x140>(v);  // row_mirror: each row of 16 lanes holds its sum
+  return (norm_lane(v, 0) + norm_lane(v, 16)) + (norm_lane(v, 32) + norm_lane(v, 48));
+}
+
+// Sum over the TPR lanes that share a row.  `turn` alternates the LDS buffer: a wave that
+// writes a buffer again has passed the barrier of the sum in between, before which every
+// wave has read it, so that one barrier per sum suffices.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* lds, int& turn) {
+  v = wave_sum(v);
+  if constexpr (TPR > 64) {
+    constexpr int NW = TPR / 64;
+    float* const b = lds + (turn & 1) * NW;
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) b[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v += b[i];
+  }
+  return v;
+}
+
+// The pieces of a row of G elements: piece p starts at element 8p, the last one V elements
+// before the row's end where V does not divide G: its first `skip` elements are then another
+// lane's, count for nothing and are not stored.
+template <int V, int TPR, int M>
+struct Pieces {
+  int at[M], skip[M];
+  __device__ __forceinline__ Pieces(int G) {
+    const int tid = TPR == 64 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int p = (m * TPR + tid) * V;
+      at[m] = min(p, G - V);
+      skip[m] = min(p - at[m], V);
+    }
+  }
+  __device__ __forceinline__ bool live(int m) const { return skip[m] < V; }
+};
+
+struct GNormGeo {
+  int64_t sx, sz, sdz;  // elements between rows
+  int64_t rows;
+  int G, groups, nblk;  // backward: workgroups per group
+  float eps, inv_g;
+  int norm_first;
+};
+
+template <bool XB, bool ZB, int V, int TPR, int M>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_norm_fwd_kernel(
+    const char* __restrict__ x, const char* __restrict__ z, const float* __restrict__ w, char* __restrict__ out,
+    float* __restrict__ rstd_out, GNormGeo g) {
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;  // rows per workgroup
+  constexpr int XS = XB ? 2 : 4, ZS = ZB ? 2 : 4;
+  __shared__ float lds[2 * 16];
+  const int64_t vr = (int64_t)blockIdx.x * RPB + (RPB > 1 ? (int)(threadIdx.x / TPR) : 0);
+  if (RPB > 1 && vr >= g.rows * g.groups) return;  // a whole wave: no barrier with one wave per row
+  const int64_t row = vr / g.groups;
+  const int c0 = (int)(vr - row * g.groups) * g.G;
+  const Pieces<V, TPR, M> pc(g.G);
+  Vec<XB, V> xr[M];
+  Vec<ZB, V> zr[M];
+  Vec<false, V> wr[M];
+  const char* const xp = x + (row * g.sx + c0) * XS;
+  const char* const zp = z + (row * g.sz + c0) * ZS;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!pc.live(m)) continue;
+    xr[m].template load<true>(xp + (int64_t)pc.at[m] * XS);
+    if (z != nullptr) zr[m].template load<true>(zp + (int64_t)pc.at[m] * ZS);
+    wr[m].load(w + c0 + pc.at[m]);
+  }
+  float u[M][V], gt[M][V], s = 0.0f;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!pc.live(m)) continue;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      u[m][c] = xr[m].get(c);
+      gt[m][c] = z != nullptr ? silu(zr[m].get(c)) : 1.0f;
+      if (!g.norm_first) u[m][c] *= gt[m][c];
+      s += c < pc.skip[m] ? 0.0f : u[m][c] * u[m][c];
+    }
+  }
+  int turn = 0;
+  s = row_sum<TPR>(s, lds, turn);
+  const float rstd = __builtin_amdgcn_rsqf(s * g.inv_g + g.eps);
+  if (rstd_out != nullptr && (threadIdx.x & (TPR - 1)) == 0) rstd_out[vr] = rstd;
+  char* const op = out + (row * (int64_t)g.G * g.groups + c0) * ZS;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!pc.live(m)) continue;
+    float o[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      o[c] = u[m][c] * rstd * wr[m].get(c);
+      if (g.norm_first) o[c] *= gt[m][c];
+    }
+    Vec<ZB, V> r;
+    r.set(o);
+    r.template store_from<true>(op + (int64_t)pc.at[m] * ZS, pc.skip[m]);
+  }
+}
+
+// Gradients.  A workgroup takes every nblk-th set of rows of one group and sums dweight over them
+// in registers; the partials are added in their order by norm_sum_kernel.
+template <bool XB, bool ZB, int V, int TPR, int M>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_norm_bwd_kernel(
+    const char* __restrict__ dout, const char* __restrict__ x, const char* __restrict__ z, const float* __restrict__ w,
+    const float* __restrict__ rstd_in, char* __restrict__ dx, char* __restrict__ dz, float* __restrict__ part,
+    GNormGeo g) {
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  constexpr int XS = XB ? 2 : 4, ZS = ZB ? 2 : 4;
+  __shared__ float lds[2 * 16];
+  const int sub = RPB > 1 ? (int)(threadIdx.x / TPR) : 0;
+  const int grp = (int)(blockIdx.x % (unsigned)g.groups);
+  const int64_t blk = blockIdx.x / (unsigned)g.groups;
+  const int c0 = grp * g.G;
+  const int64_t D = (int64_t)g.G * g.groups;
+  const Pieces<V, TPR, M> pc(g.G);
+  float wv[M][V], dw[M][V];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    Vec<false, V> wr;
+    if (pc.live(m)) wr.load(w + c0 + pc.at[m]);
+    else wr.zero();
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      wv[m][c] = wr.get(c);
+      dw[m][c] = 0.0f;
+    }
+  }
+  int turn = 0;
+  for (int64_t row = blk * RPB + sub; row < g.rows; row += (int64_t)g.nblk * RPB) {
+    Vec<XB, V> xr[M];
+    Vec<ZB, V> zr[M], dr[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      dr[m].template load<true>(dout + (row * D + c0 + pc.at[m]) * ZS);
+      xr[m].template load<true>(x + (row * g.sx + c0 + pc.at[m]) * XS);
+      if (z != nullptr) zr[m].template load<true>(z + (row * g.sz + c0 + pc.at[m]) * ZS);
+    }
+    const float rstd = rstd_in[row * g.groups + grp];
+    float s = 0.0f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float gate = z != nullptr ? silu(zr[m].get(c)) : 1.0f;
+        const float hat = xr[m].get(c) * rstd * (g.norm_first ? 1.0f : gate);
+        const float dn = dr[m].get(c) * (g.norm_first ? gate : 1.0f);
+        dw[m][c] = __builtin_fmaf(dn, hat, dw[m][c]);
+        s += c < pc.skip[m] ? 0.0f : dn * wv[m][c] * hat;
+      }
+    }
+    s = row_sum<TPR>(s, lds, turn) * g.inv_g;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      float ox[V], oz[V];
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float xv = xr[m].get(c), dv = dr[m].get(c);
+        float zv = 0.0f, sg = 1.0f, gate = 1.0f;
+        if (z != nullptr) {
+          zv = zr[m].get(c);
+          sg = fast_rcp(1.0f + fast_exp2(-zv * kLog2e));
+          gate = zv * sg;
+        }
+        const float hat = xv * rstd * (g.norm_first ? 1.0f : gate);
+        const float gh = dv * (g.norm_first ? gate : 1.0f) * wv[m][c];
+        const float du = rstd * (gh - hat * s);
+        ox[c] = g.norm_first ? du : du * gate;
+        const float dgate = g.norm_first ? dv * hat * wv[m][c] : du * xv;
+        oz[c] = dgate * sg * __builtin_fmaf(zv, 1.0f - sg, 1.0f);
+      }
+      Vec<XB, V> rx;
+      rx.set(ox);
+      rx.template store_from<true>(dx + (row * D + c0 + pc.at[m]) * XS, pc.skip[m]);
+      if (z != nullptr) {
+        Vec<ZB, V> rz;
+        rz.set(oz);
+        rz.template store_from<true>(dz + (row * g.sdz + c0 + pc.at[m]) * ZS, pc.skip[m]);
+      }
+    }
+  }
+  float* const pp = part + (blk * RPB + sub) * D + c0;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!pc.live(m)) continue;
+    Vec<false, V> r;
+    r.set(dw[m]);
+    r.store_from(pp + pc.at[m], pc.skip[m]);
+  }
+}
+
+struct RNormGeo {
+  int64_t sx, sr;  // elements between rows of x and of the residual
+  int64_t rows;
+  int D, nblk;
+  float eps, inv_d, alpha;
+};
+
+// The kernel of the residual norm.  POST: x is normed first.  residual may be residual_out itself:
+// every element is read by the lane that writes it, before the sum that precedes the writes.
+template <bool XB, bool HB, bool POST, int V, int TPR, int M>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void res_norm_fwd_kernel(
+    const char* __restrict__ x, const char* residual, const float* __restrict__ wp, const float* __restrict__ scale,
+    const float* __restrict__ w, char* __restrict__ out, char* residual_out, float* __restrict__ rstd_post,
+    float* __restrict__ rstd_out, RNormGeo g) {
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  constexpr int XS = XB ? 2 : 4, HS = HB ? 2 : 4;
+  __shared__ float lds[2 * 16];
+  const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? (int)(threadIdx.x / TPR) : 0);
+  if (RPB > 1 && row >= g.rows) return;
+  const Pieces<V, TPR, M> pc(g.D);
+  Vec<XB, V> xr[M];
+  Vec<HB, V> hr[M];
+  Vec<false, V> wr[M], pr[M], sr[M];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!pc.live(m)) continue;
+    xr[m].template load<true>(x + (row * g.sx + pc.at[m]) * XS);
+    if (residual != nullptr) hr[m].template load<true>(residual + (row * g.sr + pc.at[m]) * HS);
+    wr[m].load(w + pc.at[m]);
+    if constexpr (POST) pr[m].load(wp + pc.at[m]);
+    if (scale != nullptr) sr[m].load(scale + pc.at[m]);
+  }
+  int turn = 0;
+  const bool first = (threadIdx.x & (TPR - 1)) == 0;
+  float rp = 1.0f;
+  if constexpr (POST) {
+    float s = 0.0f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) s += c < pc.skip[m] ? 0.0f : xr[m].get(c) * xr[m].get(c);
+    }
+    s = row_sum<TPR>(s, lds, turn);
+    rp = __builtin_amdgcn_rsqf(s * g.inv_d + g.eps);
+    if (rstd_post != nullptr && first) rstd_post[row] = rp;
+  }
+  float h[M][V], s = 0.0f;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!pc.live(m)) continue;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      float v = xr[m].get(c);
+      if constexpr (POST) v *= rp * pr[m].get(c);
+      v *= scale != nullptr ? g.alpha * sr[m].get(c) : g.alpha;
+      h[m][c] = residual != nullptr ? hr[m].get(c) + v : v;
+      s += c < pc.skip[m] ? 0.0f : h[m][c] * h[m][c];
+    }
+  }
+  s = row_sum<TPR>(s, lds, turn);
+  const float rstd = __builtin_amdgcn_rsqf(s * g.inv_d + g.eps);
+  if (rstd_out != nullptr && first) rstd_out[row] = rstd;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!pc.live(m)) continue;
+    Vec<HB, V> rh;
+    rh.set(h[m]);
+    rh.template store_from<false>(residual_out + (row * (int64_t)g.D + pc.at[m]) * HS, pc.skip[m]);
+    float o[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) o[c] = h[m][c] * rstd * wr[m].get(c);  // of h' before it is rounded
+    Vec<XB, V> r;
+    r.set(o);
+    r.template store_from<true>(out + (row * (int64_t)g.D + pc.at[m]) * XS, pc.skip[m]);
+  }
+}
+
+// Gradients; partials [workgroup row][3][D]: dweight, dpost_weight, dscale (those that are wanted).
+template <bool XB, bool HB, bool POST, int V, int TPR, int M>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void res_norm_bwd_kernel(
+    const char* __restrict__ dout, const char* __restrict__ dres_out, const char* __restrict__ x,
+    const char* __restrict__ h, const float* __restrict__ wp, const float* __restrict__ scale,
+    const float* __restrict__ w, const float* __restrict__ rstd_post, const float* __restrict__ rstd_in,
+    char* __restrict__ dx, char* __restrict__ dres, float* __restrict__ part, RNormGeo g) {
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  constexpr int XS = XB ? 2 : 4, HS = HB ? 2 : 4;
+  __shared__ float lds[2 * 16];
+  const int sub = RPB > 1 ? (int)(threadIdx.x / TPR) : 0;
+  const int64_t blk = blockIdx.x;
+  const int64_t D = g.D;
+  const Pieces<V, TPR, M> pc(g.D);
+  const bool use_x = POST || scale != nullptr;
+  float wv[M][V], pv[M][V], sv[M][V], dw[M][V], dp[M][V], ds[M][V];
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    Vec<false, V> a, b, c2;
+    a.zero();
+    b.zero();
+    c2.zero();
+    if (pc.live(m)) {
+      a.load(w + pc.at[m]);
+      if constexpr (POST) b.load(wp + pc.at[m]);
+      if (scale != nullptr) c2.load(scale + pc.at[m]);
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      wv[m][c] = a.get(c);
+      pv[m][c] = POST ? b.get(c) : 1.0f;
+      sv[m][c] = scale != nullptr ? g.alpha * c2.get(c) : g.alpha;
+      dw[m][c] = dp[m][c] = ds[m][c] = 0.0f;
+    }
+  }
+  int turn = 0;
+  for (int64_t row = blk * RPB + sub; row < g.rows; row += (int64_t)g.nblk * RPB) {
+    Vec<XB, V> dr[M], xr[M];
+    Vec<HB, V> hr[M], er[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      dr[m].template load<true>(dout + (row * D + pc.at[m]) * XS);
+      hr[m].template load<true>(h + (row * D + pc.at[m]) * HS);
+      if (dres_out != nullptr) er[m].template load<true>(dres_out + (row * D + pc.at[m]) * HS);
+      if (use_x) xr[m].template load<true>(x + (row * g.sx + pc.at[m]) * XS);
+    }
+    const float rstd = rstd_in[row];
+    float s = 0.0f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float hat = hr[m].get(c) * rstd, d = dr[m].get(c);
+        dw[m][c] = __builtin_fmaf(d, hat, dw[m][c]);
+        s += c < pc.skip[m] ? 0.0f : d * wv[m][c] * hat;
+      }
+    }
+    s = row_sum<TPR>(s, lds, turn) * g.inv_d;
+    float dh[M][V];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float hat = hr[m].get(c) * rstd;
+        const float d = rstd * (dr[m].get(c) * wv[m][c] - hat * s);
+        dh[m][c] = dres_out != nullptr ? er[m].get(c) + d : d;
+      }
+      if (dres != nullptr) {
+        Vec<HB, V> r;
+        r.set(dh[m]);
+        r.template store_from<true>(dres + (row * D + pc.at[m]) * HS, pc.skip[m]);
+      }
+    }
+    const float rp = POST ? rstd_post[row] : 1.0f;
+    float s2 = 0.0f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float hat = use_x ? xr[m].get(c) * rp : 0.0f;  // x rstd(x), or x
+        const float dv = sv[m][c] * dh[m][c];
+        if (scale != nullptr) ds[m][c] = __builtin_fmaf(g.alpha * dh[m][c], hat * pv[m][c], ds[m][c]);
+        if constexpr (POST) {
+          dp[m][c] = __builtin_fmaf(dv, hat, dp[m][c]);
+          s2 += c < pc.skip[m] ? 0.0f : dv * pv[m][c] * hat;
+        }
+      }
+    }
+    if constexpr (POST) s2 = row_sum<TPR>(s2, lds, turn) * g.inv_d;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      float o[V];
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float dv = sv[m][c] * dh[m][c];
+        if constexpr (POST) o[c] = rp * (dv * pv[m][c] - xr[m].get(c) * rp * s2);
+        else o[c] = dv;
+      }
+      Vec<XB, V> r;
+      r.set(o);
+      r.template store_from<true>(dx + (row * D + pc.at[m]) * XS, pc.skip[m]);
+    }
+  }
+  const int64_t vecs = 1 + (POST ? 1 : 0) + (scale != nullptr ? 1 : 0);
+  float* pp = part + (blk * RPB + sub) * vecs * D;
+  auto put = [&](const float (&v)[M][V]) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      Vec<false, V> r;
+      r.set(v[m]);
+      r.store_from(pp + pc.at[m], pc.skip[m]);
+    }
+    pp += D;
+  };
+  put(dw);
+  if constexpr (POST) put(dp);
+  if (scale != nullptr) put(ds);
+}
+
+// Column sums of `rows` partial rows of `cols` floats, added in their order: 64 columns and 4 row
+// ranges per workgroup, the ranges joined in LDS.  Columns d, D + d, 2D + d go to out0, out1, out2.
+static __global__ __launch_bounds__(256) void norm_sum_kernel(const float* __restrict__ part, float* __restrict__ out0,
+                                                              float* __restrict__ out1, float* __restrict__ out2,
+                                                              int rows, int64_t cols, int D) {
+  __shared__ float lds[256];
+  const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+  const int64_t cc = min(col, cols - 1);
+  const int q = threadIdx.x >> 6;
+  const int per = (rows + 3) / 4;
+  const int r1 = min(rows, (q + 1) * per);
+  float s = 0.0f;
+  for (int r = q * per; r < r1; r += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)min(r + i, r1 - 1) * cols + cc];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += r + i < r1 ? v[i] : 0.0f;
+  }
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x >= 64 || col >= cols) return;
+  s = (lds[threadIdx.x] + lds[threadIdx.x + 64]) + (lds[threadIdx.x + 128] + lds[threadIdx.x + 192]);
+  const int k = (int)(col / D);
+  (k == 0 ? out0 : k == 1 ? out1 : out2)[col - (int64_t)k * D] = s;
+}
+
+// Lanes per row and pieces per lane for rows of G elements (V = 8; fewer elements: one wave, V = 1).
+struct NormShape {
+  int v, tpr, m;
+};
+static NormShape norm_shape(int64_t G) {
+  if (G < 8) return {1, 64, 1};
+  const int64_t p = (G + 7) / 8;
+  if (p <= 64) return {8, 64, 1};
+  if (p <= 128) return {8, 64, 2};
+  if (p <= 256) return {8, 256, 1};
+  if (p <= 512) return {8, 256, 2};
+  if (p <= 768) return {8, 256, 3};
+  if (p <= 1024) return {8, 256, 4};
+  if (p <= 1536) return {8, 512, 3};
+  if (p <= 2048) return {8, 512, 4};
+  return {8, 1024, 4};
+}
+
+NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, int num_cus) {
+  NormPlan pl{};
+  const NormShape sh = norm_shape(group);
+  const int rpb = sh.tpr < 256 ? 256 / sh.tpr : 1;
+  // enough workgroups to fill the device, few enough that their partials stay small
+  const int64_t want = std::max<int64_t>(1, (int64_t)num_cus * (sh.tpr > 256 ? 2 : 4) / groups);
+  pl.nblk = (int)std::max<int64_t>(1, std::min<int64_t>(want, (rows + rpb - 1) / rpb));
+  pl.part_rows = pl.nblk * rpb;
+  pl.ws_total = (size_t)pl.part_rows * vectors * group * groups * 4;
+  return pl;
+}
+
+#define SSS_NORM_SHAPES(CALL)                                                   \
+  do {                                                                          \
+    if (sh.v == 1) { CALL(1, 64, 1); }                                          \
+    else if (sh.tpr == 64 && sh.m == 1) { CALL(8, 64, 1); }                     \
+    else if (sh.tpr == 64) { CALL(8, 64, 2); }                                  \
+    else if (sh.tpr == 256 && sh.m == 1) { CALL(8, 256, 1); }                   \
+    else if (sh.tpr == 256 && sh.m == 2) { CALL(8, 256, 2); }                   \
+    else if (sh.tpr == 256 && sh.m == 3) { CALL(8, 256, 3); }                   \
+    else if (sh.tpr == 256) { CALL(8, 256, 4); }                                \
+    else if (sh.tpr == 512 && sh.m == 3) { CALL(8, 512, 3); }                   \
+    else if (sh.tpr == 512) { CALL(8, 512, 4); }                                \
+    else { CALL(8, 1024, 4); }                                                  \
+  } while (0)
+
+static GNormGeo gated_geo(const GatedNormArgs& a) {
+  GNormGeo g{};
+  g.sx = a.sx;
+  g.sz = a.sz;
+  g.sdz = a.sdz;
+  g.rows = a.rows;
+  g.G = (int)a.group;
+  g.groups = (int)a.groups;
+  g.eps = a.eps;
+  g.inv_g = 1.0f / (float)a.group;
+  g.norm_first = a.norm_first;
+  return g;
+}
+
+template <bool XB, bool ZB>
+static hipError_t gated_fwd(const GatedNormArgs& a, hipStream_t stream) {
+  const GNormGeo g = gated_geo(a);
+  const NormShape sh = norm_shape(a.group);
+  const int64_t vrows = a.rows * a.groups;
+#define CALL(V, TPR, M)                                                                                             \
+  hipLaunchKernelGGL((gated_norm_fwd_kernel<XB, ZB, V, TPR, M>),                                                    \
+                     dim3((unsigned)((vrows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))),      \
+                     dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.x, (const char*)a.z, a.w, (char*)a.out, \
+                     a.rstd, g)
+  SSS_NORM_SHAPES(CALL);
+#undef CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t stream) {
+  if (a.x_bf16) return a.z_bf16 ? gated_fwd<true, true>(a, stream) : gated_fwd<true, false>(a, stream);
+  return a.z_bf16 ? gated_fwd<false, true>(a, stream) : gated_fwd<false, false>(a, stream);
+}
+
+template <bool XB, bool ZB>
+static hipError_t gated_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStream_t stream) {
+  GNormGeo g = gated_geo(a);
+  g.nblk = pl.nblk;
+  const NormShape sh = norm_shape(a.group);
+#define CALL(V, TPR, M)                                                                                               \
+  hipLaunchKernelGGL((gated_norm_bwd_kernel<XB, ZB, V, TPR, M>), dim3((unsigned)(pl.nblk * a.groups)),                 \
+                     dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.dout, (const char*)a.x, (const char*)a.z, \
+                     a.w, a.rstd, (char*)a.dx, (char*)a.dz, (float*)a.workspace, g)
+  SSS_NORM_SHAPES(CALL);
+#undef CALL
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t D = a.group * a.groups;
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((D + 63) / 64)), dim3(256), 0, stream, (const float*)a.workspace,
+                     a.dw, (float*)nullptr, (float*)nullptr, pl.part_rows, D, (int)D);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStream_t stream) {
+  if (a.x_bf16) return a.z_bf16 ? gated_bwd<true, true>(a, pl, stream) : gated_bwd<true, false>(a, pl, stream);
+  return a.z_bf16 ? gated_bwd<false, true>(a, pl, stream) : gated_bwd<false, false>(a, pl, stream);
+}
+
+static RNormGeo res_geo(const ResNormArgs& a) {
+  RNormGeo g{};
+  g.sx = a.sx;
+  g.sr = a.sr;
+  g.rows = a.rows;
+  g.D = (int)a.dim;
+  g.eps = a.eps;
+  g.inv_d = 1.0f / (float)a.dim;
+  g.alpha = a.alpha;
+  return g;
+}
+
+template <bool XB, bool HB, bool POST>
+static hipError_t res_fwd(const ResNormArgs& a, hipStream_t stream) {
+  const RNormGeo g = res_geo(a);
+  const NormShape sh = norm_shape(a.dim);
+#define CALL(V, TPR, M)                                                                                               \
+  hipLaunchKernelGGL((res_norm_fwd_kernel<XB, HB, POST, V, TPR, M>),                                                  \
+                     dim3((unsigned)((a.rows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))),       \
+                     dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.x, (const char*)a.residual, a.wp, a.scale, \
+                     a.w, (char*)a.out, (char*)a.residual_out, a.rstd_post, a.rstd, g)
+  SSS_NORM_SHAPES(CALL);
+#undef CALL
+  return hipGetLastError();
+}
+
+template <bool XB, bool HB, bool POST>
+static hipError_t res_bwd(const ResNormArgs& a, const NormPlan& pl, hipStream_t stream) {
+  RNormGeo g = res_geo(a);
+  g.nblk = pl.nblk;
+  const NormShape sh = norm_shape(a.dim);
+#define CALL(V, TPR, M)                                                                                                \
+  hipLaunchKernelGGL((res_norm_bwd_kernel<XB, HB, POST, V, TPR, M>), dim3((unsigned)pl.nblk),                          \
+                     dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.dout, (const char*)a.dres_out,             \
+                     (const char*)a.x, (const char*)a.residual_out, a.wp, a.scale, a.w, a.rstd_post, a.rstd,           \
+                     (char*)a.dx, (char*)a.dres, (float*)a.workspace, g)
+  SSS_NORM_SHAPES(CALL);
+#undef CALL
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t cols = a.dim * (1 + (POST ? 1 : 0) + (a.scale != nullptr ? 1 : 0));
+  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream,
+                     (const float*)a.workspace, a.dw, POST ? a.dwp : a.dscale, a.dscale, pl.part_rows, cols, (int)a.dim);
+  return hipGetLastError();
+}
+
+template <bool XB, bool HB>
+static hipError_t res_types(const ResNormArgs& a, const NormPlan* pl, hipStream_t stream) {
+  if (a.wp != nullptr) return pl ? res_bwd<XB, HB, true>(a, *pl, stream) : res_fwd<XB, HB, true>(a, stream);
+  return pl ? res_bwd<XB, HB, false>(a, *pl, stream) : res_fwd<XB, HB, false>(a, stream);
+}
+
+static hipError_t res_norm(const ResNormArgs& a, const NormPlan* pl, hipStream_t stream) {
+  if (a.x_bf16) return a.h_bf16 ? res_types<true, true>(a, pl, stream) : res_types<true, false>(a, pl, stream);
+  return a.h_bf16 ? res_types<false, true>(a, pl, stream) : res_types<false, false>(a, pl, stream);
+}
+
+hipError_t launch_res_norm_fwd(const ResNormArgs& a, hipStream_t stream) { return res_norm(a, nullptr, stream); }
+hipError_t launch_res_norm_bwd(const ResNormArgs& a, const NormPlan& pl, hipStream_t stream) {
+  return res_norm(a, &pl, stream);
+}
+
+}  // namespace sss

@@ -121,3 +121,83 @@ def packed_scan(x, delta, A, B, C, D, z, cu, state, idx, initial, bias, soft):
         if where[s] is not None:
             st[where[s]] = h
     return y, st
+
+
+def grouped(v, group):
+    return v.reshape(v.shape[0], -1, group)
+
+
+def rstd_of(v, group, eps):
+    """(rows, groups) factors (mean(v^2) + eps)^-1/2."""
+    return 1.0 / np.sqrt((grouped(v, group) ** 2).mean(-1) + eps)
+
+
+def spread(r, group):
+    return np.repeat(r, group, axis=1)
+
+
+def gated_norm(x, w, z, group, eps, norm_first):
+    """(out, rstd)."""
+    gate = silu(z) if z is not None else np.ones_like(x)
+    u = x if norm_first else x * gate
+    r = rstd_of(u, group, eps)
+    out = u * spread(r, group) * w
+    return (out * gate if norm_first else out), r
+
+
+def gated_norm_grad(dout, x, w, z, rstd, group, norm_first):
+    """{name: (gradient, sum of absolute terms)} from the forward's factors."""
+    mean = lambda v: spread(grouped(v, group).mean(-1), group)
+    r = spread(rstd, group)
+    gate = silu(z) if z is not None else np.ones_like(x)
+    hat = x * r * (1.0 if norm_first else gate)
+    dn = dout * (gate if norm_first else 1.0)
+    g = dn * w
+    du = r * (g - hat * mean(g * hat))
+    du_mag = r * (np.abs(g) + np.abs(hat) * mean(np.abs(g * hat)))
+    res = {"dx": (du, du_mag) if norm_first else (du * gate, du_mag * np.abs(gate)),
+           "dweight": ((dn * hat).sum(0), np.abs(dn * hat).sum(0))}
+    if z is not None:
+        s = 1.0 / (1.0 + np.exp(-z))
+        slope = s * (1.0 + z * (1.0 - s))
+        dgate, mag = (dout * hat * w, np.abs(dout * hat * w)) if norm_first else (du * x, du_mag * np.abs(x))
+        # the slope's own terms, s and s z (1 - s), cancel near its zero
+        res["dz"] = (dgate * slope, mag * s * (1.0 + np.abs(z)))
+    return res
+
+
+def residual_norm(x, w, h, wp, scale, alpha, eps):
+    """(out, residual_out, rstd, rstd_post, sum of absolute terms of residual_out)."""
+    v, rp = x, None
+    if wp is not None:
+        rp = rstd_of(x, x.shape[1], eps)
+        v = x * rp * wp
+    v = v * alpha * (scale if scale is not None else 1.0)
+    new = v if h is None else h + v
+    r = rstd_of(new, x.shape[1], eps)
+    return new * r * w, new, r, rp, np.abs(v) + (np.abs(h) if h is not None else 0.0)
+
+
+def residual_norm_grad(dout, dnew, x, w, new, rstd, wp, scale, rstd_post, alpha):
+    """{name: (gradient, sum of absolute terms)} from the forward's results."""
+    mean = lambda v: v.mean(-1, keepdims=True)
+    hat = new * rstd
+    g = dout * w
+    dh = rstd * (g - hat * mean(g * hat))
+    mag = rstd * (np.abs(g) + np.abs(hat) * mean(np.abs(g * hat)))
+    if dnew is not None:
+        dh, mag = dh + dnew, mag + np.abs(dnew)
+    s = alpha * (scale if scale is not None else 1.0)
+    dv, dv_mag = dh * s, mag * np.abs(s)
+    res = {"dresidual": (dh, mag), "dweight": ((dout * hat).sum(0), np.abs(dout * hat).sum(0))}
+    xh = x * rstd_post if wp is not None else x
+    if scale is not None:
+        p = xh * (wp if wp is not None else 1.0)
+        res["dscale"] = ((alpha * dh * p).sum(0), np.abs(alpha * mag * p).sum(0))
+    if wp is None:
+        res["dx"] = (dv, dv_mag)
+        return res
+    res["dpost_weight"] = ((dv * xh).sum(0), (dv_mag * np.abs(xh)).sum(0))
+    g, g_mag = dv * wp, dv_mag * np.abs(wp)
+    res["dx"] = (rstd_post * (g - xh * mean(g * xh)), rstd_post * (g_mag + np.abs(xh) * mean(g_mag * np.abs(xh))))
+    return res

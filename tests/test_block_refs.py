@@ -74,3 +74,61 @@ def test_packed_scan_agrees_with_the_oracle(oracle_lib):
         np.testing.assert_allclose(y[r], np.asarray(yo)[0], rtol=1e-12, atol=1e-12)
         np.testing.assert_allclose(st[slot], np.asarray(ho)[0], rtol=1e-12, atol=1e-12)
     np.testing.assert_array_equal(st[1], state[1].astype(np.float64))
+
+
+def differences(loss, arrays, eps=1e-5):
+    """Central differences of loss() in every entry of the arrays, which it reads."""
+    res = []
+    for arr in arrays:
+        g = np.zeros_like(arr)
+        for i in np.ndindex(arr.shape):
+            keep = arr[i]
+            arr[i] = keep + eps
+            up = loss()
+            arr[i] = keep - eps
+            down = loss()
+            arr[i] = keep
+            g[i] = (up - down) / (2 * eps)
+        res.append(g)
+    return res
+
+
+@pytest.mark.parametrize("norm_first", [False, True])
+@pytest.mark.parametrize("group,with_z", [(6, True), (2, True), (3, False), (1, True)])
+def test_gated_norm_gradient_formulas_against_differences(group, with_z, norm_first):
+    rng = np.random.default_rng(5)
+    x, w, dout = rng.standard_normal((3, 6)), rng.standard_normal(6), rng.standard_normal((3, 6))
+    z = rng.standard_normal((3, 6)) if with_z else None
+    eps = 0.1  # large, so that single-channel groups have a gradient
+    loss = lambda: float((dout * ref.gated_norm(x, w, z, group, eps, norm_first)[0]).sum())
+    g = ref.gated_norm_grad(dout, x, w, z, ref.gated_norm(x, w, z, group, eps, norm_first)[1], group, norm_first)
+    names = ("dx", "dweight") + (("dz",) if with_z else ())
+    for name, d in zip(names, differences(loss, (x, w) + ((z,) if with_z else ()))):
+        np.testing.assert_allclose(g[name][0], d, rtol=1e-6, atol=1e-7, err_msg=name)
+
+
+@pytest.mark.parametrize("post,scaled,first", [(True, True, False), (True, False, False), (False, True, False),
+                                               (False, False, False), (True, True, True)])
+def test_residual_norm_gradient_formulas_against_differences(post, scaled, first):
+    rng = np.random.default_rng(6)
+    x, w, dout, dnew = (rng.standard_normal(s) for s in ((3, 5), 5, (3, 5), (3, 5)))
+    h = None if first else rng.standard_normal((3, 5))
+    wp = rng.standard_normal(5) if post else None
+    scale = rng.standard_normal(5) if scaled else None
+    fwd = lambda: ref.residual_norm(x, w, h, wp, scale, 0.7, 0.01)
+    loss = lambda: float((dout * fwd()[0]).sum() + (dnew * fwd()[1]).sum())
+    _, new, r, rp, _ = fwd()
+    g = ref.residual_norm_grad(dout, dnew, x, w, new, r, wp, scale, rp, 0.7)
+    given = {"dx": x, "dweight": w, "dresidual": h, "dpost_weight": wp, "dscale": scale}
+    given = {k: v for k, v in given.items() if v is not None}
+    for (name, _), d in zip(given.items(), differences(loss, given.values())):
+        np.testing.assert_allclose(g[name][0], d, rtol=1e-6, atol=1e-7, err_msg=name)
+
+
+def test_norms_of_hand_worked_rows():
+    out, r = ref.gated_norm(np.array([[3.0, 4.0]]), np.array([1.0, 2.0]), None, 2, 0.0, False)
+    np.testing.assert_allclose(out, [[3 / np.sqrt(12.5), 8 / np.sqrt(12.5)]])
+    out, new, *_ = ref.residual_norm(np.array([[1.0, -1.0]]), np.ones(2), np.array([[2.0, 5.0]]), np.array([2.0, 2.0]),
+                                     np.array([0.5, 1.0]), 1.0, 0.0)
+    np.testing.assert_allclose(new, [[3.0, 3.0]])
+    np.testing.assert_allclose(out, [[1.0, 1.0]])

@@ -136,3 +136,73 @@ def test_binding_rejects_host_tensors_types_and_shapes():
         sss.selective_scan_packed_fwd(t(4, 8), t(4, 8), t(8, 16), t(4, 16, dtype=torch.float64), t(4, 16), cu_seqlens=cu)
     with pytest.raises(ValueError, match="must be on a GPU"):
         sss.selective_state_update_slots(t(4, 8), t(4, 8), t(8, 16), t(4, 16), t(4, 16), state=t(4, 8, 16))
+
+
+def gated(**kw):
+    return call("rms_norm_gated_fwd", dict(x=P, sx=8, weight=2 * P, z=3 * P, sz=8, out=4 * P, rstd=5 * P, rows=3, dim=8,
+                                           group=4, eps=1e-5, flags=0, x_dtype=0, out_dtype=1, stream=0), kw)
+
+
+def gated_bwd(**kw):
+    return call("rms_norm_gated_bwd", dict(
+        dout=P, x=2 * P, sx=8, weight=3 * P, z=4 * P, sz=8, rstd=5 * P, dx=6 * P, dz=7 * P, sdz=8, dweight=8 * P, rows=3,
+        dim=8, group=4, flags=0, x_dtype=0, out_dtype=1, workspace=9 * P, workspace_bytes=1 << 20, stream=0), kw)
+
+
+def residual(**kw):
+    return call("rms_norm_residual_fwd", dict(
+        x=P, sx=8, residual=2 * P, sr=8, post=3 * P, scale=4 * P, weight=5 * P, out=6 * P, residual_out=7 * P,
+        rstd_post=8 * P, rstd=9 * P, rows=3, dim=8, alpha=1.0, eps=1e-5, io_dtype=1, residual_dtype=0, stream=0), kw)
+
+
+def residual_bwd(**kw):
+    return call("rms_norm_residual_bwd", dict(
+        dout=P, dres_out=2 * P, x=3 * P, sx=8, residual_out=4 * P, post=5 * P, scale=6 * P, weight=7 * P, rstd_post=8 * P,
+        rstd=9 * P, dx=10 * P, dres=11 * P, dweight=12 * P, dpost=13 * P, dscale=14 * P, rows=3, dim=8, alpha=1.0,
+        io_dtype=1, residual_dtype=0, workspace=15 * P, workspace_bytes=1 << 20, stream=0), kw)
+
+
+def test_gated_norm_rejections():
+    for k in ("x", "weight", "out"):
+        assert gated(**{k: 0}) == NULL_ARG, k
+    for k in ("dout", "x", "weight", "rstd", "dx", "dz", "dweight"):
+        assert gated_bwd(**{k: 0}) == NULL_ARG, k
+    for fn in (gated, gated_bwd):
+        assert fn(rows=-1) == BAD_DIM and fn(dim=0) == BAD_DIM and fn(group=3) == BAD_DIM and fn(sx=7) == BAD_DIM
+        assert fn(dim=65536, group=65536, sx=65536, sz=65536) == UNSUPPORTED
+        assert fn(rows=1 << 28) == BAD_DIM
+        assert fn(flags=2) == UNSUPPORTED and fn(x_dtype=2) == UNSUPPORTED and fn(out_dtype=-1) == UNSUPPORTED
+        assert fn(x=2 * P + 2) == UNSUPPORTED
+    assert gated(out=P) == ALIAS and gated(out=3 * P) == ALIAS and gated(rstd=4 * P) == ALIAS
+    assert gated_bwd(dx=2 * P) == ALIAS and gated_bwd(dz=6 * P) == ALIAS and gated_bwd(dweight=3 * P) == ALIAS
+    assert gated_bwd(sdz=4) == BAD_DIM and gated_bwd(workspace=9 * P + 8) == UNSUPPORTED
+    assert gated(rows=0) == 0
+
+
+def test_residual_norm_rejections():
+    for k in ("x", "weight", "out", "residual_out"):
+        assert residual(**{k: 0}) == NULL_ARG, k
+    for k in ("dout", "x", "residual_out", "weight", "rstd_post", "rstd", "dx", "dweight", "dpost", "dscale"):
+        assert residual_bwd(**{k: 0}) == NULL_ARG, k
+    for fn in (residual, residual_bwd):
+        assert fn(rows=-1) == BAD_DIM and fn(dim=0) == BAD_DIM and fn(sx=7) == BAD_DIM
+        assert fn(dim=32769, sx=32769) == UNSUPPORTED and fn(io_dtype=2) == UNSUPPORTED
+        assert fn(residual_dtype=5) == UNSUPPORTED
+    assert residual(out=P) == ALIAS and residual(residual_out=P) == ALIAS
+    assert residual(residual=7 * P, sr=9) == ALIAS      # in place needs the same rows
+    assert residual(residual=7 * P + 32) == ALIAS
+    assert residual_bwd(dx=P) == ALIAS and residual_bwd(dscale=13 * P) == ALIAS
+    assert residual(rows=0) == 0
+
+
+def test_norm_binding_rejections():
+    with pytest.raises(ValueError, match="must divide"):
+        sss.rms_norm_gated_fwd(t(2, 8), t(8), group_size=3)
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        sss.rms_norm_gated_fwd(t(2, 8), t(8))
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        sss.rms_norm_residual_fwd(t(2, 8, dtype=torch.float16), t(8))
+    with pytest.raises(ValueError, match="x is needed"):
+        sss.rms_norm_residual_bwd(t(2, 8), residual_out=t(2, 8), weight=t(8), rstd=t(2), scale=t(8))
+    with pytest.raises(ValueError, match="rstd_post is needed"):
+        sss.rms_norm_residual_bwd(t(2, 8), residual_out=t(2, 8), weight=t(8), rstd=t(2), x=t(2, 8), post_weight=t(8))
