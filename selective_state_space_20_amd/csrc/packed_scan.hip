@@ -32,10 +32,10 @@ struct PScanGeo {
   int64_t sx, sd, sz, sb, sc;  // elements between tokens of x, delta, z, B, C
   int tokens, nseq, slots, D, K, ngroups, gpb, nblk;
   int piece;  // tokens whose rows stay within 32-bit byte offsets of the first
-  int bc_bf16, y_bf16;
+  int bc_bf16;
 };
 
-constexpr int pscan_min_waves(int ns) { return ns >= 64 ? 2 : ns >= 32 ? 3 : 4; }
+constexpr int pscan_min_waves(int ns) { return ns >= 64 ? 1 : ns >= 32 ? 2 : 4; }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t pscan_rsrc(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7FFFFFFF, 0x00020000);
@@ -45,7 +45,8 @@ __device__ __forceinline__ uint32_t pscan_u32(float f) { return __builtin_bit_ca
 
 typedef uint32_t pscan_u4 __attribute__((ext_vector_type(4)));
 
-template <int NS, bool BF16, int PASS, int FL>
+// HAS_Z, YB (y is bf16): pass 2 only.
+template <int NS, bool BF16, int PASS, int FL, bool HAS_Z, bool YB>
 __global__ __launch_bounds__(128, pscan_min_waves(NS)) void packed_scan_kernel(
     const char* __restrict__ x, const char* __restrict__ delta, const float* __restrict__ A,
     const char* __restrict__ Bm, const char* __restrict__ Cm, const float* __restrict__ Dsk,
@@ -82,8 +83,8 @@ __global__ __launch_bounds__(128, pscan_min_waves(NS)) void packed_scan_kernel(
   for (int n = 0; n < NS; ++n) a2[n] = fmaxf(A[(int64_t)dc * NS + n] * kLog2e, -kFltMax);  // -inf clamped: 0*a2 = 0
   const float dbv = ((FL & kFront) != 0 && dbias != nullptr) ? dbias[dc] : 0.0f;
   const float Dd = (PASS == 2 && Dsk != nullptr) ? Dsk[dc] : 0.0f;
-  const bool has_z = PASS == 2 && z != nullptr;
-  const bool bcb = g.bc_bf16 != 0, yb = g.y_bf16 != 0;
+  constexpr bool has_z = PASS == 2 && HAS_Z, yb = YB;
+  const bool bcb = g.bc_bf16 != 0;
   float dsum = 0.0f;
   const int rstep = lane * PL / NS, rcol = lane * PL % NS;  // the row tile's piece of this lane
 
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(128, pscan_min_waves(NS)) void packed_scan_kernel(
         const int q = min(t0 + i, len - 1);
         xq[slot][i] = ld(rx, q * xs);
         dq[slot][i] = ld(rd, q * ds);
-        if (has_z) zq[slot][i] = ld(rz, q * zs);
+        if constexpr (has_z) zq[slot][i] = ld(rz, q * zs);
       }
     };
     // One step, the states in groups with three phases separated by scheduling barriers that
@@ -214,8 +215,8 @@ __global__ __launch_bounds__(128, pscan_min_waves(NS)) void packed_scan_kernel(
         asm volatile("" ::"v"(dsum));  // needed here, not at the end of the unrolled tile
       } else {
         float out = y0 + y1;
-        if (has_z) out *= silu(wid(zr));
-        if (yb) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)vec_bf16_pair(out, 0.0f), ry, yvo, i * ys, 2);
+        if constexpr (has_z) out *= silu(wid(zr));
+        if constexpr (yb) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)vec_bf16_pair(out, 0.0f), ry, yvo, i * ys, 2);
         else __builtin_amdgcn_raw_buffer_store_b32(pscan_u32(out), ry, yvo, i * ys, 2);
       }
     };
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(128, pscan_min_waves(NS)) void packed_scan_kernel(
     rows_load(1);
     int t0 = 0;
     for (; t0 + TS <= len; t0 += TS) {
-#pragma unroll 4
+#pragma unroll 1
       for (int q = 0; q < TS; q += 2 * U) {
         load(1, t0 + q + U);
 #pragma unroll
@@ -335,7 +336,6 @@ static hipError_t run_pscan(const PackedScanArgs& a, const PackedScanPlan& pl, h
   const int64_t widest = std::max({a.sx, a.sd, a.sz, a.dim, (int64_t)1});
   g.piece = (int)std::min<int64_t>((((int64_t)1 << 28) / widest) & ~(int64_t)3, 1 << 28);  // strides <= 2^24: 16 at least
   g.bc_bf16 = a.bc_bf16;
-  g.y_bf16 = a.y_bf16;
   char* ws = static_cast<char*>(a.workspace);
   float* w_end = reinterpret_cast<float*>(ws + pl.off_end);
   float* w_sum = reinterpret_cast<float*>(ws + pl.off_sum);
@@ -344,7 +344,7 @@ static hipError_t run_pscan(const PackedScanArgs& a, const PackedScanPlan& pl, h
   int32_t* w_flag = reinterpret_cast<int32_t*>(ws + pl.off_flag);
   const dim3 block(64u * g.gpb);
   if (pl.chunks > 1) {
-    hipLaunchKernelGGL((packed_scan_kernel<NS, BF16, 1, FL>), dim3((unsigned)((int64_t)g.nblk * (pl.chunks - 1))), block, 0,
+    hipLaunchKernelGGL((packed_scan_kernel<NS, BF16, 1, FL, false, false>), dim3((unsigned)((int64_t)g.nblk * (pl.chunks - 1))), block, 0,
                        stream, (const char*)a.x, (const char*)a.delta, a.A, (const char*)a.B, (const char*)a.C, a.Dsk,
                        (const char*)a.z, a.delta_bias, a.state, a.cu, a.sidx, a.init, (char*)a.y, w_end, w_sum, w_init,
                        w_enter, w_flag, g);
@@ -353,18 +353,23 @@ static hipError_t run_pscan(const PackedScanArgs& a, const PackedScanPlan& pl, h
     e = launch_pscan_carry(a.A, w_end, w_sum, w_flag, w_enter, NS, (int)a.dim, pl.chunks, stream);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((packed_scan_kernel<NS, BF16, 2, FL>), dim3((unsigned)((int64_t)g.nblk * pl.chunks)), block, 0, stream,
-                     (const char*)a.x, (const char*)a.delta, a.A, (const char*)a.B, (const char*)a.C, a.Dsk,
-                     (const char*)a.z, a.delta_bias, a.state, a.cu, a.sidx, a.init, (char*)a.y, w_end, w_sum, w_init,
-                     w_enter, w_flag, g);
+  const dim3 grid((unsigned)((int64_t)g.nblk * pl.chunks));
+#define SSS_PASS2(HZ, YB)                                                                                             \
+  hipLaunchKernelGGL((packed_scan_kernel<NS, BF16, 2, FL, HZ, YB>), grid, block, 0, stream, (const char*)a.x,         \
+                     (const char*)a.delta, a.A, (const char*)a.B, (const char*)a.C, a.Dsk, (const char*)a.z,          \
+                     a.delta_bias, a.state, a.cu, a.sidx, a.init, (char*)a.y, w_end, w_sum, w_init, w_enter, w_flag, g)
+  if (a.z != nullptr && a.y_bf16) SSS_PASS2(true, true);
+  else if (a.z != nullptr) SSS_PASS2(true, false);
+  else if (a.y_bf16) SSS_PASS2(false, true);
+  else SSS_PASS2(false, false);
+#undef SSS_PASS2
   return hipGetLastError();
 }
 
 template <int NS, bool BF16>
 hipError_t run_pscan_front(const PackedScanArgs& a, const PackedScanPlan& pl, hipStream_t stream) {
-  if (a.softplus) return run_pscan<NS, BF16, kFront | kSoftplus>(a, pl, stream);
-  if (a.delta_bias != nullptr) return run_pscan<NS, BF16, kFront>(a, pl, stream);
-  return run_pscan<NS, BF16, 0>(a, pl, stream);
+  // without a bias, kFront adds zero
+  return a.softplus ? run_pscan<NS, BF16, kFront | kSoftplus>(a, pl, stream) : run_pscan<NS, BF16, kFront>(a, pl, stream);
 }
 
 // compiled once per state count (SSS_INST_NS) and once for the host part
