@@ -13,6 +13,7 @@
 // the registers of one wave, of one workgroup of 256, 512 or 1024 lanes, whichever is the
 // smallest that holds it: 8 adjacent elements per lane and piece (16 bytes in bf16), M pieces.
 // Sums are fp32: lanes of a wave by DPP, waves through LDS.
+#include "colsum.h"
 #include "vec.h"
 #include "kernels.h"
 
@@ -434,31 +435,29 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void res_norm_bwd_kernel(
   if (scale != nullptr) put(ds);
 }
 
-// Column sums of `rows` partial rows of `cols` floats, added in their order: 64 columns and 4 row
-// ranges per workgroup, the ranges joined in LDS.  Columns d, D + d, 2D + d go to out0, out1, out2.
-static __global__ __launch_bounds__(256) void norm_sum_kernel(const float* __restrict__ part, float* __restrict__ out0,
-                                                              float* __restrict__ out1, float* __restrict__ out2,
-                                                              int rows, int64_t cols, int D) {
-  __shared__ float lds[256];
-  const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-  const int64_t cc = min(col, cols - 1);
-  const int q = threadIdx.x >> 6;
-  const int per = (rows + 3) / 4;
-  const int r1 = min(rows, (q + 1) * per);
-  float s = 0.0f;
-  for (int r = q * per; r < r1; r += 8) {
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)min(r + i, r1 - 1) * cols + cc];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += r + i < r1 ? v[i] : 0.0f;
-  }
-  lds[threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.x >= 64 || col >= cols) return;
-  s = (lds[threadIdx.x] + lds[threadIdx.x + 64]) + (lds[threadIdx.x + 128] + lds[threadIdx.x + 192]);
-  const int k = (int)(col / D);
-  (k == 0 ? out0 : k == 1 ? out1 : out2)[col - (int64_t)k * D] = s;
+// Parameter gradients from the partials, added in their order: columns d, D + d, 2D + d are those
+// of out0, out1, out2.
+template <int Q>
+static __global__ __launch_bounds__(32 * Q) void norm_sum_kernel(const float* __restrict__ part, float* __restrict__ out0,
+                                                                 float* __restrict__ out1, float* __restrict__ out2,
+                                                                 int rows, int64_t cols, int D) {
+  column_sums<Q>(part, rows, cols, [=](int64_t col, float s) {
+    if (col < D) out0[col] = s;
+    else if (col < 2 * (int64_t)D) out1[col - D] = s;
+    else out2[col - 2 * (int64_t)D] = s;
+  });
+}
+
+static hipError_t launch_norm_sum(const void* part, float* out0, float* out1, float* out2, int rows, int64_t cols,
+                                  int64_t D, hipStream_t stream) {
+  const dim3 grid(colsum_blocks(cols));
+  if (colsum_ranges(rows) == 8)
+    hipLaunchKernelGGL(norm_sum_kernel<8>, grid, dim3(256), 0, stream, (const float*)part, out0, out1, out2, rows, cols,
+                       (int)D);
+  else
+    hipLaunchKernelGGL(norm_sum_kernel<32>, grid, dim3(1024), 0, stream, (const float*)part, out0, out1, out2, rows, cols,
+                       (int)D);
+  return hipGetLastError();
 }
 
 // Lanes per row and pieces per lane for rows of G elements (V = 8; fewer elements: one wave, V = 1).
@@ -553,9 +552,7 @@ static hipError_t gated_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStrea
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t D = a.group * a.groups;
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((D + 63) / 64)), dim3(256), 0, stream, (const float*)a.workspace,
-                     a.dw, (float*)nullptr, (float*)nullptr, pl.part_rows, D, (int)D);
-  return hipGetLastError();
+  return launch_norm_sum(a.workspace, a.dw, nullptr, nullptr, pl.part_rows, D, D, stream);
 }
 
 hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStream_t stream) {
@@ -604,9 +601,7 @@ static hipError_t res_bwd(const ResNormArgs& a, const NormPlan& pl, hipStream_t 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t cols = a.dim * (1 + (POST ? 1 : 0) + (a.scale != nullptr ? 1 : 0));
-  hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream,
-                     (const float*)a.workspace, a.dw, POST ? a.dwp : a.dscale, a.dscale, pl.part_rows, cols, (int)a.dim);
-  return hipGetLastError();
+  return launch_norm_sum(a.workspace, a.dw, POST ? a.dwp : a.dscale, a.dscale, pl.part_rows, cols, a.dim, stream);
 }
 
 template <bool XB, bool HB>

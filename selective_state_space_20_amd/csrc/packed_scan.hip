@@ -393,7 +393,7 @@ SSS_EXTERN_PSCAN(64)
 // crosses: it starts at a chunk with flag 2 and goes on over those with flag 1.  The thread
 // follows the chains that start in its range, past the range's end where they reach further,
 // so that the sequences of a batch are composed in parallel.
-constexpr int kPCarryBatch = 8;
+constexpr int kPCarryBatch = 16;
 static __global__ __launch_bounds__(256) void pscan_carry_kernel(const float* __restrict__ A,
                                                                  const float* __restrict__ ends,
                                                                  const float* __restrict__ sums,
@@ -410,15 +410,24 @@ static __global__ __launch_bounds__(256) void pscan_carry_kernel(const float* __
   bool on = false;
   for (int c0 = r0; c0 < last; c0 += kPCarryBatch) {
     if (c0 >= r1 && !on) return;
-    int fl[kPCarryBatch];
+    int fl[kPCarryBatch], any = 0;
+#pragma unroll
+    for (int i = 0; i < kPCarryBatch; ++i) {
+      fl[i] = c0 + i < last ? flags[c0 + i] : 0;
+      any |= fl[i];
+    }
+    if (any == 0) {  // only short sequences here
+      on = false;
+      continue;
+    }
+    // loaded without regard to the flags, so that all of the batch is in flight together; where
+    // a flag is 0 nothing was written, and nothing is used
     float st[kPCarryBatch], ds[kPCarryBatch];
 #pragma unroll
     for (int i = 0; i < kPCarryBatch; ++i) {
-      const int c = c0 + i;
-      fl[i] = c < last ? flags[c] : 0;
-      const bool use = fl[i] != 0;
-      st[i] = use ? ends[(int64_t)c * per + idx] : 0.0f;
-      ds[i] = use ? sums[(int64_t)c * D + d] : 0.0f;
+      const int64_t c = min(c0 + i, last - 1);
+      st[i] = ends[c * per + idx];
+      ds[i] = sums[c * D + d];
     }
 #pragma unroll
     for (int i = 0; i < kPCarryBatch; ++i) {

@@ -21,6 +21,46 @@ __device__ __forceinline__ uint32_t vec_bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, vec_bf2));
 }
 
+// A row's address, the same in the whole wave, and a lane's byte offset in it: kept apart (a
+// scalar register pair and one vector register), so that an access needs no vector address
+// arithmetic.  Left alone the compiler folds both into a 64-bit vector address per access.
+typedef __attribute__((address_space(1))) char* row_ptr;
+__device__ __forceinline__ row_ptr row_at(const void* base, int64_t bytes) {
+  row_ptr p = (row_ptr)(const_cast<char*>(static_cast<const char*>(base)) + bytes);
+  asm volatile("" : "+s"(p));
+  return p;
+}
+__device__ __forceinline__ uint32_t lane_at(uint32_t off) {
+  asm volatile("" : "+v"(off));
+  return off;
+}
+
+// One access of 2, 4, 8 or 16 bytes through either kind of pointer.  The types are spelled out:
+// as a template argument a type loses its alignment, and the compiler then takes rows that are
+// the same for all lanes through scalar loads, which drop an address's low two bits.
+#define SSS_VEC_ACCESS(NAME, T, PTR, AS)                                    \
+  template <bool NT>                                                        \
+  __device__ __forceinline__ T vec_get##NAME(PTR p) {                       \
+    if constexpr (NT) return __builtin_nontemporal_load((const AS T*)p);    \
+    else return *(const AS T*)p;                                            \
+  }                                                                         \
+  template <bool NT>                                                        \
+  __device__ __forceinline__ void vec_put##NAME(PTR p, T v) {               \
+    if constexpr (NT) __builtin_nontemporal_store(v, (AS T*)p);             \
+    else *(AS T*)p = v;                                                     \
+  }
+#define SSS_VEC_AS1 __attribute__((address_space(1)))
+SSS_VEC_ACCESS(2, uint16_t, char*, )
+SSS_VEC_ACCESS(4, vec_u1, char*, )
+SSS_VEC_ACCESS(8, vec_u2, char*, )
+SSS_VEC_ACCESS(16, vec_u4, char*, )
+SSS_VEC_ACCESS(2, uint16_t, row_ptr, SSS_VEC_AS1)
+SSS_VEC_ACCESS(4, vec_u1, row_ptr, SSS_VEC_AS1)
+SSS_VEC_ACCESS(8, vec_u2, row_ptr, SSS_VEC_AS1)
+SSS_VEC_ACCESS(16, vec_u4, row_ptr, SSS_VEC_AS1)
+#undef SSS_VEC_ACCESS
+#undef SSS_VEC_AS1
+
 template <bool BF16, int V>
 struct Vec {
   static constexpr int ES = BF16 ? 2 : 4;       // bytes per element
@@ -28,22 +68,30 @@ struct Vec {
   static constexpr int ND = VB >= 4 ? VB / 4 : 1;
   uint32_t w[ND];  // raw bits: widened only when read, so that loads stay in flight
 
-  // NT: streamed data that nothing reads again soon
+  // NT: streamed data that nothing reads again soon.  P: a generic pointer, or a row_ptr + offset
   template <bool NT = false>
   __device__ __forceinline__ void load(const void* p) {
+    load_as<NT, char*>(const_cast<char*>(static_cast<const char*>(p)));
+  }
+  template <bool NT = false>
+  __device__ __forceinline__ void load(row_ptr p, uint32_t off) {
+    load_as<NT, row_ptr>(p + off);
+  }
+  template <bool NT, typename P>
+  __device__ __forceinline__ void load_as(P p) {
     if constexpr (VB == 2) {
-      w[0] = NT ? __builtin_nontemporal_load((const uint16_t*)p) : *(const uint16_t*)p;
+      w[0] = vec_get2<NT>(p);
     } else if constexpr (VB == 4) {
-      w[0] = NT ? __builtin_nontemporal_load((const vec_u1*)p) : *(const vec_u1*)p;
+      w[0] = vec_get4<NT>(p);
     } else if constexpr (VB == 8) {
-      const vec_u2 v = NT ? __builtin_nontemporal_load((const vec_u2*)p) : *(const vec_u2*)p;
+      const vec_u2 v = vec_get8<NT>(p);
       w[0] = v.x;
       w[1] = v.y;
     } else {
-      static_assert(VB % 16 == 0 || VB < 16, "vector bytes");
+      static_assert(VB % 16 == 0, "vector bytes");
 #pragma unroll
       for (int i = 0; i < VB / 16; ++i) {
-        const vec_u4 v = NT ? __builtin_nontemporal_load((const vec_u4*)p + i) : *((const vec_u4*)p + i);
+        const vec_u4 v = vec_get16<NT>(p + 16 * i);
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;
         w[4 * i + 2] = v.z;
@@ -80,22 +128,26 @@ struct Vec {
   }
   template <bool NT = false>
   __device__ __forceinline__ void store(void* p) const {
+    store_as<NT, char*>(static_cast<char*>(p));
+  }
+  template <bool NT = false>
+  __device__ __forceinline__ void store(row_ptr p, uint32_t off) const {
+    store_as<NT, row_ptr>(p + off);
+  }
+  template <bool NT, typename P>
+  __device__ __forceinline__ void store_as(P p) const {
     if constexpr (VB == 2) {
-      if constexpr (NT) __builtin_nontemporal_store((uint16_t)w[0], (uint16_t*)p);
-      else *(uint16_t*)p = (uint16_t)w[0];
+      vec_put2<NT>(p, (uint16_t)w[0]);
     } else if constexpr (VB == 4) {
-      if constexpr (NT) __builtin_nontemporal_store(w[0], (vec_u1*)p);
-      else *(vec_u1*)p = w[0];
+      vec_put4<NT>(p, w[0]);
     } else if constexpr (VB == 8) {
       const vec_u2 v = {w[0], w[1]};
-      if constexpr (NT) __builtin_nontemporal_store(v, (vec_u2*)p);
-      else *(vec_u2*)p = v;
+      vec_put8<NT>(p, v);
     } else {
 #pragma unroll
       for (int i = 0; i < VB / 16; ++i) {
         const vec_u4 v = {w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
-        if constexpr (NT) __builtin_nontemporal_store(v, (vec_u4*)p + i);
-        else *((vec_u4*)p + i) = v;
+        vec_put16<NT>(p + 16 * i, v);
       }
     }
   }
@@ -105,12 +157,24 @@ struct Vec {
     if (skip == 0) {
       store<NT>(p);
     } else {
+      part_as(static_cast<char*>(p), skip);
+    }
+  }
+  template <bool NT = false>
+  __device__ __forceinline__ void store_from(row_ptr p, uint32_t off, int skip) const {
+    if (skip == 0) {
+      store<NT>(p, off);
+    } else {
+      part_as(p + off, skip);
+    }
+  }
+  template <typename P>
+  __device__ __forceinline__ void part_as(P p, int skip) const {
 #pragma unroll
-      for (int c = 1; c < V; ++c) {
-        if (c < skip) continue;
-        if constexpr (BF16) ((uint16_t*)p)[c] = (uint16_t)((c & 1) ? w[c >> 1] >> 16 : w[c >> 1]);
-        else ((uint32_t*)p)[c] = w[c];
-      }
+    for (int c = 1; c < V; ++c) {
+      if (c < skip) continue;
+      if constexpr (BF16) vec_put2<false>(p + 2 * c, (uint16_t)((c & 1) ? w[c >> 1] >> 16 : w[c >> 1]));
+      else vec_put4<false>(p + 4 * c, w[c]);
     }
   }
 };
