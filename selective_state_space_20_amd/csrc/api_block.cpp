@@ -34,9 +34,9 @@ int conv_impl(const void* x, int64_t x_stride, const float* weight, const float*
     return SSS_ERR_BAD_DIM;
   if (width < 1 || width > 8 || !dtype_ok(io_dtype)) return SSS_ERR_UNSUPPORTED;
   if (!stride_ok(x_stride, dim)) return SSS_ERR_BAD_DIM;
-  // threads of the launch: 256 per row and 512 channels, or 64 per 32 tokens and 128 channels
+  // threads of the launch: 256 per row and 512 channels, or 64 per 8 tokens and 128 channels
   const double threads = step ? (double)tokens * (double)((dim + 511) / 512) * 256.0
-                              : (double)(tokens / 32 + 1) * (double)((dim + 127) / 128) * 64.0;
+                              : (double)(tokens / 8 + 1) * (double)((dim + 127) / 128) * 64.0;
   if (threads > 2147483647.0) return SSS_ERR_BAD_DIM;
   const int64_t es = dtype_size(io_dtype);
   Regions r;

@@ -195,11 +195,17 @@ ConvBwdPlan plan_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
   ConvBwdPlan pl{};
   const int wide = bf16 ? 4 : 2;
   pl.cpl = dim >= wide ? wide : 1;
-  const int64_t waves = batch * ((dim + 64 * pl.cpl - 1) / (64 * pl.cpl));
-  const int64_t target = (int64_t)std::max(num_cus, 1) * 32;
-  int64_t S = waves >= target ? 1 : (target + waves - 1) / waves;
-  // every segment walks width-1 steps of the next one again and leaves a partial: 64 steps at least
-  S = std::min<int64_t>(S, std::max<int64_t>(1, seqlen / 64));
+  const int64_t per_step = batch * ((dim + 64 * pl.cpl - 1) / (64 * pl.cpl));  // waves per time segment
+  const int64_t cus = std::max(num_cus, 1);
+  // Every segment walks width-1 steps of its neighbours again and leaves a row of partials, so
+  // that segments are as long as six waves per CU allow, up to 192 steps (2 x 8192 x 5120 bf16:
+  // 104 us with 192 steps, 110 with 112, 116 with 48).  Small layers are bound by one wave's walk and
+  // take 32 steps, or 16 or 8 where those would leave most CUs with less than two waves
+  // (3 x 1001 x 777 fp32: 16 us with 32 steps, 24 with 64; 64 x 5120: 9.5 with 8, 15 with 32).
+  auto waves = [&](int64_t steps) { return per_step * ((seqlen + steps - 1) / steps); };
+  const int64_t least = waves(32) >= 2 * cus ? 32 : waves(16) >= 2 * cus ? 16 : 8;
+  const int64_t steps = std::max(least, std::min<int64_t>(192, seqlen * per_step / (6 * cus)));
+  int64_t S = (seqlen + steps - 1) / steps;
   const int forced = env_int("SSS_FORCE_SEGMENTS", 0);
   if (forced > 0) S = std::min<int64_t>(forced, seqlen);
   pl.seg_len = (seqlen + S - 1) / S;

@@ -220,10 +220,14 @@ template <bool BF16>
 constexpr int kPConvCpl = BF16 ? 4 : 2;  // 8 bytes per lane
 
 static int chunk_tokens(int64_t tokens, int64_t groups, int width, int num_cus) {
-  // short-lived waves stream best: aim at 80 per CU (see conv1d.hip), chunks of 32 tokens at least
-  const int64_t target = (int64_t)std::max(num_cus, 1) * 80;
-  const int64_t chunks = std::max<int64_t>(1, target / std::max<int64_t>(1, groups));
-  int64_t k = std::max<int64_t>((tokens + chunks - 1) / chunks, 32);
+  // Short-lived waves stream best: aim at 20 per CU (16384 x 5120: 64.4 us with 20, chunks of
+  // 64 tokens, 67.5 with 40, 75 with 80).  Chunks of 12 tokens at
+  // least, of 8 where those leave less than eight waves per CU (16384 x 1024: 20.0 us with 12,
+  // 20.9 with 8, 22.5 with 32; 512 x 2048: 5.3 us with 8, 6.0 with 12, 9.0 with 32).
+  const int64_t cus = std::max(num_cus, 1);
+  const int64_t chunks = std::max<int64_t>(1, cus * 20 / std::max<int64_t>(1, groups));
+  const int64_t least = groups * ((tokens + 7) / 8) < cus * 8 ? 8 : 12;
+  int64_t k = std::max<int64_t>((tokens + chunks - 1) / chunks, least);
   const int forced = env_int("SSS_FORCE_SEGMENTS", 0);
   if (forced > 0) k = std::max<int64_t>((tokens + forced - 1) / forced, width);
   return (int)std::max<int64_t>(k, width);  // a sequence's first width-1 tokens reach one chunk further at most

@@ -461,16 +461,21 @@ static size_t pscan_align(size_t v) { return (v + 255) / 256 * 256; }
 PackedScanPlan plan_packed_scan(int64_t tokens, int64_t dim, int64_t dstate, int num_cus) {
   PackedScanPlan pl{};
   const int64_t groups = (dim + 63) / 64;
+  // Waves (one per channel group and chunk) that the device holds at once in pass 2.  All waves
+  // take about as long, so that a launch of one or two full rounds wastes nothing, and one of
+  // a little more than a round nearly half: 9001 tokens x 2048 x 16 takes 135 us in 126 chunks (one
+  // round), 153 in 141; 32768 x 5120 x 16 975 us in 51 (one), 906 in 102 (two), 1051 in 52.
   const int64_t simds = (int64_t)std::max(num_cus, 1) * 4;
-  // as the dense scan's segments: about 20 waves per SIMD, chunks of 64 tokens at least, of 32
-  // where even those would leave SIMDs without a wave
-  int64_t S = std::max<int64_t>(1, (simds * 20 + groups / 2) / groups);
-  const int64_t min_len = groups * std::max<int64_t>(1, tokens / 64) >= simds ? 64 : 32;
-  S = std::min<int64_t>(S, std::max<int64_t>(1, tokens / min_len));
+  const int64_t round = std::max<int64_t>(1, simds * pscan_min_waves((int)dstate) / groups);  // chunks
+  // two rounds of chunks of 64 tokens at least (16384 x 1024 x 8: 90 us in one round of 64 tokens,
+  // 98 in two of 32), else one of 32; 16 where 32 would leave most SIMDs idle (300 x 1024 x 16:
+  // 23 us, 31 with 32)
+  int64_t S = tokens >= 2 * round * 64 ? 2 * round : round;
+  const int64_t shortest = groups * ((tokens + 31) / 32) * 2 >= simds ? 32 : 16;
+  S = std::min<int64_t>(S, std::max<int64_t>(1, tokens / shortest));
   const int forced = env_int("SSS_FORCE_SEGMENTS", 0);
   if (forced > 0) S = std::min<int64_t>(forced, tokens);
-  int64_t K = std::max<int64_t>(1, (tokens + S - 1) / S);
-  if (forced <= 0) K = (K + 15) / 16 * 16;
+  const int64_t K = std::max<int64_t>(1, (tokens + S - 1) / S);
   pl.K = K;
   pl.chunks = (int)((tokens + K - 1) / K);
   if (pl.chunks > 1) {
