@@ -11,42 +11,75 @@ from . import _lib
 from ._lib import SSS_BF16, SSS_DELTA_SOFTPLUS, SSS_F32, SSS_NORM_BEFORE_GATE, SSSError, load
 
 
-def _rows(t, name, dtype, rows, dim, device):
-    """Checks a (rows, dim) tensor whose rows may be strided; returns (pointer, row stride)."""
+_torch = None
+
+
+def torch_():
+    """torch, imported with the first call (as the library is), not with the package."""
+    global _torch
+    if _torch is None:
+        load()
+        import torch
+        _torch = torch
+    return _torch
+
+
+# The checks below take one combined condition where all is well, since a decode step on small
+# batches is as long as its call; what is wrong is found out afterwards.
+def _refuse(t, name, dtype, shape, index):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.ndim != 2 or t.shape[0] != rows or t.shape[1] != dim:
-        raise ValueError(f"{name} must have shape {(rows, dim)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU ({device}), got {t.device}")
-    s0, s1 = t.stride()
-    if s1 != 1 and dim != 1:
-        raise ValueError(f"{name}: the elements of a row must be adjacent, got strides {(s0, s1)}")
-    if rows > 1 and s0 < dim:
-        raise ValueError(f"{name}: rows must not overlap, got strides {(s0, s1)}")
-    return t.data_ptr(), max(s0, dim)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be on a GPU ({f'cuda:{index}' if index >= 0 else 'that of x'}), got {t.device}")
 
 
-def _dense(t, name, dtype, shape, device):
+def _rows(t, name, dtype, rows, dim, index):
+    """Checks a (rows, dim) tensor whose rows may be strided; returns (pointer, row stride)."""
+    if t.dtype is dtype and t.shape == (rows, dim) and t.get_device() == index >= 0:
+        s0, s1 = t.stride()
+        if s1 == 1 and s0 >= dim:
+            return t.data_ptr(), s0
+        if (s1 == 1 or dim == 1) and (rows <= 1 or s0 >= dim):  # sizes of one: strides without a meaning
+            return t.data_ptr(), max(s0, dim)
+        raise ValueError(f"{name}: rows must be {dim} adjacent elements and not overlap, got strides {(s0, s1)}")
+    _refuse(t, name, dtype, (rows, dim), index)
+
+
+def _dense(t, name, dtype, shape, index):
     """Checks a contiguous tensor on the call's GPU; returns its pointer (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU ({device}), got {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, index)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _out(out, name, like, dtype, shape, index):
+    """The given output, checked, or a new one on like's GPU; returns (tensor, pointer)."""
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+        return out, out.data_ptr()
+    return out, _dense(out, name, dtype, shape, index)
+
+
+def _scratch(workspace, nbytes, like):
+    """The given workspace, checked, or a new one; returns (tensor to keep, pointer, bytes)."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, 0
+        workspace = like.new_empty((nbytes,), dtype=_torch.uint8)
+        return workspace, workspace.data_ptr(), nbytes
+    return (workspace, *_lib._workspace(workspace, like.device))
 
 
 def _code(dtype, name):
-    import torch
-    if dtype == torch.bfloat16:
+    torch = torch_()
+    if dtype is torch.bfloat16:
         return SSS_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return SSS_F32
     raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
 
@@ -57,31 +90,29 @@ def _two_d(t, name):
     return t.shape
 
 
-def _stream(stream, device):
-    if stream is not None:
-        return stream
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+def _stream(stream, index):
+    """The given stream, or the current one of the call's GPU (its handle without a Stream object)."""
+    return stream if stream is not None else _torch._C._cuda_getCurrentRawStream(index)
 
 
-def _cache(state, name, dtype, tail, device):
+def _cache(state, name, dtype, tail, index):
     """A (slots, *tail) cache; returns (pointer, slots)."""
     if state is None:
         return 0, 0
     if state.ndim != 1 + len(tail) or state.shape[0] < 1:
         raise ValueError(f"{name} must have shape (slots, {', '.join(map(str, tail))}), got {tuple(state.shape)}")
     slots = state.shape[0]
-    return _dense(state, name, dtype, (slots, *tail), device), slots
+    return _dense(state, name, dtype, (slots, *tail), index), slots
 
 
-def _sequences(cu_seqlens, state_indices, has_initial, state, slots, device):
+def _sequences(cu_seqlens, state_indices, has_initial, state, slots, index):
     """Checks what describes a packed batch; returns (nseq, cu, indices, initial) with pointers."""
-    import torch
+    torch = torch_()
     if cu_seqlens.ndim != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError(f"cu_seqlens must be 1-D with one entry more than sequences, got {tuple(cu_seqlens.shape)}")
     nseq = cu_seqlens.shape[0] - 1
-    cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), device)
-    idx = _dense(state_indices, "state_indices", torch.int32, (nseq,), device)
+    cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), index)
+    idx = _dense(state_indices, "state_indices", torch.int32, (nseq,), index)
     if state is not None and state_indices is None and nseq > slots:
         raise ValueError(f"{nseq} sequences need as many slots or state_indices, the cache has {slots}")
     if state is None and has_initial is not None:
@@ -90,7 +121,7 @@ def _sequences(cu_seqlens, state_indices, has_initial, state, slots, device):
     if has_initial is not None:
         if has_initial.dtype not in (torch.bool, torch.uint8):
             raise ValueError(f"has_initial must be bool or uint8, got {has_initial.dtype}")
-        ini = _dense(has_initial, "has_initial", has_initial.dtype, (nseq,), device)
+        ini = _dense(has_initial, "has_initial", has_initial.dtype, (nseq,), index)
     return nseq, cu, idx, ini
 
 
@@ -103,22 +134,21 @@ def causal_conv1d_packed_fwd(x, weight, bias=None, *, cu_seqlens, conv_state=Non
     each sequence's last width-1 inputs (updated in place) in slot state_indices[s] (int32; None:
     slot s; -1: none); has_initial (nseq) bool marks the sequences that continue their slot.
     Rows outside every sequence are left as they are in ``out``."""
-    import torch
-    dev = x.device
+    torch = torch_()
+    gpu = x.get_device()
     tokens, dim = _two_d(x, "x")
     code = _code(x.dtype, "x")
-    xp, xs = _rows(x, "x", x.dtype, tokens, dim, dev)
+    xp, xs = _rows(x, "x", x.dtype, tokens, dim, gpu)
     width = _two_d(weight, "weight")[1]
-    wp = _dense(weight, "weight", torch.float32, (dim, width), dev)
-    bp = _dense(bias, "bias", torch.float32, (dim,), dev)
-    sp, slots = _cache(conv_state, "conv_state", x.dtype, (width - 1, dim), dev)
-    nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, conv_state, slots, dev)
-    o = out if out is not None else torch.empty((tokens, dim), dtype=x.dtype, device=dev)
-    op = _dense(o, "out", x.dtype, (tokens, dim), dev)
+    wp = _dense(weight, "weight", torch.float32, (dim, width), gpu)
+    bp = _dense(bias, "bias", torch.float32, (dim,), gpu)
+    sp, slots = _cache(conv_state, "conv_state", x.dtype, (width - 1, dim), gpu)
+    nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, conv_state, slots, gpu)
+    o, op = _out(out, "out", x, x.dtype, (tokens, dim), gpu)
     if tokens == 0:
         return o
     rc = load().causal_conv1d_packed_fwd(xp, xs, wp, bp, sp, cu, idx, ini, op, tokens, nseq, slots if sp else 0, dim,
-                                         width, code, int(bool(silu)), _stream(stream, dev))
+                                         width, code, int(bool(silu)), _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_packed_fwd")
     return o
@@ -130,24 +160,23 @@ def causal_conv1d_update(x, weight, bias=None, *, conv_state, state_indices=None
     x (batch, dim), rows may be strided; conv_state (slots, width-1, dim) in x's dtype, updated
     in place, row b's in slot state_indices[b] (int32; None: slot b; -1: none, the row starts
     from zeros and keeps nothing)."""
-    import torch
-    dev = x.device
+    torch = torch_()
+    gpu = x.get_device()
     batch, dim = _two_d(x, "x")
     code = _code(x.dtype, "x")
-    xp, xs = _rows(x, "x", x.dtype, batch, dim, dev)
+    xp, xs = _rows(x, "x", x.dtype, batch, dim, gpu)
     width = _two_d(weight, "weight")[1]
-    wp = _dense(weight, "weight", torch.float32, (dim, width), dev)
-    bp = _dense(bias, "bias", torch.float32, (dim,), dev)
-    sp, slots = _cache(conv_state, "conv_state", x.dtype, (width - 1, dim), dev)
-    idx = _dense(state_indices, "state_indices", torch.int32, (batch,), dev)
+    wp = _dense(weight, "weight", torch.float32, (dim, width), gpu)
+    bp = _dense(bias, "bias", torch.float32, (dim,), gpu)
+    sp, slots = _cache(conv_state, "conv_state", x.dtype, (width - 1, dim), gpu)
+    idx = _dense(state_indices, "state_indices", torch.int32, (batch,), gpu)
     if state_indices is None and batch > slots:
         raise ValueError(f"{batch} rows need as many slots or state_indices, the cache has {slots}")
-    o = out if out is not None else torch.empty((batch, dim), dtype=x.dtype, device=dev)
-    op = _dense(o, "out", x.dtype, (batch, dim), dev)
+    o, op = _out(out, "out", x, x.dtype, (batch, dim), gpu)
     if batch == 0:
         return o
     rc = load().causal_conv1d_update(xp, xs, wp, bp, sp, idx, op, batch, slots, dim, width, code, int(bool(silu)),
-                                     _stream(stream, dev))
+                                     _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_update")
     return o
@@ -157,14 +186,12 @@ def causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, io_dtype=SSS_BF1
     return int(load().causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, io_dtype, device))
 
 
-def _blocks(t, name, shape, device):
+def _blocks(t, name, dtype, shape, index):
     """Checks a (batch, rows, dim) tensor whose rows and batch entries may be strided; returns
     (pointer, batch stride, row stride)."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU ({device}), got {t.device}")
-    batch, rows, dim = shape
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0:
+        _refuse(t, name, dtype, shape, index)
+    _, rows, dim = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and dim != 1) or (rows > 1 and s1 < dim):
         raise ValueError(f"{name}: rows must be {dim} adjacent elements, got strides {(s0, s1, s2)}")
@@ -178,8 +205,8 @@ def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, worksp
     seqlen, dim) float32 or x's dtype, contiguous.  Returns a dict of dx (x's dtype, or that of
     the given ``dx`` tensor: float32 or x's dtype, strided or not), dweight (dim, width) and,
     with a bias, dbias (dim), both float32."""
-    import torch
-    dev = x.device
+    torch = torch_()
+    gpu = x.get_device()
     if x.ndim != 3:
         raise ValueError(f"x must be (batch, seqlen, dim), got shape {tuple(x.shape)}")
     batch, seqlen, dim = x.shape
@@ -187,25 +214,26 @@ def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, worksp
     width = _two_d(weight, "weight")[1]
     if dout.dtype not in (torch.float32, x.dtype):
         raise ValueError(f"dout must be float32 or {x.dtype}, got {dout.dtype}")
-    xp, xb, xr = _blocks(x, "x", (batch, seqlen, dim), dev)
-    wp = _dense(weight, "weight", torch.float32, (dim, width), dev)
-    bp = _dense(bias, "bias", torch.float32, (dim,), dev)
-    dp = _dense(dout, "dout", dout.dtype, (batch, seqlen, dim), dev)
-    g = {"dx": dx if dx is not None else torch.empty((batch, seqlen, dim), dtype=x.dtype, device=dev),
-         "dweight": torch.empty((dim, width), dtype=torch.float32, device=dev)}
-    if g["dx"].dtype not in (torch.float32, x.dtype):
-        raise ValueError(f"dx must be float32 or {x.dtype}, got {g['dx'].dtype}")
-    gp, gb, gr = _blocks(g["dx"], "dx", (batch, seqlen, dim), dev)
+    xp, xb, xr = _blocks(x, "x", x.dtype, (batch, seqlen, dim), gpu)
+    wp = _dense(weight, "weight", torch.float32, (dim, width), gpu)
+    bp = _dense(bias, "bias", torch.float32, (dim,), gpu)
+    dp = _dense(dout, "dout", dout.dtype, (batch, seqlen, dim), gpu)
+    if dx is None:
+        dx = x.new_empty((batch, seqlen, dim))
+        gp, gb, gr = dx.data_ptr(), seqlen * dim, dim
+    else:
+        if dx.dtype not in (torch.float32, x.dtype):
+            raise ValueError(f"dx must be float32 or {x.dtype}, got {dx.dtype}")
+        gp, gb, gr = _blocks(dx, "dx", dx.dtype, (batch, seqlen, dim), gpu)
+    g = {"dx": dx, "dweight": x.new_empty((dim, width), dtype=torch.float32)}
     if bias is not None:
-        g["dbias"] = torch.empty((dim,), dtype=torch.float32, device=dev)
-    if workspace is None:
-        n = causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, code, dev.index or 0)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-    wsp, wsn = _lib._workspace(workspace, dev)
+        g["dbias"] = x.new_empty((dim,), dtype=torch.float32)
+    need = causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, code, gpu) if workspace is None else 0
+    workspace, wsp, wsn = _scratch(workspace, need, x)
     rc = load().causal_conv1d_bwd(xp, xb, xr, wp, bp, dp, gp, gb, gr, g["dweight"].data_ptr(),
                                   g["dbias"].data_ptr() if bias is not None else 0, batch, seqlen, dim, width, code,
-                                  _code(dout.dtype, "dout"), _code(g["dx"].dtype, "dx"), int(bool(silu)), wsp, wsn,
-                                  _stream(stream, dev))
+                                  _code(dout.dtype, "dout"), _code(dx.dtype, "dx"), int(bool(silu)), wsp, wsn,
+                                  _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_bwd")
     return g
@@ -213,21 +241,21 @@ def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, worksp
 
 def _scan_operands(x, delta, A, B, C, D, z, delta_bias):
     """The scan's operands, checked, as the leading arguments of the C calls."""
-    import torch
-    dev = x.device
+    torch = torch_()
+    gpu = x.get_device()
     rows, dim = _two_d(x, "x")
     code = _code(x.dtype, "x")
     n = _two_d(A, "A")[1]
     bc = _code(B.dtype, "B")
-    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
-    dp, ds = _rows(delta, "delta", x.dtype, rows, dim, dev)
-    Ap = _dense(A, "A", torch.float32, (dim, n), dev)
-    Bp, bs = _rows(B, "B", B.dtype, rows, n, dev)
-    Cp, cs = _rows(C, "C", B.dtype, rows, n, dev)
-    zp, zs = _rows(z, "z", x.dtype, rows, dim, dev) if z is not None else (0, 0)
-    Dp = _dense(D, "D", torch.float32, (dim,), dev)
-    bp = _dense(delta_bias, "delta_bias", torch.float32, (dim,), dev)
-    return (xp, xs, dp, ds, Ap, Bp, bs, Cp, cs, Dp, zp, zs, bp), rows, dim, n, code, bc, dev
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, gpu)
+    dp, ds = _rows(delta, "delta", x.dtype, rows, dim, gpu)
+    Ap = _dense(A, "A", torch.float32, (dim, n), gpu)
+    Bp, bs = _rows(B, "B", B.dtype, rows, n, gpu)
+    Cp, cs = _rows(C, "C", B.dtype, rows, n, gpu)
+    zp, zs = _rows(z, "z", x.dtype, rows, dim, gpu) if z is not None else (0, 0)
+    Dp = _dense(D, "D", torch.float32, (dim,), gpu)
+    bp = _dense(delta_bias, "delta_bias", torch.float32, (dim,), gpu)
+    return (xp, xs, dp, ds, Ap, Bp, bs, Cp, cs, Dp, zp, zs, bp), rows, dim, n, code, bc, gpu
 
 
 def selective_scan_packed_fwd_workspace_size(tokens, dim, dstate, device=0) -> int:
@@ -245,21 +273,19 @@ def selective_scan_packed_fwd(x, delta, A, B, C, D=None, z=None, *, cu_seqlens, 
     state (updated in place) in slot state_indices[s] (int32; None: slot s; -1: none);
     has_initial (nseq) bool marks the sequences that continue their slot.  Rows outside every
     sequence are left as they are in ``out``."""
-    import torch
-    ops, tokens, dim, n, code, bc, dev = _scan_operands(x, delta, A, B, C, D, z, delta_bias)
-    sp, slots = _cache(state, "state", torch.float32, (dim, n), dev)
-    nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, state, slots, dev)
-    y = out if out is not None else torch.empty((tokens, dim), dtype=torch.float32, device=dev)
-    yc = _code(y.dtype, "out")
-    yp = _dense(y, "out", y.dtype, (tokens, dim), dev)
+    torch = torch_()
+    ops, tokens, dim, n, code, bc, gpu = _scan_operands(x, delta, A, B, C, D, z, delta_bias)
+    sp, slots = _cache(state, "state", torch.float32, (dim, n), gpu)
+    nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, state, slots, gpu)
+    yd = torch.float32 if out is None else out.dtype
+    yc = _code(yd, "out")
+    y, yp = _out(out, "out", x, yd, (tokens, dim), gpu)
     if tokens == 0:
         return y
-    if workspace is None:
-        nb = selective_scan_packed_fwd_workspace_size(tokens, dim, n, dev.index or 0)
-        workspace = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    wsp, wsn = _lib._workspace(workspace, dev)
+    need = selective_scan_packed_fwd_workspace_size(tokens, dim, n, gpu) if workspace is None else 0
+    workspace, wsp, wsn = _scratch(workspace, need, x)
     rc = load().selective_scan_packed_fwd(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, cu, idx, ini, yp,
-                                          tokens, nseq, slots, dim, n, code, bc, yc, wsp, wsn, _stream(stream, dev))
+                                          tokens, nseq, slots, dim, n, code, bc, yc, wsp, wsn, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "selective_scan_packed_fwd")
     return y
@@ -272,19 +298,19 @@ def selective_state_update_slots(x, delta, A, B, C, D=None, z=None, *, state, st
     Operands as selective_scan_packed_fwd with one row per request; state (slots, dim, dstate)
     float32 updated in place, row b's in slot state_indices[b] (int32; None: slot b; -1: none, the
     row starts from zero and keeps nothing)."""
-    import torch
-    ops, batch, dim, n, code, bc, dev = _scan_operands(x, delta, A, B, C, D, z, delta_bias)
-    sp, slots = _cache(state, "state", torch.float32, (dim, n), dev)
-    idx = _dense(state_indices, "state_indices", torch.int32, (batch,), dev)
+    torch = torch_()
+    ops, batch, dim, n, code, bc, gpu = _scan_operands(x, delta, A, B, C, D, z, delta_bias)
+    sp, slots = _cache(state, "state", torch.float32, (dim, n), gpu)
+    idx = _dense(state_indices, "state_indices", torch.int32, (batch,), gpu)
     if state_indices is None and batch > slots:
         raise ValueError(f"{batch} rows need as many slots or state_indices, the cache has {slots}")
-    y = out if out is not None else torch.empty((batch, dim), dtype=torch.float32, device=dev)
-    yc = _code(y.dtype, "out")
-    yp = _dense(y, "out", y.dtype, (batch, dim), dev)
+    yd = torch.float32 if out is None else out.dtype
+    yc = _code(yd, "out")
+    y, yp = _out(out, "out", x, yd, (batch, dim), gpu)
     if batch == 0:
         return y
     rc = load().selective_state_update_slots(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, idx, yp, batch,
-                                             slots, dim, n, code, bc, yc, _stream(stream, dev))
+                                             slots, dim, n, code, bc, yc, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "selective_state_update_slots")
     return y
@@ -305,23 +331,22 @@ def rms_norm_gated_fwd(x, weight, z=None, *, eps=1e-5, group_size=None, norm_bef
     x (rows, dim) float32 or bfloat16 (the scan's output), z (rows, dim) float32 or bfloat16, rows
     may be strided; weight (dim) float32.  Returns out (rows, dim) in z's dtype (x's without z),
     and with return_rstd the (rows, groups) float32 factors that rms_norm_gated_bwd takes."""
-    import torch
-    dev = x.device
+    torch = torch_()
+    gpu = x.get_device()
     rows, dim = _two_d(x, "x")
     xc = _code(x.dtype, "x")
     g = _group(dim, group_size)
-    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, gpu)
     od = z.dtype if z is not None else x.dtype
     oc = _code(od, "z")
-    zp, zs = _rows(z, "z", od, rows, dim, dev) if z is not None else (0, 0)
-    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
-    o = out if out is not None else torch.empty((rows, dim), dtype=od, device=dev)
-    op = _dense(o, "out", od, (rows, dim), dev)
-    rstd = torch.empty((rows, dim // g), dtype=torch.float32, device=dev) if return_rstd else None
+    zp, zs = _rows(z, "z", od, rows, dim, gpu) if z is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
+    o, op = _out(out, "out", x, od, (rows, dim), gpu)
+    rstd = x.new_empty((rows, dim // g), dtype=torch.float32) if return_rstd else None
     if rows > 0:
         rc = load().rms_norm_gated_fwd(xp, xs, wp, zp, zs, op, rstd.data_ptr() if return_rstd else 0, rows, dim, g,
                                        float(eps), SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc,
-                                       _stream(stream, dev))
+                                       _stream(stream, gpu))
         if rc != 0:
             raise SSSError(rc, "rms_norm_gated_fwd")
     return (o, rstd) if return_rstd else o
@@ -336,31 +361,32 @@ def rms_norm_gated_bwd(dout, x, weight, z=None, *, rstd, group_size=None, norm_b
     """Gradients of sum(dout * rms_norm_gated_fwd(...)): a dict of dx (x's dtype), dz (z's dtype,
     with z; into the given ``dz``, strided or not) and dweight float32.  dout (rows, dim) in the
     forward output's dtype, contiguous; rstd as the forward returned it."""
-    import torch
-    dev = x.device
+    torch = torch_()
+    gpu = x.get_device()
     rows, dim = _two_d(x, "x")
     xc = _code(x.dtype, "x")
     g = _group(dim, group_size)
     od = z.dtype if z is not None else x.dtype
     oc = _code(od, "z")
-    dp = _dense(dout, "dout", od, (rows, dim), dev)
-    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
-    zp, zs = _rows(z, "z", od, rows, dim, dev) if z is not None else (0, 0)
-    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
-    rp = _dense(rstd, "rstd", torch.float32, (rows, dim // g), dev)
-    res = {"dx": torch.empty((rows, dim), dtype=x.dtype, device=dev),
-           "dweight": torch.empty((dim,), dtype=torch.float32, device=dev)}
+    dp = _dense(dout, "dout", od, (rows, dim), gpu)
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, gpu)
+    zp, zs = _rows(z, "z", od, rows, dim, gpu) if z is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
+    rp = _dense(rstd, "rstd", torch.float32, (rows, dim // g), gpu)
+    res = {"dx": x.new_empty((rows, dim)), "dweight": x.new_empty((dim,), dtype=torch.float32)}
     gp, gs = 0, 0
     if z is not None:
-        res["dz"] = dz if dz is not None else torch.empty((rows, dim), dtype=od, device=dev)
-        gp, gs = _rows(res["dz"], "dz", od, rows, dim, dev)
-    if workspace is None:
-        workspace = torch.empty(rms_norm_gated_bwd_workspace_size(rows, dim, g, dev.index or 0), dtype=torch.uint8,
-                                device=dev)
-    wsp, wsn = _lib._workspace(workspace, dev)
+        if dz is None:
+            res["dz"] = x.new_empty((rows, dim), dtype=od)
+            gp, gs = res["dz"].data_ptr(), dim
+        else:
+            res["dz"] = dz
+            gp, gs = _rows(dz, "dz", od, rows, dim, gpu)
+    need = rms_norm_gated_bwd_workspace_size(rows, dim, g, gpu) if workspace is None else 0
+    workspace, wsp, wsn = _scratch(workspace, need, x)
     rc = load().rms_norm_gated_bwd(dp, xp, xs, wp, zp, zs, rp, res["dx"].data_ptr(), gp, gs, res["dweight"].data_ptr(),
                                    rows, dim, g, SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc, wsp, wsn,
-                                   _stream(stream, dev))
+                                   _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "rms_norm_gated_bwd")
     return res
@@ -375,31 +401,29 @@ def rms_norm_residual_fwd(x, weight, residual=None, *, post_weight=None, scale=N
     strided; weight, post_weight, scale (dim) float32.  Returns (out in x's dtype, residual_out in
     the residual's dtype, float32 without one), and with return_rstd also the (rows,) float32
     factors rstd and rstd_post (None without post_weight).  residual_out may be the residual."""
-    import torch
-    dev = x.device
+    torch = torch_()
+    gpu = x.get_device()
     rows, dim = _two_d(x, "x")
     xc = _code(x.dtype, "x")
     hd = (residual.dtype if residual is not None else residual_out.dtype if residual_out is not None
           else torch.float32)
     hc = _code(hd, "residual")
-    xp, xs = _rows(x, "x", x.dtype, rows, dim, dev)
-    hp, hs = _rows(residual, "residual", hd, rows, dim, dev) if residual is not None else (0, 0)
-    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
-    pp = _dense(post_weight, "post_weight", torch.float32, (dim,), dev)
-    sp = _dense(scale, "scale", torch.float32, (dim,), dev)
-    o = out if out is not None else torch.empty((rows, dim), dtype=x.dtype, device=dev)
-    op = _dense(o, "out", x.dtype, (rows, dim), dev)
-    h = residual_out if residual_out is not None else torch.empty((rows, dim), dtype=hd, device=dev)
-    ho = _dense(h, "residual_out", hd, (rows, dim), dev)
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, gpu)
+    hp, hs = _rows(residual, "residual", hd, rows, dim, gpu) if residual is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
+    pp = _dense(post_weight, "post_weight", torch.float32, (dim,), gpu)
+    sp = _dense(scale, "scale", torch.float32, (dim,), gpu)
+    o, op = _out(out, "out", x, x.dtype, (rows, dim), gpu)
+    h, ho = _out(residual_out, "residual_out", x, hd, (rows, dim), gpu)
     rstd = rstd_post = None
     if return_rstd:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
-        rstd_post = torch.empty((rows,), dtype=torch.float32, device=dev) if post_weight is not None else None
+        rstd = x.new_empty((rows,), dtype=torch.float32)
+        rstd_post = x.new_empty((rows,), dtype=torch.float32) if post_weight is not None else None
     if rows > 0:
         rc = load().rms_norm_residual_fwd(xp, xs, hp, hs, pp, sp, wp, op, ho,
                                           0 if rstd_post is None else rstd_post.data_ptr(),
                                           0 if rstd is None else rstd.data_ptr(), rows, dim, float(alpha), float(eps),
-                                          xc, hc, _stream(stream, dev))
+                                          xc, hc, _stream(stream, gpu))
         if rc != 0:
             raise SSSError(rc, "rms_norm_residual_fwd")
     return (o, h, rstd, rstd_post) if return_rstd else (o, h)
@@ -417,8 +441,8 @@ def rms_norm_residual_bwd(dout, dresidual_out=None, *, residual_out, weight, rst
     contiguous; rstd, rstd_post as the forward returned them; x is needed with post_weight or
     scale.  Returns a dict of dx (x's dtype), dresidual (the residual's, unless not wanted),
     dweight, and dpost_weight / dscale with post_weight / scale, float32."""
-    import torch
-    dev = dout.device
+    torch = torch_()
+    gpu = dout.get_device()
     rows, dim = _two_d(dout, "dout")
     xd, hd = dout.dtype, residual_out.dtype
     xc, hc = _code(xd, "dout"), _code(hd, "residual_out")
@@ -426,31 +450,29 @@ def rms_norm_residual_bwd(dout, dresidual_out=None, *, residual_out, weight, rst
         raise ValueError("x is needed for the gradients through post_weight or scale")
     if post_weight is not None and rstd_post is None:
         raise ValueError("rstd_post is needed with post_weight")
-    dp = _dense(dout, "dout", xd, (rows, dim), dev)
-    ep = _dense(dresidual_out, "dresidual_out", hd, (rows, dim), dev)
-    hp = _dense(residual_out, "residual_out", hd, (rows, dim), dev)
-    xp, xs = _rows(x, "x", xd, rows, dim, dev) if x is not None else (0, 0)
-    wp = _dense(weight, "weight", torch.float32, (dim,), dev)
-    pp = _dense(post_weight, "post_weight", torch.float32, (dim,), dev)
-    sp = _dense(scale, "scale", torch.float32, (dim,), dev)
-    rp = _dense(rstd, "rstd", torch.float32, (rows,), dev)
-    rpp = _dense(rstd_post, "rstd_post", torch.float32, (rows,), dev) if post_weight is not None else 0
-    vec = lambda: torch.empty((dim,), dtype=torch.float32, device=dev)
-    res = {"dx": torch.empty((rows, dim), dtype=xd, device=dev), "dweight": vec()}
+    dp = _dense(dout, "dout", xd, (rows, dim), gpu)
+    ep = _dense(dresidual_out, "dresidual_out", hd, (rows, dim), gpu)
+    hp = _dense(residual_out, "residual_out", hd, (rows, dim), gpu)
+    xp, xs = _rows(x, "x", xd, rows, dim, gpu) if x is not None else (0, 0)
+    wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
+    pp = _dense(post_weight, "post_weight", torch.float32, (dim,), gpu)
+    sp = _dense(scale, "scale", torch.float32, (dim,), gpu)
+    rp = _dense(rstd, "rstd", torch.float32, (rows,), gpu)
+    rpp = _dense(rstd_post, "rstd_post", torch.float32, (rows,), gpu) if post_weight is not None else 0
+    vec = lambda: dout.new_empty((dim,), dtype=torch.float32)
+    res = {"dx": dout.new_empty((rows, dim)), "dweight": vec()}
     if want_dresidual:
-        res["dresidual"] = torch.empty((rows, dim), dtype=hd, device=dev)
+        res["dresidual"] = dout.new_empty((rows, dim), dtype=hd)
     if post_weight is not None:
         res["dpost_weight"] = vec()
     if scale is not None:
         res["dscale"] = vec()
     ptr = lambda k: res[k].data_ptr() if k in res else 0
-    if workspace is None:
-        workspace = torch.empty(rms_norm_residual_bwd_workspace_size(rows, dim, dev.index or 0), dtype=torch.uint8,
-                                device=dev)
-    wsp, wsn = _lib._workspace(workspace, dev)
+    need = rms_norm_residual_bwd_workspace_size(rows, dim, gpu) if workspace is None else 0
+    workspace, wsp, wsn = _scratch(workspace, need, dout)
     rc = load().rms_norm_residual_bwd(dp, ep, xp, xs, hp, pp, sp, wp, rpp, rp, ptr("dx"), ptr("dresidual"),
                                       ptr("dweight"), ptr("dpost_weight"), ptr("dscale"), rows, dim, float(alpha), xc,
-                                      hc, wsp, wsn, _stream(stream, dev))
+                                      hc, wsp, wsn, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "rms_norm_residual_bwd")
     return res
