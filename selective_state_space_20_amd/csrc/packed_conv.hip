@@ -13,7 +13,7 @@
 
 namespace sss {
 
-constexpr int kPConvU = 2;  // steps per load batch (16384 x 5120: 68 us; 4 steps 70, 8 steps 72)
+constexpr int kPConvU = 2;  // steps per load batch (4 and 8 measured within 1%)
 
 struct PConvGeo {
   int64_t x_stride;  // elements between tokens of x
@@ -141,10 +141,10 @@ __global__ __launch_bounds__(64) void packed_conv_kernel(const char* __restrict_
       }
       R r;
       r.set(o);
-      // cached: what follows the convolution reads it back (and it is the faster policy: 72 us
-      // against 77 non-temporal on 16384 x 5120)
-      if constexpr (RAGGED) r.store_from(row_at(ob, (int64_t)i * orow), lane_at(lo_), skip);
-      else r.store(row_at(ob, (int64_t)i * orow), lane_at(lo_));
+      // non-temporal both ways: 75 us on 16384 x 5120 (4.5 TB/s), 78 with cached stores, 79 with
+      // cached loads
+      if constexpr (RAGGED) r.template store_from<true>(row_at(ob, (int64_t)i * orow), lane_at(lo_), skip);
+      else r.template store<true>(row_at(ob, (int64_t)i * orow), lane_at(lo_));
     };
     load(0, 0);
     int t0 = 0;
@@ -220,12 +220,12 @@ template <bool BF16>
 constexpr int kPConvCpl = BF16 ? 4 : 2;  // 8 bytes per lane
 
 static int chunk_tokens(int64_t tokens, int64_t groups, int width, int num_cus) {
-  // Short-lived waves stream best: aim at 20 per CU (16384 x 5120: 64.4 us with 20, chunks of
-  // 64 tokens, 67.5 with 40, 75 with 80).  Chunks of 12 tokens at
-  // least, of 8 where those leave less than eight waves per CU (16384 x 1024: 20.0 us with 12,
-  // 20.9 with 8, 22.5 with 32; 512 x 2048: 5.3 us with 8, 6.0 with 12, 9.0 with 32).
+  // Short-lived waves stream best: 40 per CU (16384 x 5120: 75 us, chunks of 32 tokens; 76 with 20
+  // or 80).  Chunks of 12 tokens at least, of 8 where those leave less than eight waves per CU
+  // (16384 x 1024: 20.0 us with 12, 20.9 with 8, 22.5 with 32; 512 x 2048: 5.3 us with 8, 6.0 with
+  // 12, 9.0 with 32).
   const int64_t cus = std::max(num_cus, 1);
-  const int64_t chunks = std::max<int64_t>(1, cus * 20 / std::max<int64_t>(1, groups));
+  const int64_t chunks = std::max<int64_t>(1, cus * 40 / std::max<int64_t>(1, groups));
   const int64_t least = groups * ((tokens + 7) / 8) < cus * 8 ? 8 : 12;
   int64_t k = std::max<int64_t>((tokens + chunks - 1) / chunks, least);
   const int forced = env_int("SSS_FORCE_SEGMENTS", 0);
