@@ -240,8 +240,7 @@ hipError_t launch_slot_update(const PackedScanArgs& a, hipStream_t stream);
 // Norms around the block (norms.hip).  Pointers marked nullable may be null.
 constexpr int64_t kMaxNormDim = 32768;  // elements of a normed row: 1024 lanes of 32
 struct NormPlan {
-  int nblk;       // workgroups per group of the gradients kernel
-  int part_rows;  // rows of partial parameter gradients
+  int nblk;  // workgroups per group of the gradients kernel: rows of partial parameter gradients
   size_t ws_total;
 };
 

@@ -74,6 +74,39 @@ struct Pieces {
   __device__ __forceinline__ bool live(int m) const { return skip[m] < V; }
 };
 
+// One row of partial parameter gradients per workgroup: where each wave has rows of its own, the
+// waves' sums are joined in LDS first, in their order (RPB * G floats of it).
+template <int V, int TPR, int M>
+__device__ __forceinline__ void put_partials(float* __restrict__ to, const float (&v)[M][V], const Pieces<V, TPR, M>& pc,
+                                             float* lds, int G) {
+  if constexpr (TPR >= 256) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      Vec<false, V> r;
+      r.set(v[m]);
+      r.store_from(to + pc.at[m], pc.skip[m]);
+    }
+  } else {
+    constexpr int RPB = 256 / TPR;
+    float* const mine = lds + (threadIdx.x / TPR) * G;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+#pragma unroll
+      for (int c = 0; c < V; ++c)
+        if (pc.live(m) && c >= pc.skip[m]) mine[pc.at[m] + c] = v[m][c];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < G; i += 256) {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < RPB; ++q) s += lds[q * G + i];
+      to[i] = s;
+    }
+    __syncthreads();
+  }
+}
+
 struct GNormGeo {
   int64_t sx, sz, sdz;  // elements between rows
   int64_t rows;
@@ -222,14 +255,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_norm_bwd_kernel(
       }
     }
   }
-  float* const pp = part + (blk * RPB + sub) * D + c0;
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    if (!pc.live(m)) continue;
-    Vec<false, V> r;
-    r.set(dw[m]);
-    r.store_from(pp + pc.at[m], pc.skip[m]);
-  }
+  extern __shared__ float norm_lds[];
+  put_partials<V, TPR, M>(part + blk * D + c0, dw, pc, norm_lds, g.G);
 }
 
 struct RNormGeo {
@@ -310,7 +337,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void res_norm_fwd_kernel(
   }
 }
 
-// Gradients; partials [workgroup row][3][D]: dweight, dpost_weight, dscale (those that are wanted).
+// Gradients; partials [workgroup][up to 3][D]: dweight, dpost_weight, dscale (those that are wanted).
 template <bool XB, bool HB, bool POST, int V, int TPR, int M>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void res_norm_bwd_kernel(
     const char* __restrict__ dout, const char* __restrict__ dres_out, const char* __restrict__ x,
@@ -419,20 +446,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void res_norm_bwd_kernel(
     }
   }
   const int64_t vecs = 1 + (POST ? 1 : 0) + (scale != nullptr ? 1 : 0);
-  float* pp = part + (blk * RPB + sub) * vecs * D;
-  auto put = [&](const float (&v)[M][V]) {
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      if (!pc.live(m)) continue;
-      Vec<false, V> r;
-      r.set(v[m]);
-      r.store_from(pp + pc.at[m], pc.skip[m]);
-    }
-    pp += D;
-  };
-  put(dw);
-  if constexpr (POST) put(dp);
-  if (scale != nullptr) put(ds);
+  extern __shared__ float norm_lds[];
+  float* pp = part + blk * vecs * D;
+  put_partials<V, TPR, M>(pp, dw, pc, norm_lds, g.D);
+  if constexpr (POST) put_partials<V, TPR, M>(pp += D, dp, pc, norm_lds, g.D);
+  if (scale != nullptr) put_partials<V, TPR, M>(pp += D, ds, pc, norm_lds, g.D);
 }
 
 // Parameter gradients from the partials, added in their order: columns d, D + d, 2D + d are those
@@ -482,11 +500,14 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
   NormPlan pl{};
   const NormShape sh = norm_shape(group);
   const int rpb = sh.tpr < 256 ? 256 / sh.tpr : 1;
-  // enough workgroups to fill the device, few enough that their partials stay small
-  const int64_t want = std::max<int64_t>(1, (int64_t)num_cus * (sh.tpr > 256 ? 2 : 4) / groups);
-  pl.nblk = (int)std::max<int64_t>(1, std::min<int64_t>(want, (rows + rpb - 1) / rpb));
-  pl.part_rows = pl.nblk * rpb;
-  pl.ws_total = (size_t)pl.part_rows * vectors * group * groups * 4;
+  // Four workgroups per CU (two of more than 256 lanes), but six rows for each as long as every CU
+  // has one: a workgroup leaves a row of partials for each vector of parameters (3000 x 5121
+  // fp32 with three of them: 108 us with six rows, 121 with three).
+  const int64_t sets = std::max<int64_t>(1, (rows + rpb - 1) / rpb), cus = std::max(num_cus, 1);
+  const int64_t want = std::max<int64_t>(1, cus * (sh.tpr > 256 ? 2 : 4) / groups);
+  const int64_t one_each = std::max<int64_t>(1, std::min<int64_t>(sets, cus / groups));
+  pl.nblk = (int)std::min<int64_t>(want, std::max<int64_t>(one_each, rows / 6));
+  pl.ws_total = (size_t)pl.nblk * vectors * group * groups * 4;
   return pl;
 }
 
@@ -545,14 +566,14 @@ static hipError_t gated_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStrea
   const NormShape sh = norm_shape(a.group);
 #define CALL(V, TPR, M)                                                                                               \
   hipLaunchKernelGGL((gated_norm_bwd_kernel<XB, ZB, V, TPR, M>), dim3((unsigned)(pl.nblk * a.groups)),                 \
-                     dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.dout, (const char*)a.x, (const char*)a.z, \
+                     dim3(TPR < 256 ? 256 : TPR), TPR < 256 ? (256 / TPR) * a.group * 4 : 0, stream, (const char*)a.dout, (const char*)a.x, (const char*)a.z, \
                      a.w, a.rstd, (char*)a.dx, (char*)a.dz, (float*)a.workspace, g)
   SSS_NORM_SHAPES(CALL);
 #undef CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t D = a.group * a.groups;
-  return launch_norm_sum(a.workspace, a.dw, nullptr, nullptr, pl.part_rows, D, D, stream);
+  return launch_norm_sum(a.workspace, a.dw, nullptr, nullptr, pl.nblk, D, D, stream);
 }
 
 hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStream_t stream) {
@@ -593,7 +614,7 @@ static hipError_t res_bwd(const ResNormArgs& a, const NormPlan& pl, hipStream_t 
   const NormShape sh = norm_shape(a.dim);
 #define CALL(V, TPR, M)                                                                                                \
   hipLaunchKernelGGL((res_norm_bwd_kernel<XB, HB, POST, V, TPR, M>), dim3((unsigned)pl.nblk),                          \
-                     dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.dout, (const char*)a.dres_out,             \
+                     dim3(TPR < 256 ? 256 : TPR), TPR < 256 ? (256 / TPR) * a.dim * 4 : 0, stream, (const char*)a.dout, (const char*)a.dres_out,             \
                      (const char*)a.x, (const char*)a.residual_out, a.wp, a.scale, a.w, a.rstd_post, a.rstd,           \
                      (char*)a.dx, (char*)a.dres, (float*)a.workspace, g)
   SSS_NORM_SHAPES(CALL);
@@ -601,7 +622,7 @@ static hipError_t res_bwd(const ResNormArgs& a, const NormPlan& pl, hipStream_t 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t cols = a.dim * (1 + (POST ? 1 : 0) + (a.scale != nullptr ? 1 : 0));
-  return launch_norm_sum(a.workspace, a.dw, POST ? a.dwp : a.dscale, a.dscale, pl.part_rows, cols, a.dim, stream);
+  return launch_norm_sum(a.workspace, a.dw, POST ? a.dwp : a.dscale, a.dscale, pl.nblk, cols, a.dim, stream);
 }
 
 template <bool XB, bool HB>
