@@ -180,8 +180,8 @@ int norm_dims(int64_t rows, int64_t dim, int64_t group) {
   if (rows < 0 || dim < 1 || group < 1 || rows > kMaxTokens || dim > kMaxRowDim || dim % group != 0)
     return SSS_ERR_BAD_DIM;
   if (group > kMaxNormDim) return SSS_ERR_UNSUPPORTED;
-  const double threads = group <= 1024 ? 64.0 : group <= 8192 ? 256.0 : group <= 16384 ? 512.0 : 1024.0;
-  if (((double)rows * (double)(dim / group) + 4.0) * threads > 2147483647.0) return SSS_ERR_BAD_DIM;
+  const double threads = group <= 64 ? 8.0 : group <= 1024 ? 64.0 : group <= 8192 ? 256.0 : group <= 16384 ? 512.0 : 1024.0;
+  if (((double)rows * (double)(dim / group) + 32.0) * threads > 2147483647.0) return SSS_ERR_BAD_DIM;
   return SSS_OK;
 }
 

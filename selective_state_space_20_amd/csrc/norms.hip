@@ -10,7 +10,7 @@
 // Gradients, with hat = u rstd(u) and g the gradient of hat:  du = rstd (g - hat mean(g hat)).
 //
 // Streaming: each element read once and each result written once.  A row (of a group) is held in
-// the registers of one wave, of one workgroup of 256, 512 or 1024 lanes, whichever is the
+// the registers of 8, 16, 32 or 64 lanes of a wave, or of a workgroup of 256, 512 or 1024 lanes, whichever is the
 // smallest that holds it: 8 adjacent elements per lane and piece (16 bytes in bf16), M pieces.
 // Sums are fp32: lanes of a wave by DPP, waves through LDS.
 #include "colsum.h"
@@ -40,8 +40,17 @@ __device__ __forceinline__ float wave_sum(float v) {
 // Sum over the TPR lanes that share a row.  `turn` alternates the LDS buffer: a wave that
 // writes a buffer again has passed the barrier of the sum in between, before which every
 // wave has read it, so that one barrier per sum suffices.
+// Up to 64 lanes per row are a wave or an aligned part of one.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* lds, int& turn) {
+  if constexpr (TPR < 64) {
+    v += norm_dpp<0xB1>(v);
+    v += norm_dpp<0x4E>(v);
+    v += norm_dpp<0x141>(v);
+    if constexpr (TPR >= 16) v += norm_dpp<0x140>(v);
+    if constexpr (TPR >= 32) v += __shfl_xor(v, 16);
+    return v;
+  }
   v = wave_sum(v);
   if constexpr (TPR > 64) {
     constexpr int NW = TPR / 64;
@@ -63,7 +72,7 @@ template <int V, int TPR, int M>
 struct Pieces {
   int at[M], skip[M];
   __device__ __forceinline__ Pieces(int G) {
-    const int tid = TPR == 64 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
+    const int tid = (int)threadIdx.x & (TPR - 1);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       const int p = (m * TPR + tid) * V;
@@ -123,7 +132,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void gated_norm_fwd_kernel(
   constexpr int XS = XB ? 2 : 4, ZS = ZB ? 2 : 4;
   __shared__ float lds[2 * 16];
   const int64_t vr = (int64_t)blockIdx.x * RPB + (RPB > 1 ? (int)(threadIdx.x / TPR) : 0);
-  if (RPB > 1 && vr >= g.rows * g.groups) return;  // a whole wave: no barrier with one wave per row
+  if (RPB > 1 && vr >= g.rows * g.groups) return;  // all lanes of the row; no barrier where a workgroup has many
   const int64_t row = vr / g.groups;
   const int c0 = (int)(vr - row * g.groups) * g.G;
   const Pieces<V, TPR, M> pc(g.G);
@@ -478,13 +487,16 @@ static hipError_t launch_norm_sum(const void* part, float* out0, float* out1, fl
   return hipGetLastError();
 }
 
-// Lanes per row and pieces per lane for rows of G elements (V = 8; fewer elements: one wave, V = 1).
+// Lanes per row and pieces per lane for rows of G elements (V = 8; fewer elements: 8 lanes, V = 1).
 struct NormShape {
   int v, tpr, m;
 };
 static NormShape norm_shape(int64_t G) {
-  if (G < 8) return {1, 64, 1};
+  if (G < 8) return {1, 8, 1};
   const int64_t p = (G + 7) / 8;
+  if (p <= 8) return {8, 8, 1};  // 16384 x 5120 in groups of 64: forward 421 us with a wave per row
+  if (p <= 16) return {8, 16, 1};
+  if (p <= 32) return {8, 32, 1};
   if (p <= 64) return {8, 64, 1};
   if (p <= 128) return {8, 64, 2};
   if (p <= 256) return {8, 256, 1};
@@ -513,7 +525,10 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
 
 #define SSS_NORM_SHAPES(CALL)                                                   \
   do {                                                                          \
-    if (sh.v == 1) { CALL(1, 64, 1); }                                          \
+    if (sh.v == 1) { CALL(1, 8, 1); }                                           \
+    else if (sh.tpr == 8) { CALL(8, 8, 1); }                                    \
+    else if (sh.tpr == 16) { CALL(8, 16, 1); }                                  \
+    else if (sh.tpr == 32) { CALL(8, 32, 1); }                                  \
     else if (sh.tpr == 64 && sh.m == 1) { CALL(8, 64, 1); }                     \
     else if (sh.tpr == 64) { CALL(8, 64, 2); }                                  \
     else if (sh.tpr == 256 && sh.m == 1) { CALL(8, 256, 1); }                   \

@@ -31,7 +31,8 @@ def rounding(bf16, v):
     (70, 8, 1, True, True), (9, 18, 2, False, True), (1, 511, 1, True, True), (4, 1026, 2, False, False),
     (3, 1032, 1, True, False), (2, 2057, 1, False, True), (5, 6150, 1, True, True), (2, 8191, 1, False, True),
     (2, 12289, 1, True, True), (1, 16384, 1, False, False), (2, 32768, 1, True, True), (1100, 24, 3, False, True),
-    (6, 768, 6, True, None), (3, 4100, 1, False, None)])
+    (6, 768, 6, True, None), (3, 4100, 1, False, None), (37, 129, 1, False, True), (9, 400, 2, True, True),
+    (33, 640, 10, False, True), (5, 300, 20, False, False), (40, 16, 8, True, True)])
 def test_gated_norm(rows, dim, groups, x16, z16, norm_first):
     import torch
     import selective_state_space_20_amd as sss
@@ -70,7 +71,7 @@ def test_gated_norm(rows, dim, groups, x16, z16, norm_first):
     (3, 2560, True, False), (1, 1, False, False), (5, 7, True, True), (70, 8, True, False), (2, 65, False, False),
     (9, 600, True, True), (1, 1025, True, False), (300, 40, False, False), (3, 2051, True, False),
     (2, 5120, False, True), (2, 8192, True, False), (2, 8200, True, False), (1, 16000, False, False),
-    (2, 32768, True, True)])
+    (2, 32768, True, True), (35, 100, True, False), (17, 250, False, True), (3, 9, True, False)])
 def test_residual_norm(rows, dim, x16, h16, post, scaled, first):
     import torch
     import selective_state_space_20_amd as sss
