@@ -75,6 +75,16 @@ def _scratch(workspace, nbytes, like):
     return (workspace, *_lib._workspace(workspace, like.device))
 
 
+def _keep(stream, index, *tensors):
+    """Memory allocated in the call (on the current stream) that work on a given other stream uses:
+    not handed out again before that work is done."""
+    if stream is not None and stream != _torch._C._cuda_getCurrentRawStream(index):
+        s = _torch.cuda.ExternalStream(stream, device=_torch.device("cuda", index))
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
 def _code(dtype, name):
     torch = torch_()
     if dtype is torch.bfloat16:
@@ -151,6 +161,7 @@ def causal_conv1d_packed_fwd(x, weight, bias=None, *, cu_seqlens, conv_state=Non
                                          width, code, int(bool(silu)), _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_packed_fwd")
+    _keep(stream, gpu, o)
     return o
 
 
@@ -179,6 +190,7 @@ def causal_conv1d_update(x, weight, bias=None, *, conv_state, state_indices=None
                                      _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_update")
+    _keep(stream, gpu, o)
     return o
 
 
@@ -236,6 +248,7 @@ def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, worksp
                                   _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_bwd")
+    _keep(stream, gpu, workspace, *g.values())
     return g
 
 
@@ -288,6 +301,7 @@ def selective_scan_packed_fwd(x, delta, A, B, C, D=None, z=None, *, cu_seqlens, 
                                           tokens, nseq, slots, dim, n, code, bc, yc, wsp, wsn, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "selective_scan_packed_fwd")
+    _keep(stream, gpu, workspace, y)
     return y
 
 
@@ -313,6 +327,7 @@ def selective_state_update_slots(x, delta, A, B, C, D=None, z=None, *, state, st
                                              slots, dim, n, code, bc, yc, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "selective_state_update_slots")
+    _keep(stream, gpu, y)
     return y
 
 
@@ -349,6 +364,7 @@ def rms_norm_gated_fwd(x, weight, z=None, *, eps=1e-5, group_size=None, norm_bef
                                        _stream(stream, gpu))
         if rc != 0:
             raise SSSError(rc, "rms_norm_gated_fwd")
+        _keep(stream, gpu, o, rstd)
     return (o, rstd) if return_rstd else o
 
 
@@ -389,6 +405,7 @@ def rms_norm_gated_bwd(dout, x, weight, z=None, *, rstd, group_size=None, norm_b
                                    _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "rms_norm_gated_bwd")
+    _keep(stream, gpu, workspace, *res.values())
     return res
 
 
@@ -426,6 +443,7 @@ def rms_norm_residual_fwd(x, weight, residual=None, *, post_weight=None, scale=N
                                           xc, hc, _stream(stream, gpu))
         if rc != 0:
             raise SSSError(rc, "rms_norm_residual_fwd")
+        _keep(stream, gpu, o, h, rstd, rstd_post)
     return (o, h, rstd, rstd_post) if return_rstd else (o, h)
 
 
@@ -475,4 +493,5 @@ def rms_norm_residual_bwd(dout, dresidual_out=None, *, residual_out, weight, rst
                                       hc, wsp, wsn, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "rms_norm_residual_bwd")
+    _keep(stream, gpu, workspace, *res.values())
     return res
