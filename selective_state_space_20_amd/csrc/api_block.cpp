@@ -51,8 +51,7 @@ int conv_impl(const void* x, int64_t x_stride, const float* weight, const float*
   if (!r.aligned) return SSS_ERR_UNSUPPORTED;
   if (!r.ok()) return SSS_ERR_ALIAS;
   if (tokens == 0 || nseq == 0) return SSS_OK;
-  const int cus = current_device_cus();
-  if (cus <= 0) return SSS_ERR_HIP;
+  if (current_device_cus() <= 0) return SSS_ERR_HIP;
   PackedConvArgs a{};
   a.x = x;
   a.x_stride = x_stride;
@@ -71,7 +70,7 @@ int conv_impl(const void* x, int64_t x_stride, const float* weight, const float*
   a.bf16 = io_dtype == SSS_BF16;
   a.silu = apply_silu != 0;
   a.step = step;
-  return status_of(launch_packed_conv(a, cus, reinterpret_cast<hipStream_t>(stream)));
+  return status_of(launch_packed_conv(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 bool conv_bwd_dims_ok(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {

@@ -175,7 +175,7 @@ struct PackedConvArgs {
   int width, bf16, silu, step;
 };
 
-hipError_t launch_packed_conv(const PackedConvArgs& a, int num_cus, hipStream_t stream);
+hipError_t launch_packed_conv(const PackedConvArgs& a, hipStream_t stream);
 
 // Gradients of the causal convolution (conv_bwd.hip).
 struct ConvBwdPlan {

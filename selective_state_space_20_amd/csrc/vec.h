@@ -183,19 +183,31 @@ struct Vec {
 // among cu[0..nseq] (-1: before the first).  The whole wave searches: 64 boundaries per load,
 // so that 64 sequences take one load and 4096 two.  Any contents of cu give a number in
 // [-1, nseq].
-__device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int nseq, int t, int lane) {
-  int lo = 0, cnt = nseq + 1;
-  while (cnt > 64) {
-    const int step = (cnt + 63) >> 6;
-    const int i = lane * step;
-    const bool le = i < cnt && cu[lo + i] <= t;
-    const int k = __builtin_popcountll(__builtin_amdgcn_ballot_w64(le));
-    if (k == 0) return lo - 1;
-    lo += (k - 1) * step;
-    cnt = min(step, cnt - (k - 1) * step);
+// In two halves, so that the first load can be issued ahead of others: vector loads return in
+// order, and waiting for this one does not wait for those after it.
+struct SeqSearch {
+  const int32_t* cu;
+  int cnt, lane, first;
+  __device__ __forceinline__ SeqSearch(const int32_t* cu_, int nseq, int lane_) : cu(cu_), cnt(nseq + 1), lane(lane_) {
+    first = cu[min(lane * ((cnt + 63) >> 6), nseq)];
   }
-  const bool le = lane < cnt && cu[lo + lane] <= t;
-  return lo - 1 + __builtin_popcountll(__builtin_amdgcn_ballot_w64(le));
+  __device__ __forceinline__ int find(int t) const {
+    int step = (cnt + 63) >> 6, lo = 0, n = cnt;
+    int k = __builtin_popcountll(__builtin_amdgcn_ballot_w64(lane * step < n && first <= t));
+    while (step > 1) {
+      if (k == 0) return lo - 1;
+      lo += (k - 1) * step;
+      n = min(step, n - (k - 1) * step);
+      step = (n + 63) >> 6;
+      const int i = lane * step;
+      const bool le = i < n && cu[lo + i] <= t;
+      k = __builtin_popcountll(__builtin_amdgcn_ballot_w64(le));
+    }
+    return lo - 1 + k;
+  }
+};
+__device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int nseq, int t, int lane) {
+  return SeqSearch(cu, nseq, lane).find(t);
 }
 
 }  // namespace sss

@@ -110,6 +110,32 @@ def test_packed_conv(lens, dim, width, bf16, chunks):
                            before[s].view(torch.int16 if bf16 else torch.int32))
 
 
+@pytest.mark.parametrize("dim,width,bf16", [(5120, 4, True), (4099, 3, True), (2560, 5, False), (2561, 8, False)])
+def test_packed_conv_wide(dim, width, bf16):
+    """Sizes past those where a lane takes 16 bytes of a row: sampled columns against the reference,
+    the whole against the same sequences in two smaller calls."""
+    import torch
+    import selective_state_space_20_amd as sss
+    rng = np.random.default_rng(dim)
+    t = 8192 if bf16 else 7000
+    cu = np.array([0, 3, 1500, 1500, 1507, 4000, t], np.int32)
+    idx, initial = np.array([5, 3, 1, -1, 0, 2], np.int32), np.array([1, 1, 1, 1, 0, 1], np.uint8)
+    x, w, b = rand(rng, (t, dim), bf16), rand(rng, (dim, width), scale=0.5), rand(rng, (dim,))
+    state = rand(rng, (6, width - 1, dim), bf16)
+    st, st2 = dev_of(state), dev_of(state)
+    d = [dev_of(v) for v in (x, w, b, idx, initial)]
+    out = sss.causal_conv1d_packed_fwd(d[0], d[1], d[2], cu_seqlens=dev_of(cu), conv_state=st, state_indices=d[3],
+                                       has_initial=d[4], silu=True)
+    parts = [sss.causal_conv1d_packed_fwd(d[0][lo:hi], d[1], d[2], cu_seqlens=dev_of(c), conv_state=st2,
+                                          state_indices=d[3][s], has_initial=d[4][s], silu=True)
+             for lo, hi, s, c in ((0, 1507, slice(0, 4), cu[:5]), (1507, t, slice(4, 6), cu[4:] - 1507))]
+    assert torch.equal(torch.cat(parts), out) and torch.equal(st, st2)
+    cols = np.unique(np.concatenate([np.arange(9), np.arange(dim - 9, dim), rng.integers(0, dim, 30)]))
+    want, want_state, mag = ref.packed_conv(x[:, cols], w[cols], b[cols], cu, state[:, :, cols], idx, initial, True)
+    close(host(out)[:, cols], want, 2 * (width + 6) * EPS * mag + (2.0 ** -8 * np.abs(want) if bf16 else 0) + 1e-37, "out")
+    np.testing.assert_array_equal(host(st)[:, :, cols], want_state)
+
+
 def test_packed_conv_without_cache_and_rows_outside():
     import torch
     import selective_state_space_20_amd as sss
