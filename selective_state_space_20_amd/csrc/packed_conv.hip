@@ -198,12 +198,7 @@ __global__ __launch_bounds__(64 * kPConvWaves) void packed_conv_kernel(const cha
     for (int c = 0; c < CPL; ++c)
 #pragma unroll
       for (int k = 0; k < H; ++k) win[c][k] = hist[k].get(c);
-    for (; t < e; ++t) {
-      R cur = q[H];  // the chunk's tokens are in registers, those after it are not
-#pragma unroll
-      for (int i = 1; i < K; ++i)
-        if (t - c0 == i) cur = q[H + i];
-      if (t - c0 >= K) cur.load(xl + (int64_t)t * xrow);
+    auto step = [&](const R& cur) {
       float o[CPL];
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
@@ -218,6 +213,20 @@ __global__ __launch_bounds__(64 * kPConvWaves) void packed_conv_kernel(const cha
       R r;
       r.set(o);
       put(r, t);
+    };
+    // The chunk's tokens are in registers, those after it are not.  Two loops: one that takes each
+    // token from either has been compiled (8-byte lanes, fp32) with a copy of the window lost.
+    for (const int last = min(e, c0 + K); t < last; ++t) {
+      R cur = q[H];
+#pragma unroll
+      for (int i = 1; i < K; ++i)
+        if (t - c0 == i) cur = q[H + i];
+      step(cur);
+    }
+    for (; t < e; ++t) {
+      R cur;
+      cur.load(xl + (int64_t)t * xrow);
+      step(cur);
     }
   }
 }
