@@ -285,7 +285,8 @@ struct ResNormArgs {
   int x_bf16, h_bf16;
 };
 
-NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, int num_cus);
+// fp32: the residual norm with an fp32 tensor (its kernels take other shapes)
+NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, bool fp32, int num_cus);
 hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t stream);
 hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, const NormPlan& plan, hipStream_t stream);
 hipError_t launch_res_norm_fwd(const ResNormArgs& a, hipStream_t stream);

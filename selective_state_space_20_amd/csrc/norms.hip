@@ -11,7 +11,8 @@
 //
 // Streaming: each element read once and each result written once.  A row (of a group) is held in
 // the registers of 8, 16, 32 or 64 lanes of a wave, or of a workgroup of 256, 512 or 1024 lanes, whichever is the
-// smallest that holds it: 8 adjacent elements per lane and piece (16 bytes in bf16), M pieces.
+// smallest that holds it: 8 or 4 adjacent elements per lane and piece (16 bytes of bf16 or fp32), M
+// pieces.
 // Sums are fp32: lanes of a wave by DPP, waves through LDS.
 #include "colsum.h"
 #include "vec.h"
@@ -65,7 +66,7 @@ __device__ __forceinline__ float row_sum(float v, float* lds, int& turn) {
   return v;
 }
 
-// The pieces of a row of G elements: piece p starts at element 8p, the last one V elements
+// The pieces of a row of G elements: piece p starts at element V p, the last one V elements
 // before the row's end where V does not divide G: its first `skip` elements are then another
 // lane's, count for nothing and are not stored.
 template <int V, int TPR, int M>
@@ -487,30 +488,36 @@ static hipError_t launch_norm_sum(const void* part, float* out0, float* out1, fl
   return hipGetLastError();
 }
 
-// Lanes per row and pieces per lane for rows of G elements (V = 8; fewer elements: 8 lanes, V = 1).
+// Lanes per row and pieces per lane for rows of G elements, V elements per piece.  V = 8 is 16 bytes
+// of bf16.  Where a tensor is fp32, V = 4 makes every access of it 16 adjacent bytes per lane instead of
+// two accesses of every other 16: forward of 16384 x 5120, fp32 x and bf16 z, 129 -> 114 us;
+// residual norm of 16384 x 2560 with an fp32 stream, forward 110 -> 94 us, gradients 144 -> 136.  (Not
+// the gated norm's gradients, of which most is bf16: 275 us with 8, 305 with 4.)  Above 5120 elements V
+// = 4 would take more pieces per lane than fit.  Fewer than 8 elements: one each, 8 lanes.
 struct NormShape {
   int v, tpr, m;
 };
-static NormShape norm_shape(int64_t G) {
+static NormShape norm_shape(int64_t G, bool fp32) {
   if (G < 8) return {1, 8, 1};
-  const int64_t p = (G + 7) / 8;
-  if (p <= 8) return {8, 8, 1};  // 16384 x 5120 in groups of 64: forward 421 us with a wave per row
-  if (p <= 16) return {8, 16, 1};
-  if (p <= 32) return {8, 32, 1};
-  if (p <= 64) return {8, 64, 1};
-  if (p <= 128) return {8, 64, 2};
-  if (p <= 256) return {8, 256, 1};
-  if (p <= 512) return {8, 256, 2};
-  if (p <= 768) return {8, 256, 3};
-  if (p <= 1024) return {8, 256, 4};
-  if (p <= 1536) return {8, 512, 3};
-  if (p <= 2048) return {8, 512, 4};
-  return {8, 1024, 4};
+  const int v = fp32 && G <= 5120 ? 4 : 8;
+  const int64_t p = (G + v - 1) / v;
+  if (p <= 8) return {v, 8, 1};  // 16384 x 5120 in groups of 64: forward 421 us with a wave per row
+  if (p <= 16) return {v, 16, 1};
+  if (p <= 32) return {v, 32, 1};
+  if (p <= 64) return {v, 64, 1};
+  if (p <= 128) return {v, 64, 2};
+  if (p <= 1280) {
+    const int m = (int)((p + 255) / 256);
+    if (m <= 4 || v == 4) return {v, 256, m};
+  }
+  if (p <= 1536) return {v, 512, 3};
+  if (p <= 2048) return {v, 512, 4};
+  return {v, 1024, 4};
 }
 
-NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, int num_cus) {
+NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, bool fp32, int num_cus) {
   NormPlan pl{};
-  const NormShape sh = norm_shape(group);
+  const NormShape sh = norm_shape(group, fp32);
   const int rpb = sh.tpr < 256 ? 256 / sh.tpr : 1;
   // Four workgroups per CU (two of more than 256 lanes), but six rows for each as long as every CU
   // has one: a workgroup leaves a row of partials for each vector of parameters (3000 x 5121
@@ -523,21 +530,32 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
   return pl;
 }
 
-#define SSS_NORM_SHAPES(CALL)                                                   \
+// CALL(V, TPR, M) of the shape sh; F32: one of the tensors is fp32
+#define SSS_NORM_SMALL(CALL, V)                                                 \
+  if (sh.tpr == 8) { CALL(V, 8, 1); }                                           \
+  else if (sh.tpr == 16) { CALL(V, 16, 1); }                                    \
+  else if (sh.tpr == 32) { CALL(V, 32, 1); }                                    \
+  else if (sh.tpr == 64 && sh.m == 1) { CALL(V, 64, 1); }                       \
+  else if (sh.tpr == 64) { CALL(V, 64, 2); }                                    \
+  else if (sh.tpr == 256 && sh.m == 1) { CALL(V, 256, 1); }                     \
+  else if (sh.tpr == 256 && sh.m == 2) { CALL(V, 256, 2); }                     \
+  else if (sh.tpr == 256 && sh.m == 3) { CALL(V, 256, 3); }                     \
+  else if (sh.tpr == 256 && sh.m == 4) { CALL(V, 256, 4); }
+#define SSS_NORM_SHAPES(CALL, F32)                                              \
   do {                                                                          \
-    if (sh.v == 1) { CALL(1, 8, 1); }                                           \
-    else if (sh.tpr == 8) { CALL(8, 8, 1); }                                    \
-    else if (sh.tpr == 16) { CALL(8, 16, 1); }                                  \
-    else if (sh.tpr == 32) { CALL(8, 32, 1); }                                  \
-    else if (sh.tpr == 64 && sh.m == 1) { CALL(8, 64, 1); }                     \
-    else if (sh.tpr == 64) { CALL(8, 64, 2); }                                  \
-    else if (sh.tpr == 256 && sh.m == 1) { CALL(8, 256, 1); }                   \
-    else if (sh.tpr == 256 && sh.m == 2) { CALL(8, 256, 2); }                   \
-    else if (sh.tpr == 256 && sh.m == 3) { CALL(8, 256, 3); }                   \
-    else if (sh.tpr == 256) { CALL(8, 256, 4); }                                \
-    else if (sh.tpr == 512 && sh.m == 3) { CALL(8, 512, 3); }                   \
-    else if (sh.tpr == 512) { CALL(8, 512, 4); }                                \
-    else { CALL(8, 1024, 4); }                                                  \
+    if (sh.v == 1) {                                                            \
+      CALL(1, 8, 1);                                                            \
+    } else if (sh.v == 4) {                                                     \
+      if constexpr (F32) {                                                      \
+        SSS_NORM_SMALL(CALL, 4)                                                 \
+        else { CALL(4, 256, 5); }                                               \
+      }                                                                         \
+    } else {                                                                    \
+      SSS_NORM_SMALL(CALL, 8)                                                   \
+      else if (sh.tpr == 512 && sh.m == 3) { CALL(8, 512, 3); }                 \
+      else if (sh.tpr == 512) { CALL(8, 512, 4); }                              \
+      else { CALL(8, 1024, 4); }                                                \
+    }                                                                           \
   } while (0)
 
 static GNormGeo gated_geo(const GatedNormArgs& a) {
@@ -557,14 +575,14 @@ static GNormGeo gated_geo(const GatedNormArgs& a) {
 template <bool XB, bool ZB>
 static hipError_t gated_fwd(const GatedNormArgs& a, hipStream_t stream) {
   const GNormGeo g = gated_geo(a);
-  const NormShape sh = norm_shape(a.group);
+  const NormShape sh = norm_shape(a.group, !XB || !ZB);
   const int64_t vrows = a.rows * a.groups;
 #define CALL(V, TPR, M)                                                                                             \
   hipLaunchKernelGGL((gated_norm_fwd_kernel<XB, ZB, V, TPR, M>),                                                    \
                      dim3((unsigned)((vrows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))),      \
                      dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.x, (const char*)a.z, a.w, (char*)a.out, \
                      a.rstd, g)
-  SSS_NORM_SHAPES(CALL);
+  SSS_NORM_SHAPES(CALL, !XB || !ZB);
 #undef CALL
   return hipGetLastError();
 }
@@ -578,12 +596,12 @@ template <bool XB, bool ZB>
 static hipError_t gated_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStream_t stream) {
   GNormGeo g = gated_geo(a);
   g.nblk = pl.nblk;
-  const NormShape sh = norm_shape(a.group);
+  const NormShape sh = norm_shape(a.group, false);
 #define CALL(V, TPR, M)                                                                                               \
   hipLaunchKernelGGL((gated_norm_bwd_kernel<XB, ZB, V, TPR, M>), dim3((unsigned)(pl.nblk * a.groups)),                 \
                      dim3(TPR < 256 ? 256 : TPR), TPR < 256 ? (256 / TPR) * a.group * 4 : 0, stream, (const char*)a.dout, (const char*)a.x, (const char*)a.z, \
                      a.w, a.rstd, (char*)a.dx, (char*)a.dz, (float*)a.workspace, g)
-  SSS_NORM_SHAPES(CALL);
+  SSS_NORM_SHAPES(CALL, false);
 #undef CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -611,13 +629,13 @@ static RNormGeo res_geo(const ResNormArgs& a) {
 template <bool XB, bool HB, bool POST>
 static hipError_t res_fwd(const ResNormArgs& a, hipStream_t stream) {
   const RNormGeo g = res_geo(a);
-  const NormShape sh = norm_shape(a.dim);
+  const NormShape sh = norm_shape(a.dim, !XB || !HB);
 #define CALL(V, TPR, M)                                                                                               \
   hipLaunchKernelGGL((res_norm_fwd_kernel<XB, HB, POST, V, TPR, M>),                                                  \
                      dim3((unsigned)((a.rows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))),       \
                      dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.x, (const char*)a.residual, a.wp, a.scale, \
                      a.w, (char*)a.out, (char*)a.residual_out, a.rstd_post, a.rstd, g)
-  SSS_NORM_SHAPES(CALL);
+  SSS_NORM_SHAPES(CALL, !XB || !HB);
 #undef CALL
   return hipGetLastError();
 }
@@ -626,13 +644,13 @@ template <bool XB, bool HB, bool POST>
 static hipError_t res_bwd(const ResNormArgs& a, const NormPlan& pl, hipStream_t stream) {
   RNormGeo g = res_geo(a);
   g.nblk = pl.nblk;
-  const NormShape sh = norm_shape(a.dim);
+  const NormShape sh = norm_shape(a.dim, !XB || !HB);
 #define CALL(V, TPR, M)                                                                                                \
   hipLaunchKernelGGL((res_norm_bwd_kernel<XB, HB, POST, V, TPR, M>), dim3((unsigned)pl.nblk),                          \
                      dim3(TPR < 256 ? 256 : TPR), TPR < 256 ? (256 / TPR) * a.dim * 4 : 0, stream, (const char*)a.dout, (const char*)a.dres_out,             \
                      (const char*)a.x, (const char*)a.residual_out, a.wp, a.scale, a.w, a.rstd_post, a.rstd,           \
                      (char*)a.dx, (char*)a.dres, (float*)a.workspace, g)
-  SSS_NORM_SHAPES(CALL);
+  SSS_NORM_SHAPES(CALL, !XB || !HB);
 #undef CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
