@@ -229,7 +229,9 @@ size_t rms_norm_gated_bwd_workspace_size(int64_t rows, int64_t dim, int64_t grou
   if (norm_dims(rows, dim, group) != SSS_OK) return 0;
   int cus = device_cus(device);
   if (cus <= 0) cus = 256;
-  return plan_norm_bwd(rows, group, dim / group, 1, false, cus).ws_total;
+  // of either kernel shape: the query does not know the types
+  return std::max(plan_norm_bwd(rows, group, dim / group, 1, false, cus).ws_total,
+                  plan_norm_bwd(rows, group, dim / group, 1, true, cus).ws_total);
 }
 
 int rms_norm_gated_bwd(const void* dout, const void* x, int64_t x_stride, const float* weight, const void* z,
@@ -258,7 +260,8 @@ int rms_norm_gated_bwd(const void* dout, const void* x, int64_t x_stride, const 
   if (!r.ok()) return SSS_ERR_ALIAS;
   const int cus = current_device_cus();
   if (cus <= 0) return SSS_ERR_HIP;
-  const NormPlan pl = plan_norm_bwd(rows, group, dim / group, 1, false, cus);
+  const bool fp32 = x_dtype == SSS_F32 || out_dtype == SSS_F32;
+  const NormPlan pl = plan_norm_bwd(rows, group, dim / group, 1, fp32, cus);
   if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
   r.output(workspace, (int64_t)pl.ws_total, 16);
   if (!r.ok()) return SSS_ERR_ALIAS;

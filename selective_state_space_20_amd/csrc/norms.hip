@@ -9,10 +9,11 @@
 //   v = x rstd(x) wp  (or x),  h' = h + alpha s v,  out = h' rstd(h') w
 // Gradients, with hat = u rstd(u) and g the gradient of hat:  du = rstd (g - hat mean(g hat)).
 //
-// Streaming: each element read once and each result written once.  A row (of a group) is held in
-// the registers of 8, 16, 32 or 64 lanes of a wave, or of a workgroup of 256, 512 or 1024 lanes, whichever is the
-// smallest that holds it: 8 or 4 adjacent elements per lane and piece (16 bytes of bf16 or fp32), M
-// pieces.
+// Bound by memory: each element read once and each result written once (16384 x 5120, fp32 x and
+// bf16 z: forward 671 MB in 115 us, gradients 1174 MB in 217-240 us; 16384 x 2560 bf16 with an fp32
+// stream: forward 503 MB in 94 us, gradients 755 MB in 134 us).  A row (of a group) is held in
+// the registers of 8, 16, 32 or 64 lanes of a wave, or of a workgroup of 256, 512 or 1024 lanes (norm_shape):
+// 8 or 4 adjacent elements per lane and piece (16 bytes of bf16 or fp32), M pieces.
 // Sums are fp32: lanes of a wave by DPP, waves through LDS.
 #include "colsum.h"
 #include "vec.h"
@@ -491,27 +492,26 @@ static hipError_t launch_norm_sum(const void* part, float* out0, float* out1, fl
 // Lanes per row and pieces per lane for rows of G elements, V elements per piece.  V = 8 is 16 bytes
 // of bf16.  Where a tensor is fp32, V = 4 makes every access of it 16 adjacent bytes per lane instead of
 // two accesses of every other 16: forward of 16384 x 5120, fp32 x and bf16 z, 129 -> 114 us;
-// residual norm of 16384 x 2560 with an fp32 stream, forward 110 -> 94 us, gradients 144 -> 136.  (Not
-// the gated norm's gradients, of which most is bf16: 275 us with 8, 305 with 4.)  Above 5120 elements V
-// = 4 would take more pieces per lane than fit.  Fewer than 8 elements: one each, 8 lanes.
+// residual norm of 16384 x 2560 with an fp32 stream, forward 110 -> 94 us, gradients 144 -> 136.
+// At most three pieces per lane, then 512 lanes: with five of V = 4 the gradients' registers leave few
+// waves (gated forward and gradients of 16384 x 5120 332 us on 512 lanes, 402 on 256, 372 with V =
+// 8 on 256; x 2560 174 on 256 lanes with three pieces, 187 on 512 with two; residual norm x 4096 383 on
+// 512, 421 on 256 with four; bf16 x 8192 forward 185, 188).  Above 6144 elements V = 4 would need 1024
+// lanes.  Fewer than 8 elements: one each, 8 lanes.
 struct NormShape {
   int v, tpr, m;
 };
 static NormShape norm_shape(int64_t G, bool fp32) {
   if (G < 8) return {1, 8, 1};
-  const int v = fp32 && G <= 5120 ? 4 : 8;
+  const int v = fp32 && G <= 6144 ? 4 : 8;
   const int64_t p = (G + v - 1) / v;
   if (p <= 8) return {v, 8, 1};  // 16384 x 5120 in groups of 64: forward 421 us with a wave per row
   if (p <= 16) return {v, 16, 1};
   if (p <= 32) return {v, 32, 1};
   if (p <= 64) return {v, 64, 1};
   if (p <= 128) return {v, 64, 2};
-  if (p <= 1280) {
-    const int m = (int)((p + 255) / 256);
-    if (m <= 4 || v == 4) return {v, 256, m};
-  }
-  if (p <= 1536) return {v, 512, 3};
-  if (p <= 2048) return {v, 512, 4};
+  if (p <= 768) return {v, 256, (int)((p + 255) / 256)};
+  if (p <= 2048) return {v, 512, (int)((p + 511) / 512)};
   return {v, 1024, 4};
 }
 
@@ -539,8 +539,9 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
   else if (sh.tpr == 64) { CALL(V, 64, 2); }                                    \
   else if (sh.tpr == 256 && sh.m == 1) { CALL(V, 256, 1); }                     \
   else if (sh.tpr == 256 && sh.m == 2) { CALL(V, 256, 2); }                     \
-  else if (sh.tpr == 256 && sh.m == 3) { CALL(V, 256, 3); }                     \
-  else if (sh.tpr == 256 && sh.m == 4) { CALL(V, 256, 4); }
+  else if (sh.tpr == 256) { CALL(V, 256, 3); }                                  \
+  else if (sh.m == 2) { CALL(V, 512, 2); }                                      \
+  else if (sh.m == 3) { CALL(V, 512, 3); }
 #define SSS_NORM_SHAPES(CALL, F32)                                              \
   do {                                                                          \
     if (sh.v == 1) {                                                            \
@@ -548,11 +549,9 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
     } else if (sh.v == 4) {                                                     \
       if constexpr (F32) {                                                      \
         SSS_NORM_SMALL(CALL, 4)                                                 \
-        else { CALL(4, 256, 5); }                                               \
       }                                                                         \
     } else {                                                                    \
       SSS_NORM_SMALL(CALL, 8)                                                   \
-      else if (sh.tpr == 512 && sh.m == 3) { CALL(8, 512, 3); }                 \
       else if (sh.tpr == 512) { CALL(8, 512, 4); }                              \
       else { CALL(8, 1024, 4); }                                                \
     }                                                                           \
@@ -596,12 +595,12 @@ template <bool XB, bool ZB>
 static hipError_t gated_bwd(const GatedNormArgs& a, const NormPlan& pl, hipStream_t stream) {
   GNormGeo g = gated_geo(a);
   g.nblk = pl.nblk;
-  const NormShape sh = norm_shape(a.group, false);
+  const NormShape sh = norm_shape(a.group, !XB || !ZB);
 #define CALL(V, TPR, M)                                                                                               \
   hipLaunchKernelGGL((gated_norm_bwd_kernel<XB, ZB, V, TPR, M>), dim3((unsigned)(pl.nblk * a.groups)),                 \
                      dim3(TPR < 256 ? 256 : TPR), TPR < 256 ? (256 / TPR) * a.group * 4 : 0, stream, (const char*)a.dout, (const char*)a.x, (const char*)a.z, \
                      a.w, a.rstd, (char*)a.dx, (char*)a.dz, (float*)a.workspace, g)
-  SSS_NORM_SHAPES(CALL, false);
+  SSS_NORM_SHAPES(CALL, !XB || !ZB);
 #undef CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -158,3 +158,20 @@ def test_zero_rows_and_zero_values():
     x[0, 5] = float("nan")  # stays in its row
     out = sss.rms_norm_gated_fwd(x, w, x)
     assert bool(out[0].isnan().all()) and bool(out[1].isfinite().all())
+
+
+# rows on 512 lanes, in two to four pieces of each width, just below and above the widths' ends
+@pytest.mark.parametrize("norm_first", [False, True])
+@pytest.mark.parametrize("rows,dim,groups,x16,z16", [
+    (1100, 3333, 1, False, True), (3, 4096, 1, True, False), (2, 8202, 2, False, False), (4, 6143, 1, False, True),
+    (3, 6145, 1, False, True), (700, 5120, 1, False, True), (2, 9001, 1, True, True), (3, 13000, 1, False, None)])
+def test_gated_norm_on_512_lanes(rows, dim, groups, x16, z16, norm_first):
+    test_gated_norm(rows, dim, groups, x16, z16, norm_first)
+
+
+@pytest.mark.parametrize("post,scaled,first", [(True, True, False), (False, False, True)])
+@pytest.mark.parametrize("rows,dim,x16,h16", [
+    (1100, 3333, True, False), (3, 4096, False, True), (2, 4097, False, False), (5, 6144, True, False),
+    (3, 6145, True, False), (2, 6200, True, True), (600, 8192, True, True)])
+def test_residual_norm_on_512_lanes(rows, dim, x16, h16, post, scaled, first):
+    test_residual_norm(rows, dim, x16, h16, post, scaled, first)
