@@ -29,6 +29,7 @@
 // A slot is read in pass 1 (or in pass 2 by the wave that also writes it), so that it is updated in
 // place.
 #include "front.h"
+#include "seq_walk.h"
 #include "vec.h"
 #include "kernels.h"
 
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(128, pscan_min_waves(NS)) void packed_scan_kernel(
       }
       const int slot = sidx != nullptr ? sidx[s] : s;
       const bool kept = state != nullptr && (unsigned)slot < (unsigned)g.slots;
-      if (cu[s] < c0) {
+      if (began_before(cu[s], c0)) {
 #pragma unroll
         for (int n = 0; n < NS; ++n) h[n] = ws_enter[((int64_t)chunk * NS + n) * D + dc];
       } else if (kept && init != nullptr && init[s] != 0) {

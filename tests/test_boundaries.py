@@ -1,0 +1,56 @@
+"""Boundaries of packed batches whose contents are not as they should be (negative, decreasing,
+past the tokens): no address depends on them unchecked.  The kernels' index functions, compiled
+for the CPU, over any contents."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "selective_state_space_20_amd", "csrc")
+
+
+def run_native(name, tmp_path):
+    exe = str(tmp_path / name)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-I", CSRC, os.path.join(ROOT, "tests", "native", name + ".cpp"),
+                    "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+def test_scan_walk_stays_in_range(tmp_path):
+    run_native("scan_walk", tmp_path)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", [[-5, 10], [-1, 4, 9, 10], [0, 5, -3, 10], [-2 ** 31, 2 ** 31 - 1], [7, 3, 12, -1, 10]])
+@pytest.mark.parametrize("chunks", [None, 4])
+def test_scan_of_malformed_boundaries(cu, chunks, monkeypatch):
+    """With one chunk there is no workspace, and no row reads it; nothing outside the outputs is written."""
+    import torch
+    import selective_state_space_20_amd as sss
+    if chunks:
+        monkeypatch.setenv("SSS_FORCE_SEGMENTS", str(chunks))
+    g = torch.Generator(device="cuda:0").manual_seed(2)
+    r = lambda *s: torch.randn(*s, device="cuda:0", generator=g)
+    t, d, n = 10, 70, 16
+    nseq = len(cu) - 1
+    out, state = torch.full((t + 4, d), 7.0, device="cuda:0"), torch.full((nseq + 2, d, n), 7.0, device="cuda:0")
+    sss.selective_scan_packed_fwd(r(t, d), r(t, d).abs(), -r(d, n).abs(), r(t, n), r(t, n), cu_seqlens=torch.tensor(
+        cu, dtype=torch.int32, device="cuda:0"), state=state[1:-1], out=out[2:-2])
+    torch.cuda.synchronize()
+    for a in (out[:2], out[-2:], state[0], state[-1]):
+        assert bool((a == 7.0).all())
+
+
+@pytest.mark.gpu
+def test_scan_from_a_negative_boundary():
+    """A first sequence that starts before row 0 is the one that starts at row 0."""
+    import torch
+    import selective_state_space_20_amd as sss
+    g = torch.Generator(device="cuda:0").manual_seed(3)
+    r = lambda *s: torch.randn(*s, device="cuda:0", generator=g)
+    v = (r(10, 70), r(10, 70).abs(), -r(70, 16).abs(), r(10, 16), r(10, 16))
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda:0")
+    assert torch.equal(sss.selective_scan_packed_fwd(*v, cu_seqlens=i32(-5, 10)),
+                       sss.selective_scan_packed_fwd(*v, cu_seqlens=i32(0, 10)))
