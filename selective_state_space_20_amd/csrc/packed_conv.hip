@@ -6,9 +6,9 @@
 //   out[t,d] = bias[d] + sum_{k<W} w[d,k] * u[t-(W-1)+k, d],  then optionally silu,
 // and the slot is left with the last W-1 inputs.  Pure streaming: 2 + 2 bytes per element in
 // bf16 and W fmas.
+#include "seq_walk.h"
 #include "vec.h"
 #include "kernels.h"
-
 
 namespace sss {
 
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(64 * kPConvWaves) void packed_conv_kernel(const cha
     if constexpr (RAGGED) r.template store_from<true>(p, lane_at(at), skip);
     else r.template store<true>(p, lane_at(at));
   };
-  if (tend - t == K && cu[s] <= c0 - H && cu[s + 1] >= tend) {
+  if (tend - t == K && began_before(cu[s], c0 - H + 1) && cu[s + 1] >= tend) {
     R o[K];
 #pragma unroll
     for (int c = 0; c < CPL; c += 2) {
@@ -152,12 +152,12 @@ __global__ __launch_bounds__(64 * kPConvWaves) void packed_conv_kernel(const cha
       if (++s >= g.nseq) break;
       continue;
     }
-    const int beg = min(max(cu[s], 0), t);
-    if (beg < c0 && t - beg < H) {  // the chunk before this one has these tokens
-      t = min(beg + H, end);
+    const ConvPiece piece = conv_piece(cu[s], end, t, c0, tend, H);
+    if (!piece.mine) {
+      t = piece.next;
       continue;
     }
-    const int e = min(end, beg < c0 ? tend : max(tend, beg + H));
+    const int beg = piece.beg, e = piece.next;
     const int slot = sidx != nullptr ? sidx[s] : s;
     const bool kept = state != nullptr && (unsigned)slot < (unsigned)g.slots;
 

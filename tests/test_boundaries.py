@@ -22,6 +22,10 @@ def test_scan_walk_stays_in_range(tmp_path):
     run_native("scan_walk", tmp_path)
 
 
+def test_convolution_walk_stays_in_range(tmp_path):
+    run_native("conv_walk", tmp_path)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("cu", [[-5, 10], [-1, 4, 9, 10], [0, 5, -3, 10], [-2 ** 31, 2 ** 31 - 1], [7, 3, 12, -1, 10]])
 @pytest.mark.parametrize("chunks", [None, 4])
@@ -54,3 +58,38 @@ def test_scan_from_a_negative_boundary():
     i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda:0")
     assert torch.equal(sss.selective_scan_packed_fwd(*v, cu_seqlens=i32(-5, 10)),
                        sss.selective_scan_packed_fwd(*v, cu_seqlens=i32(0, 10)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [2, 4, 8])
+@pytest.mark.parametrize("cu", [[0, 2, 1, 20], [5, 2, 20], [0, 9, 8, 20], [-5, 20], [3, 1, 40, -7, 20], [-2 ** 31, 2 ** 31 - 1]])
+def test_convolution_of_malformed_boundaries(cu, width):
+    """No row before or after x is read (NaN there would reach the results), nothing outside the outputs written."""
+    import torch
+    import selective_state_space_20_amd as sss
+    g = torch.Generator(device="cuda:0").manual_seed(4)
+    r = lambda *s: torch.randn(*s, device="cuda:0", generator=g)
+    t, d = 20, 70
+    nseq = len(cu) - 1
+    x = torch.full((t + 16, d), float("nan"), device="cuda:0")
+    x[8:-8] = r(t, d)
+    out = torch.full((t + 4, d), 7.0, device="cuda:0")
+    state = torch.full((nseq + 2, width - 1, d), 7.0, device="cuda:0")
+    sss.causal_conv1d_packed_fwd(x[8:-8], r(d, width), cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda:0"),
+                                 conv_state=state[1:-1], out=out[2:-2])
+    torch.cuda.synchronize()
+    for a in (out[:2], out[-2:], state[0], state[-1]):
+        assert bool((a == 7.0).all())
+    assert not bool(out.isnan().any()) and not bool(state.isnan().any())
+
+
+@pytest.mark.gpu
+def test_convolution_from_a_negative_boundary():
+    """A first sequence that starts before row 0 is the one that starts at row 0."""
+    import torch
+    import selective_state_space_20_amd as sss
+    g = torch.Generator(device="cuda:0").manual_seed(5)
+    x, w = torch.randn(20, 70, device="cuda:0", generator=g), torch.randn(70, 4, device="cuda:0", generator=g)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda:0")
+    assert torch.equal(sss.causal_conv1d_packed_fwd(x, w, cu_seqlens=i32(-5, 20)),
+                       sss.causal_conv1d_packed_fwd(x, w, cu_seqlens=i32(0, 20)))
