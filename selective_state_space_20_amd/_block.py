@@ -4,6 +4,10 @@ the block.
 
 As in ``_lib``, only argument checks, output allocation and the C call: every step of the
 computation runs in the library's HIP kernels.
+
+``stream`` is the handle of the HIP stream that a call's work is queued on (None: the current one).
+For another one than the current, the caller has it wait for what makes the operands, keeps the
+operands until the work is done, and has the current stream wait before it uses the results.
 """
 from __future__ import annotations
 
@@ -57,29 +61,51 @@ def _dense(t, name, dtype, shape, index):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _out(out, name, like, dtype, shape, index):
+def _stream_of(stream, index):
+    """The Stream object of a handle (0, the default stream's, would make ExternalStream a new one)."""
+    if stream == 0:
+        return _torch.cuda.default_stream(index)
+    return _torch.cuda.ExternalStream(stream, device=index)
+
+
+def _new(like, shape, dtype, stream):
+    """A tensor on like's GPU for the call's work, in memory of the stream that the work runs on: what
+    the current stream's allocator hands out may still be in use by work queued there, which a given
+    other stream does not wait for.  Not handed out again before the current stream, where a result
+    is used as a rule, is done with it either."""
+    if stream is None or stream == _torch._C._cuda_getCurrentRawStream(like.get_device()):
+        return like.new_empty(shape, dtype=dtype)
+    index = like.get_device()
+    current = _torch.cuda.current_stream(index)
+    with _torch.cuda.stream(_stream_of(stream, index)):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(current)
+    return t
+
+
+def _out(out, name, like, dtype, shape, index, stream):
     """The given output, checked, or a new one on like's GPU; returns (tensor, pointer)."""
     if out is None:
-        out = like.new_empty(shape, dtype=dtype)
+        out = _new(like, shape, dtype, stream)
         return out, out.data_ptr()
     return out, _dense(out, name, dtype, shape, index)
 
 
-def _scratch(workspace, nbytes, like):
+def _scratch(workspace, nbytes, like, stream):
     """The given workspace, checked, or a new one; returns (tensor to keep, pointer, bytes)."""
     if workspace is None:
         if nbytes == 0:
             return None, 0, 0
-        workspace = like.new_empty((nbytes,), dtype=_torch.uint8)
+        workspace = _new(like, (nbytes,), _torch.uint8, stream)
         return workspace, workspace.data_ptr(), nbytes
     return (workspace, *_lib._workspace(workspace, like.device))
 
 
 def _keep(stream, index, *tensors):
-    """Memory allocated in the call (on the current stream) that work on a given other stream uses:
-    not handed out again before that work is done."""
+    """Memory of the caller's that work on a given other stream writes: not handed out again before
+    that work is done."""
     if stream is not None and stream != _torch._C._cuda_getCurrentRawStream(index):
-        s = _torch.cuda.ExternalStream(stream, device=_torch.device("cuda", index))
+        s = _stream_of(stream, index)
         for t in tensors:
             if t is not None:
                 t.record_stream(s)
@@ -154,7 +180,7 @@ def causal_conv1d_packed_fwd(x, weight, bias=None, *, cu_seqlens, conv_state=Non
     bp = _dense(bias, "bias", torch.float32, (dim,), gpu)
     sp, slots = _cache(conv_state, "conv_state", x.dtype, (width - 1, dim), gpu)
     nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, conv_state, slots, gpu)
-    o, op = _out(out, "out", x, x.dtype, (tokens, dim), gpu)
+    o, op = _out(out, "out", x, x.dtype, (tokens, dim), gpu, stream)
     if tokens == 0:
         return o
     rc = load().causal_conv1d_packed_fwd(xp, xs, wp, bp, sp, cu, idx, ini, op, tokens, nseq, slots if sp else 0, dim,
@@ -183,7 +209,7 @@ def causal_conv1d_update(x, weight, bias=None, *, conv_state, state_indices=None
     idx = _dense(state_indices, "state_indices", torch.int32, (batch,), gpu)
     if state_indices is None and batch > slots:
         raise ValueError(f"{batch} rows need as many slots or state_indices, the cache has {slots}")
-    o, op = _out(out, "out", x, x.dtype, (batch, dim), gpu)
+    o, op = _out(out, "out", x, x.dtype, (batch, dim), gpu, stream)
     if batch == 0:
         return o
     rc = load().causal_conv1d_update(xp, xs, wp, bp, sp, idx, op, batch, slots, dim, width, code, int(bool(silu)),
@@ -231,17 +257,17 @@ def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, worksp
     bp = _dense(bias, "bias", torch.float32, (dim,), gpu)
     dp = _dense(dout, "dout", dout.dtype, (batch, seqlen, dim), gpu)
     if dx is None:
-        dx = x.new_empty((batch, seqlen, dim))
+        dx = _new(x, (batch, seqlen, dim), x.dtype, stream)
         gp, gb, gr = dx.data_ptr(), seqlen * dim, dim
     else:
         if dx.dtype not in (torch.float32, x.dtype):
             raise ValueError(f"dx must be float32 or {x.dtype}, got {dx.dtype}")
         gp, gb, gr = _blocks(dx, "dx", dx.dtype, (batch, seqlen, dim), gpu)
-    g = {"dx": dx, "dweight": x.new_empty((dim, width), dtype=torch.float32)}
+    g = {"dx": dx, "dweight": _new(x, (dim, width), torch.float32, stream)}
     if bias is not None:
-        g["dbias"] = x.new_empty((dim,), dtype=torch.float32)
+        g["dbias"] = _new(x, (dim,), torch.float32, stream)
     need = causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, code, gpu) if workspace is None else 0
-    workspace, wsp, wsn = _scratch(workspace, need, x)
+    workspace, wsp, wsn = _scratch(workspace, need, x, stream)
     rc = load().causal_conv1d_bwd(xp, xb, xr, wp, bp, dp, gp, gb, gr, g["dweight"].data_ptr(),
                                   g["dbias"].data_ptr() if bias is not None else 0, batch, seqlen, dim, width, code,
                                   _code(dout.dtype, "dout"), _code(dx.dtype, "dx"), int(bool(silu)), wsp, wsn,
@@ -292,11 +318,11 @@ def selective_scan_packed_fwd(x, delta, A, B, C, D=None, z=None, *, cu_seqlens, 
     nseq, cu, idx, ini = _sequences(cu_seqlens, state_indices, has_initial, state, slots, gpu)
     yd = torch.float32 if out is None else out.dtype
     yc = _code(yd, "out")
-    y, yp = _out(out, "out", x, yd, (tokens, dim), gpu)
+    y, yp = _out(out, "out", x, yd, (tokens, dim), gpu, stream)
     if tokens == 0:
         return y
     need = selective_scan_packed_fwd_workspace_size(tokens, dim, n, gpu) if workspace is None else 0
-    workspace, wsp, wsn = _scratch(workspace, need, x)
+    workspace, wsp, wsn = _scratch(workspace, need, x, stream)
     rc = load().selective_scan_packed_fwd(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, cu, idx, ini, yp,
                                           tokens, nseq, slots, dim, n, code, bc, yc, wsp, wsn, _stream(stream, gpu))
     if rc != 0:
@@ -320,7 +346,7 @@ def selective_state_update_slots(x, delta, A, B, C, D=None, z=None, *, state, st
         raise ValueError(f"{batch} rows need as many slots or state_indices, the cache has {slots}")
     yd = torch.float32 if out is None else out.dtype
     yc = _code(yd, "out")
-    y, yp = _out(out, "out", x, yd, (batch, dim), gpu)
+    y, yp = _out(out, "out", x, yd, (batch, dim), gpu, stream)
     if batch == 0:
         return y
     rc = load().selective_state_update_slots(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, idx, yp, batch,
@@ -356,8 +382,8 @@ def rms_norm_gated_fwd(x, weight, z=None, *, eps=1e-5, group_size=None, norm_bef
     oc = _code(od, "z")
     zp, zs = _rows(z, "z", od, rows, dim, gpu) if z is not None else (0, 0)
     wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
-    o, op = _out(out, "out", x, od, (rows, dim), gpu)
-    rstd = x.new_empty((rows, dim // g), dtype=torch.float32) if return_rstd else None
+    o, op = _out(out, "out", x, od, (rows, dim), gpu, stream)
+    rstd = _new(x, (rows, dim // g), torch.float32, stream) if return_rstd else None
     if rows > 0:
         rc = load().rms_norm_gated_fwd(xp, xs, wp, zp, zs, op, rstd.data_ptr() if return_rstd else 0, rows, dim, g,
                                        float(eps), SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc,
@@ -389,17 +415,17 @@ def rms_norm_gated_bwd(dout, x, weight, z=None, *, rstd, group_size=None, norm_b
     zp, zs = _rows(z, "z", od, rows, dim, gpu) if z is not None else (0, 0)
     wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
     rp = _dense(rstd, "rstd", torch.float32, (rows, dim // g), gpu)
-    res = {"dx": x.new_empty((rows, dim)), "dweight": x.new_empty((dim,), dtype=torch.float32)}
+    res = {"dx": _new(x, (rows, dim), x.dtype, stream), "dweight": _new(x, (dim,), torch.float32, stream)}
     gp, gs = 0, 0
     if z is not None:
         if dz is None:
-            res["dz"] = x.new_empty((rows, dim), dtype=od)
+            res["dz"] = _new(x, (rows, dim), od, stream)
             gp, gs = res["dz"].data_ptr(), dim
         else:
             res["dz"] = dz
             gp, gs = _rows(dz, "dz", od, rows, dim, gpu)
     need = rms_norm_gated_bwd_workspace_size(rows, dim, g, gpu) if workspace is None else 0
-    workspace, wsp, wsn = _scratch(workspace, need, x)
+    workspace, wsp, wsn = _scratch(workspace, need, x, stream)
     rc = load().rms_norm_gated_bwd(dp, xp, xs, wp, zp, zs, rp, res["dx"].data_ptr(), gp, gs, res["dweight"].data_ptr(),
                                    rows, dim, g, SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc, wsp, wsn,
                                    _stream(stream, gpu))
@@ -430,12 +456,12 @@ def rms_norm_residual_fwd(x, weight, residual=None, *, post_weight=None, scale=N
     wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
     pp = _dense(post_weight, "post_weight", torch.float32, (dim,), gpu)
     sp = _dense(scale, "scale", torch.float32, (dim,), gpu)
-    o, op = _out(out, "out", x, x.dtype, (rows, dim), gpu)
-    h, ho = _out(residual_out, "residual_out", x, hd, (rows, dim), gpu)
+    o, op = _out(out, "out", x, x.dtype, (rows, dim), gpu, stream)
+    h, ho = _out(residual_out, "residual_out", x, hd, (rows, dim), gpu, stream)
     rstd = rstd_post = None
     if return_rstd:
-        rstd = x.new_empty((rows,), dtype=torch.float32)
-        rstd_post = x.new_empty((rows,), dtype=torch.float32) if post_weight is not None else None
+        rstd = _new(x, (rows,), torch.float32, stream)
+        rstd_post = _new(x, (rows,), torch.float32, stream) if post_weight is not None else None
     if rows > 0:
         rc = load().rms_norm_residual_fwd(xp, xs, hp, hs, pp, sp, wp, op, ho,
                                           0 if rstd_post is None else rstd_post.data_ptr(),
@@ -477,17 +503,17 @@ def rms_norm_residual_bwd(dout, dresidual_out=None, *, residual_out, weight, rst
     sp = _dense(scale, "scale", torch.float32, (dim,), gpu)
     rp = _dense(rstd, "rstd", torch.float32, (rows,), gpu)
     rpp = _dense(rstd_post, "rstd_post", torch.float32, (rows,), gpu) if post_weight is not None else 0
-    vec = lambda: dout.new_empty((dim,), dtype=torch.float32)
-    res = {"dx": dout.new_empty((rows, dim)), "dweight": vec()}
+    vec = lambda: _new(dout, (dim,), torch.float32, stream)
+    res = {"dx": _new(dout, (rows, dim), dout.dtype, stream), "dweight": vec()}
     if want_dresidual:
-        res["dresidual"] = dout.new_empty((rows, dim), dtype=hd)
+        res["dresidual"] = _new(dout, (rows, dim), hd, stream)
     if post_weight is not None:
         res["dpost_weight"] = vec()
     if scale is not None:
         res["dscale"] = vec()
     ptr = lambda k: res[k].data_ptr() if k in res else 0
     need = rms_norm_residual_bwd_workspace_size(rows, dim, gpu) if workspace is None else 0
-    workspace, wsp, wsn = _scratch(workspace, need, dout)
+    workspace, wsp, wsn = _scratch(workspace, need, dout, stream)
     rc = load().rms_norm_residual_bwd(dp, ep, xp, xs, hp, pp, sp, wp, rpp, rp, ptr("dx"), ptr("dresidual"),
                                       ptr("dweight"), ptr("dpost_weight"), ptr("dscale"), rows, dim, float(alpha), xc,
                                       hc, wsp, wsn, _stream(stream, gpu))
