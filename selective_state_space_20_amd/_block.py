@@ -61,26 +61,11 @@ def _dense(t, name, dtype, shape, index):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _stream_of(stream, index):
-    """The Stream object of a handle (0, the default stream's, would make ExternalStream a new one)."""
-    if stream == 0:
-        return _torch.cuda.default_stream(index)
-    return _torch.cuda.ExternalStream(stream, device=index)
-
-
 def _new(like, shape, dtype, stream):
-    """A tensor on like's GPU for the call's work, in memory of the stream that the work runs on: what
-    the current stream's allocator hands out may still be in use by work queued there, which a given
-    other stream does not wait for.  Not handed out again before the current stream, where a result
-    is used as a rule, is done with it either."""
+    """A tensor on like's GPU for the call's work, in memory of the stream that the work runs on."""
     if stream is None or stream == _torch._C._cuda_getCurrentRawStream(like.get_device()):
         return like.new_empty(shape, dtype=dtype)
-    index = like.get_device()
-    current = _torch.cuda.current_stream(index)
-    with _torch.cuda.stream(_stream_of(stream, index)):
-        t = like.new_empty(shape, dtype=dtype)
-    t.record_stream(current)
-    return t
+    return _lib._empty(shape, dtype, like.device, stream)
 
 
 def _out(out, name, like, dtype, shape, index, stream):
@@ -105,7 +90,7 @@ def _keep(stream, index, *tensors):
     """Memory of the caller's that work on a given other stream writes: not handed out again before
     that work is done."""
     if stream is not None and stream != _torch._C._cuda_getCurrentRawStream(index):
-        s = _stream_of(stream, index)
+        s = _lib._stream_of(stream, index)
         for t in tensors:
             if t is not None:
                 t.record_stream(s)

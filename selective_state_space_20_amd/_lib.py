@@ -234,7 +234,7 @@ def selective_scan_bwd(x, delta, A, B, C, D=None, z=None, h0=None, *, dy, dh_las
     if front and states is not None:
         raise ValueError("the delta front end has no saved-states form (states=)")
     _on_device(dev, x=x, delta=delta, z=z, A=A, B=B, C=C, D=D, h0=h0, dy=dy, dh_last=dh_last, delta_bias=delta_bias)
-    e = lambda *sh: torch.empty(sh, dtype=f32, device=dev)
+    e = lambda *sh: _empty(sh, f32, dev, stream)
     g = dict(dx=e(batch, seqlen, dim), ddelta=e(batch, seqlen, dim), dA=e(dim, dstate), dB=e(batch, seqlen, dstate),
              dC=e(batch, seqlen, dstate))
     g["dD"] = e(dim) if D is not None else None
@@ -244,7 +244,7 @@ def selective_scan_bwd(x, delta, A, B, C, D=None, z=None, h0=None, *, dy, dh_las
         g["ddelta_bias"] = e(dim)
     wsb = selective_scan_bwd_workspace_size(batch, seqlen, dim, dstate, dev.index or 0)
     if workspace is None:
-        workspace = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(wsb, 1), torch.uint8, dev, stream)
     wsp, wsn = _workspace(workspace, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
     if front:
@@ -291,7 +291,7 @@ def causal_conv1d_fwd(x, weight, bias=None, *, silu=False, out=None, stream=None
     _need(x, "x", io, (batch, seqlen, dim), dev)
     _need(weight, "weight", torch.float32, (dim, width), dev)
     _need(bias, "bias", torch.float32, (dim,), dev)
-    o = out if out is not None else torch.empty((batch, seqlen, dim), dtype=io, device=dev)
+    o = out if out is not None else _empty((batch, seqlen, dim), io, dev, stream)
     _need(o, "out", io, (batch, seqlen, dim), dev)
     _on_device(dev, x=x, weight=weight, bias=bias, out=o)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
@@ -327,6 +327,28 @@ def elementwise_scan_workspace_size(batch, seqlen, dim, device=0) -> int:
 # ---------------------------------------------------------------- torch-tensor entry points
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
+
+
+def _stream_of(stream, index):
+    """The Stream object of a handle (0, the default stream's, would make ExternalStream a new one)."""
+    import torch
+    return torch.cuda.default_stream(index) if stream == 0 else torch.cuda.ExternalStream(stream, device=index)
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call's work, in memory of the stream that the work runs on: what the current
+    stream's allocator hands out may still be in use by work queued there, which a given other stream
+    does not wait for.  Not handed out again before the current stream, where a result is used as a
+    rule, is done with it either."""
+    import torch
+    if stream is None or device.type != "cuda" or stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    index = device.index or 0
+    current = torch.cuda.current_stream(index)
+    with torch.cuda.stream(_stream_of(stream, index)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
 
 
 def _need(t, name, dtype, shape, device):
@@ -403,9 +425,9 @@ def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, return_las
     _need(C, "C", f32, bc_shape, dev)
     _need(D, "D", f32, (dim,), dev)
     _need(h0, "h0", f32, (batch, dim, dstate), dev)
-    y = out if out is not None else torch.empty(io_shape, dtype=f32, device=dev)
+    y = out if out is not None else _empty(io_shape, f32, dev, stream)
     hl = out_last if out_last is not None else (
-        torch.empty((batch, dim, dstate), dtype=f32, device=dev) if return_last else None)
+        _empty((batch, dim, dstate), f32, dev, stream) if return_last else None)
     _need(y, "out", f32, io_shape, dev)
     _need(hl, "out_last", f32, (batch, dim, dstate), dev)
     flags = ((SSS_EXACT_ZOH if exact_zoh else 0) | (SSS_DELTA_SOFTPLUS if delta_softplus else 0)
@@ -414,7 +436,7 @@ def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, return_las
     _on_device(dev, x=x, delta=delta, z=z, A=A, B=B, C=C, D=D, h0=h0, out=y, out_last=hl, delta_bias=delta_bias)
     wsb = selective_scan_fwd_ex_workspace_size(batch, seqlen, dim, dstate, flags, dev.index or 0)
     if workspace is None and wsb > 0:
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        workspace = _empty(wsb, torch.uint8, dev, stream)
     wsp, wsn = _workspace(workspace, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
     if states is not None:  # selective_scan_fwd_save: the plain form, keeping the segment entering states
@@ -453,7 +475,7 @@ def selective_state_update(x, delta, A, B, C, D=None, z=None, *, state, out=None
     _need(C, "C", f32, (batch, dstate), dev)
     _need(D, "D", f32, (dim,), dev)
     _need(state, "state", f32, (batch, dim, dstate), dev)
-    y = out if out is not None else torch.empty((batch, dim), dtype=f32, device=dev)
+    y = out if out is not None else _empty((batch, dim), f32, dev, stream)
     _need(y, "out", f32, (batch, dim), dev)
     _on_device(dev, x=x, delta=delta, z=z, A=A, B=B, C=C, D=D, state=state, out=y)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
@@ -474,15 +496,15 @@ def elementwise_scan(x, A, B, C, h0=None, *, return_last=True, out=None, out_las
     for t, n in ((x, "x"), (A, "A"), (B, "B"), (C, "C")):
         _need(t, n, f32, (batch, seqlen, dim), dev)
     _need(h0, "h0", f32, (batch, dim), dev)
-    y = out if out is not None else torch.empty((batch, seqlen, dim), dtype=f32, device=dev)
+    y = out if out is not None else _empty((batch, seqlen, dim), f32, dev, stream)
     hl = out_last if out_last is not None else (
-        torch.empty((batch, dim), dtype=f32, device=dev) if return_last else None)
+        _empty((batch, dim), f32, dev, stream) if return_last else None)
     _need(y, "out", f32, (batch, seqlen, dim), dev)
     _need(hl, "out_last", f32, (batch, dim), dev)
     _on_device(dev, x=x, A=A, B=B, C=C, h0=h0, out=y, out_last=hl)
     wsb = elementwise_scan_workspace_size(batch, seqlen, dim, dev.index or 0)
     if workspace is None and wsb > 0:
-        workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+        workspace = _empty(wsb, torch.uint8, dev, stream)
     wsp, wsn = _workspace(workspace, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
     rc = elementwise_scan_raw(_ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(h0), _ptr(y), _ptr(hl), batch, seqlen, dim,

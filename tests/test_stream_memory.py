@@ -3,6 +3,7 @@ allocator may hand out a block that kernels queued there still use, which work o
 stream would overwrite.  On the CPU with stand-ins for the tensors, the library and the current stream;
 on the GPU with the allocator itself."""
 import math
+import sys
 import types
 
 import pytest
@@ -102,9 +103,30 @@ def block_calls(t):
     }
 
 
+def dense_calls(t):
+    """The same for the calls on equal-length batches."""
+    x, m, A, h, v = t((2, 6, 8)), t((2, 6, 4)), t((8, 4)), t((2, 8, 4)), t((8,))
+    e, r, rm = t((2, 6, 8)), t((2, 8)), t((2, 4))
+    return {
+        "dense scan": lambda **k: sss.selective_scan_fwd(x, x, A, m, m, **k),
+        "dense scan gradients": lambda **k: sss.selective_scan_bwd(x, x, A, m, m, dy=x, **k),
+        "dense scan gradients, bias": lambda **k: sss.selective_scan_bwd(x, x, A, m, m, v, x, h, dy=x, delta_bias=v, **k),
+        "dense step": lambda **k: sss.selective_state_update(r, r, A, rm, rm, state=h, **k),
+        "dense conv": lambda **k: sss.causal_conv1d_fwd(x, t((8, 4)), v, **k),
+        "elementwise scan": lambda **k: sss.elementwise_scan(e, e, e, e, **k),
+    }
+
+
 BLOCK = list(block_calls(lambda *a: None).keys())
 MADE = {"conv": 1, "conv step": 1, "conv gradients": 4, "scan": 2, "scan step": 1, "gated norm": 2,
-        "gated norm gradients": 4, "residual norm": 4, "residual norm gradients": 6}
+        "gated norm gradients": 4, "residual norm": 4, "residual norm gradients": 6,
+        "dense scan": 3, "dense scan gradients": 7, "dense scan gradients, bias": 10, "dense step": 1, "dense conv": 1,
+        "elementwise scan": 3}
+DENSE = list(dense_calls(lambda *a: None).keys())
+
+
+def calls(t):
+    return {**block_calls(t), **dense_calls(t)}
 
 
 @pytest.fixture
@@ -113,31 +135,33 @@ def gpu(monkeypatch):
         g, lib = Gpu(current), Library()
         for m in (_block, _lib):
             monkeypatch.setattr(m, "load", lambda: lib)
-        monkeypatch.setattr(_block, "_torch", g.torch())
-        monkeypatch.setattr(_block, "torch_", lambda: _block._torch)
+        stand_in = g.torch()
+        monkeypatch.setitem(sys.modules, "torch", stand_in)
+        monkeypatch.setattr(_block, "_torch", stand_in)
+        monkeypatch.setattr(_block, "torch_", lambda: stand_in)
         monkeypatch.setattr(_lib, "_lib", lib)
         return g, lib
     return make
 
 
-@pytest.mark.parametrize("name", BLOCK)
+@pytest.mark.parametrize("name", BLOCK + DENSE)
 @pytest.mark.parametrize("current, given", [(0, 7), (5, 7), (5, 0)])
 def test_memory_of_the_given_stream(gpu, name, current, given):
     g, lib = gpu(current)
-    res = block_calls(g.tensor)[name](stream=given)
+    res = calls(g.tensor)[name](stream=given)
     assert lib.streams == [given] and len(g.made) == MADE[name]
     assert [t.stream for t in g.made] == [given] * len(g.made)
     results = res.values() if isinstance(res, dict) else res if isinstance(res, tuple) else [res]
-    for t in results:  # used on the current stream as a rule: not freed under it
+    for t in (t for t in results if t is not None):  # used on the current stream as a rule: not freed under it
         assert current in t.recorded and "a new stream" not in t.recorded
     assert g.now == [current]
 
 
-@pytest.mark.parametrize("name", BLOCK)
+@pytest.mark.parametrize("name", BLOCK + DENSE)
 @pytest.mark.parametrize("current, given", [(0, None), (5, None), (5, 5)])
 def test_memory_of_the_current_stream(gpu, name, current, given):
     g, lib = gpu(current)
-    block_calls(g.tensor)[name](stream=given)
+    calls(g.tensor)[name](stream=given)
     assert lib.streams == [current] and len(g.made) == MADE[name]
     assert all(t.stream == current and t.recorded == [] for t in g.made)
 
