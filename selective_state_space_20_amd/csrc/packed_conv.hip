@@ -214,8 +214,11 @@ __global__ __launch_bounds__(64 * kPConvWaves) void packed_conv_kernel(const cha
       r.set(o);
       put(r, t);
     };
-    // The chunk's tokens are in registers, those after it are not.  Two loops: one that takes each
-    // token from either has been compiled (8-byte lanes, fp32) with a copy of the window lost.
+    // The chunk's tokens are in registers, those after it are not.  Two loops: in one that takes each
+    // token from either, the compiler (ROCm 7.2.0) lost a copy of the window in every fp32 kernel of
+    // 8 bytes per lane and three taps or more.  Of a row's two registers, set by a select or by a load, it
+    // took the upper one for undefined at the loop's head, and dropped `window = the next` of the
+    // lane's second channel.  tests/test_codegen.py looks for such copies in the machine code.
     for (const int last = min(e, c0 + K); t < last; ++t) {
       R cur = q[H];
 #pragma unroll
