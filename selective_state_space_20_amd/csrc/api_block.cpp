@@ -174,14 +174,34 @@ int scan_impl(const void* x, int64_t x_stride, const void* delta, int64_t delta_
   return status_of(launch_packed_scan(a, pl, s));
 }
 
-// rows of a norm: at most one workgroup of 256 to 1024 threads per row and group, 2^31 threads
-int norm_dims(int64_t rows, int64_t dim, int64_t group) {
+constexpr double kMaxThreads = 4294967295.0;  // of a launch
+
+// rows of a norm: norm_lanes threads for each row and group, in workgroups of at most 1024
+int norm_dims(int64_t rows, int64_t dim, int64_t group, bool fp32) {
   if (rows < 0 || dim < 1 || group < 1 || rows > kMaxTokens || dim > kMaxRowDim || dim % group != 0)
     return SSS_ERR_BAD_DIM;
   if (group > kMaxNormDim) return SSS_ERR_UNSUPPORTED;
-  const double threads = group <= 64 ? 8.0 : group <= 1024 ? 64.0 : group <= 8192 ? 256.0 : group <= 16384 ? 512.0 : 1024.0;
-  if (((double)rows * (double)(dim / group) + 32.0) * threads > 2147483647.0) return SSS_ERR_BAD_DIM;
+  if ((double)rows * (double)(dim / group) * (double)norm_lanes(group, fp32) + 1024.0 > kMaxThreads) return SSS_ERR_BAD_DIM;
   return SSS_OK;
+}
+
+// its gradients: each group a workgroup at least (and otherwise no more than four per CU)
+int norm_bwd_dims(int64_t rows, int64_t dim, int64_t group, bool fp32) {
+  const int st = norm_dims(rows, dim, group, fp32);
+  if (st == SSS_OK && (double)(dim / group) * (double)std::max(256, norm_lanes(group, fp32)) > kMaxThreads)
+    return SSS_ERR_BAD_DIM;
+  return st;
+}
+
+// bytes for either kernel shape: a query does not know the types
+size_t norm_bwd_bytes(int64_t rows, int64_t dim, int64_t group, int vectors, int device) {
+  int cus = device_cus(device);
+  if (cus <= 0) cus = 256;
+  size_t most = 0;
+  for (const bool fp32 : {false, true})
+    if (norm_bwd_dims(rows, dim, group, fp32) == SSS_OK)
+      most = std::max(most, plan_norm_bwd(rows, group, dim / group, vectors, fp32, cus).ws_total);
+  return most;
 }
 
 }  // namespace
@@ -192,7 +212,8 @@ int rms_norm_gated_fwd(const void* x, int64_t x_stride, const float* weight, con
                        float* rstd, int64_t rows, int64_t dim, int64_t group, float eps, unsigned flags, int x_dtype,
                        int out_dtype, sss_stream_t stream) {
   if (!x || !weight || !out) return SSS_ERR_NULL_ARG;
-  const int st = norm_dims(rows, dim, group);
+  const bool fp32 = x_dtype == SSS_F32 || out_dtype == SSS_F32;
+  const int st = norm_dims(rows, dim, group, fp32);
   if (st != SSS_OK) return st;
   if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype) || (flags & ~(unsigned)SSS_NORM_BEFORE_GATE) != 0)
     return SSS_ERR_UNSUPPORTED;
@@ -226,12 +247,7 @@ int rms_norm_gated_fwd(const void* x, int64_t x_stride, const float* weight, con
 }
 
 size_t rms_norm_gated_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, int device) {
-  if (norm_dims(rows, dim, group) != SSS_OK) return 0;
-  int cus = device_cus(device);
-  if (cus <= 0) cus = 256;
-  // of either kernel shape: the query does not know the types
-  return std::max(plan_norm_bwd(rows, group, dim / group, 1, false, cus).ws_total,
-                  plan_norm_bwd(rows, group, dim / group, 1, true, cus).ws_total);
+  return norm_bwd_bytes(rows, dim, group, 1, device);
 }
 
 int rms_norm_gated_bwd(const void* dout, const void* x, int64_t x_stride, const float* weight, const void* z,
@@ -239,7 +255,8 @@ int rms_norm_gated_bwd(const void* dout, const void* x, int64_t x_stride, const 
                        int64_t rows, int64_t dim, int64_t group, unsigned flags, int x_dtype, int out_dtype,
                        void* workspace, size_t workspace_bytes, sss_stream_t stream) {
   if (!dweight || (rows != 0 && (!dout || !x || !weight || !rstd || !dx || (z && !dz)))) return SSS_ERR_NULL_ARG;
-  const int st = norm_dims(rows, dim, group);
+  const bool fp32 = x_dtype == SSS_F32 || out_dtype == SSS_F32;
+  const int st = norm_bwd_dims(rows, dim, group, fp32);
   if (st != SSS_OK) return st;
   if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype) || (flags & ~(unsigned)SSS_NORM_BEFORE_GATE) != 0)
     return SSS_ERR_UNSUPPORTED;
@@ -260,7 +277,6 @@ int rms_norm_gated_bwd(const void* dout, const void* x, int64_t x_stride, const 
   if (!r.ok()) return SSS_ERR_ALIAS;
   const int cus = current_device_cus();
   if (cus <= 0) return SSS_ERR_HIP;
-  const bool fp32 = x_dtype == SSS_F32 || out_dtype == SSS_F32;
   const NormPlan pl = plan_norm_bwd(rows, group, dim / group, 1, fp32, cus);
   if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
   r.output(workspace, (int64_t)pl.ws_total, 16);
@@ -292,7 +308,8 @@ int rms_norm_residual_fwd(const void* x, int64_t x_stride, const void* residual,
                           void* residual_out, float* rstd_post, float* rstd, int64_t rows, int64_t dim, float alpha,
                           float eps, int io_dtype, int residual_dtype, sss_stream_t stream) {
   if (!x || !weight || !out || !residual_out) return SSS_ERR_NULL_ARG;
-  const int st = norm_dims(rows, dim, dim);
+  const bool fp32 = io_dtype == SSS_F32 || residual_dtype == SSS_F32;
+  const int st = norm_dims(rows, dim, dim, fp32);
   if (st != SSS_OK) return st;
   if (!dtype_ok(io_dtype) || !dtype_ok(residual_dtype)) return SSS_ERR_UNSUPPORTED;
   if (!stride_ok(x_stride, dim) || (residual && !stride_ok(residual_stride, dim))) return SSS_ERR_BAD_DIM;
@@ -334,11 +351,7 @@ int rms_norm_residual_fwd(const void* x, int64_t x_stride, const void* residual,
 }
 
 size_t rms_norm_residual_bwd_workspace_size(int64_t rows, int64_t dim, int device) {
-  if (norm_dims(rows, dim, dim) != SSS_OK) return 0;
-  int cus = device_cus(device);
-  if (cus <= 0) cus = 256;
-  // of either kernel shape: the query does not know the types
-  return std::max(plan_norm_bwd(rows, dim, 1, 3, false, cus).ws_total, plan_norm_bwd(rows, dim, 1, 3, true, cus).ws_total);
+  return norm_bwd_bytes(rows, dim, dim, 3, device);
 }
 
 int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const void* x, int64_t x_stride,
@@ -350,7 +363,8 @@ int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const voi
   if (rows != 0 && (!dout || !residual_out || !weight || !rstd || !dx || (post_weight && !rstd_post) ||
                     ((post_weight || scale) && !x)))
     return SSS_ERR_NULL_ARG;
-  const int st = norm_dims(rows, dim, dim);
+  const bool fp32 = io_dtype == SSS_F32 || residual_dtype == SSS_F32;
+  const int st = norm_bwd_dims(rows, dim, dim, fp32);
   if (st != SSS_OK) return st;
   if (!dtype_ok(io_dtype) || !dtype_ok(residual_dtype)) return SSS_ERR_UNSUPPORTED;
   if (x && !stride_ok(x_stride, dim)) return SSS_ERR_BAD_DIM;
@@ -375,7 +389,6 @@ int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const voi
   if (!r.ok()) return SSS_ERR_ALIAS;
   const int cus = current_device_cus();
   if (cus <= 0) return SSS_ERR_HIP;
-  const bool fp32 = io_dtype == SSS_F32 || residual_dtype == SSS_F32;
   const NormPlan pl = plan_norm_bwd(rows, dim, 1, 3, fp32, cus);
   if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
   r.output(workspace, (int64_t)pl.ws_total, 16);

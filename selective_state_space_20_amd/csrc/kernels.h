@@ -285,7 +285,8 @@ struct ResNormArgs {
   int x_bf16, h_bf16;
 };
 
-// fp32: the residual norm with an fp32 tensor (its kernels take other shapes)
+// fp32: one of the call's tensors is (its kernels take other shapes)
+int norm_lanes(int64_t group, bool fp32);  // lanes that share a row of a group
 NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, bool fp32, int num_cus);
 hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t stream);
 hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, const NormPlan& plan, hipStream_t stream);

@@ -515,6 +515,8 @@ static NormShape norm_shape(int64_t G, bool fp32) {
   return {v, 1024, 4};
 }
 
+int norm_lanes(int64_t group, bool fp32) { return norm_shape(group, fp32).tpr; }
+
 NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors, bool fp32, int num_cus) {
   NormPlan pl{};
   const NormShape sh = norm_shape(group, fp32);

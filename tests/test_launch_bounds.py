@@ -1,0 +1,59 @@
+"""Calls whose launch would have more threads than a launch can have are refused before any device work
+(CPU: fake addresses, far apart, never dereferenced); those below that run."""
+import pytest
+
+from selective_state_space_20_amd import load
+
+BAD_DIM = -2
+P = 1 << 44
+F32, BF16 = 0, 1
+MAX_THREADS = (1 << 32) - 1
+
+
+def gated(rows, group, x, out):
+    return load().rms_norm_gated_fwd(P, group, 2 * P, 3 * P, group, 4 * P, 5 * P, rows, group, group, 1e-5, 0, x, out, 0)
+
+
+def gated_bwd(rows, dim, group, x, out):
+    return load().rms_norm_gated_bwd(P, 2 * P, dim, 3 * P, 4 * P, dim, 5 * P, 6 * P, 7 * P, dim, 8 * P, rows, dim, group, 0,
+                                     x, out, 9 * P, 1 << 40, 0)
+
+
+def residual(rows, dim, io, res):
+    return load().rms_norm_residual_fwd(P, dim, 2 * P, dim, 3 * P, 4 * P, 5 * P, 6 * P, 7 * P, 8 * P, 9 * P, rows, dim, 1.0,
+                                        1e-5, io, res, 0)
+
+
+# lanes that share a row, by its length: with an fp32 tensor, without
+LANES = [(4, 8, 8), (32, 8, 8), (33, 16, 8), (64, 16, 8), (65, 32, 16), (512, 64, 64), (513, 256, 64), (1024, 256, 64),
+         (1025, 256, 256), (3072 + 4, 512, 256), (6144, 512, 256), (6145, 512, 512), (8192, 512, 512), (20000, 1024, 1024)]
+
+
+@pytest.mark.parametrize("n, fp32, bf16", LANES)
+def test_norm_launches_are_counted_in_the_lanes_they_have(n, fp32, bf16):
+    for x, out in ((F32, BF16), (BF16, F32), (F32, F32), (BF16, BF16)):
+        rows = MAX_THREADS // (bf16 if (x, out) == (BF16, BF16) else fp32) + 1
+        assert gated(rows, n, x, out) == BAD_DIM and residual(rows, n, x, out) == BAD_DIM
+        assert gated_bwd(rows, n, n, x, out) == BAD_DIM
+
+
+def test_norm_gradients_of_too_many_groups():
+    assert gated_bwd(1, 1 << 24, 1, BF16, BF16) == BAD_DIM
+    assert load().rms_norm_gated_bwd_workspace_size(1, 1 << 24, 1, 0) == 0
+
+
+@pytest.mark.gpu
+def test_norm_of_more_than_2_31_threads():
+    import torch
+    import selective_state_space_20_amd as sss
+    rows, at = 300_000_000, (1 << 31) // 8  # eight lanes per row
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device="cuda:0")
+    w = torch.rand(8, device="cuda:0")
+    spots = [slice(0, 64), slice(at - 64, at + 64), slice(rows - 64, rows)]
+    for s in spots:
+        x[s] = torch.randn_like(x[s], dtype=torch.float32).bfloat16()
+    out = sss.rms_norm_gated_fwd(x, w)
+    for s in spots:
+        assert torch.equal(out[s], sss.rms_norm_gated_fwd(x[s].clone(), w))
+    del x, out
+    torch.cuda.empty_cache()
