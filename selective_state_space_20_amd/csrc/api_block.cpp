@@ -17,6 +17,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // token numbers are 32-bit on the device
 constexpr int64_t kMaxRowDim = (int64_t)1 << 24;  // as the scan's dim; also the largest row stride
+constexpr double kMaxThreads = 4294967295.0;      // of a launch
 
 bool dtype_ok(int t) { return t == SSS_F32 || t == SSS_BF16; }
 int64_t dtype_size(int t) { return t == SSS_BF16 ? 2 : 4; }
@@ -99,6 +100,7 @@ int scan_impl(const void* x, int64_t x_stride, const void* delta, int64_t delta_
   const int st = scan_dims(tokens, nseq, slots, dim, dstate);
   if (st != SSS_OK) return st;
   if (state && (slots < 1 || (!state_indices && nseq > slots))) return SSS_ERR_BAD_DIM;
+  if (step && slot_update_threads(tokens, dim, dstate) > kMaxThreads) return SSS_ERR_BAD_DIM;
   if (!dtype_ok(io_dtype) || !dtype_ok(bc_dtype) || !dtype_ok(y_dtype)) return SSS_ERR_UNSUPPORTED;
   if ((flags & ~(unsigned)SSS_DELTA_SOFTPLUS) != 0) return SSS_ERR_UNSUPPORTED;
   if (!stride_ok(x_stride, dim) || !stride_ok(delta_stride, dim) || (z && !stride_ok(z_stride, dim)) ||
@@ -154,11 +156,7 @@ int scan_impl(const void* x, int64_t x_stride, const void* delta, int64_t delta_
   a.y_bf16 = y_dtype == SSS_BF16;
   a.softplus = (flags & SSS_DELTA_SOFTPLUS) != 0;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (step) {
-    // one workgroup of 256 lanes per 256 pieces of four states; 32-bit grid
-    if ((double)tokens * ((double)dim * (double)dstate / 256.0 + 1.0) > 2147483647.0) return SSS_ERR_BAD_DIM;
-    return status_of(launch_slot_update(a, s));
-  }
+  if (step) return status_of(launch_slot_update(a, s));
   const PackedScanPlan pl = plan_packed_scan(tokens, dim, dstate, cus);
   if ((double)pl.chunks * (double)((dim + 63) / 64) > (double)((int64_t)1 << 24)) return SSS_ERR_BAD_DIM;
   if (pl.ws_total > 0) {
@@ -173,8 +171,6 @@ int scan_impl(const void* x, int64_t x_stride, const void* delta, int64_t delta_
                  io_dtype == SSS_BF16 ? "bf16" : "f32", pl.chunks, (long long)pl.K, pl.ws_total);
   return status_of(launch_packed_scan(a, pl, s));
 }
-
-constexpr double kMaxThreads = 4294967295.0;  // of a launch
 
 // rows of a norm: norm_lanes threads for each row and group, in workgroups of at most 1024
 int norm_dims(int64_t rows, int64_t dim, int64_t group, bool fp32) {

@@ -235,6 +235,7 @@ PackedScanPlan plan_packed_scan(int64_t tokens, int64_t dim, int64_t dstate, int
 hipError_t launch_packed_scan(const PackedScanArgs& a, const PackedScanPlan& plan, hipStream_t stream);
 hipError_t launch_pscan_carry(const float* A, const float* ends, const float* sums, const int32_t* flags, float* enter,
                               int dstate, int dim, int chunks, hipStream_t stream);
+double slot_update_threads(int64_t rows, int64_t dim, int64_t dstate);  // of its launch
 hipError_t launch_slot_update(const PackedScanArgs& a, hipStream_t stream);
 
 // Norms around the block (norms.hip).  Pointers marked nullable may be null.

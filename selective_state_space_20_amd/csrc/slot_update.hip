@@ -13,6 +13,8 @@
 #include "vec.h"
 #include "kernels.h"
 
+#include <algorithm>
+
 namespace sss {
 
 typedef float slot_f4 __attribute__((ext_vector_type(4)));
@@ -163,9 +165,17 @@ static hipError_t run_slots_r(const PackedScanArgs& a, hipStream_t stream) {
 // Two rows per thread: 37 us at 256 rows x 5120 x 16 with the states loaded past the caches and
 // stored through them, against 43 with four rows and cached loads, 39 with four and past the
 // caches both ways, 40 with one row.
+constexpr int kSlotRows = 2;
+
 template <int NS, bool BF16>
 static hipError_t run_slots(const PackedScanArgs& a, hipStream_t stream) {
-  return run_slots_r<NS, BF16, 2>(a, stream);
+  return run_slots_r<NS, BF16, kSlotRows>(a, stream);
+}
+
+// as run_slots_r: four states per lane (or all of fewer), whole workgroups per group of rows
+double slot_update_threads(int64_t rows, int64_t dim, int64_t dstate) {
+  const int64_t lanes = dim * std::max<int64_t>(dstate / 4, 1);
+  return (double)((rows + kSlotRows - 1) / kSlotRows) * (double)((lanes + 255) / 256) * 256.0;
 }
 
 template <bool BF16>

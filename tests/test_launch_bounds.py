@@ -42,6 +42,41 @@ def test_norm_gradients_of_too_many_groups():
     assert load().rms_norm_gated_bwd_workspace_size(1, 1 << 24, 1, 0) == 0
 
 
+def step(batch, dim, dstate):
+    return load().selective_state_update_slots(P, dim, 2 * P, dim, 3 * P, 4 * P, dstate, 5 * P, dstate, 0, 0, 0, 0, 0, 6 * P,
+                                               7 * P, 8 * P, batch, 4, dim, dstate, BF16, BF16, F32, 0)
+
+
+@pytest.mark.parametrize("batch, dim, dstate", [(1 << 17, 1 << 14, 16), ((1 << 19) - 1, 1 << 16, 1), (1 << 25, 100, 4),
+                                                (1 << 17, 4090, 64)])
+def test_scan_step_launches_are_counted_in_threads(batch, dim, dstate):
+    """Two rows per thread, four states per lane."""
+    assert step(batch, dim, dstate) == BAD_DIM
+
+
+@pytest.mark.gpu
+def test_scan_step_below_the_bound():
+    """A batch of which nearly all rows are padding: 2^31 threads and more."""
+    import torch
+    import selective_state_space_20_amd as sss
+    batch, dim, n = 1 << 20, 4096, 4
+    one = lambda *s: torch.full(s, 0.5, device="cuda:0")
+    x = torch.full((batch, dim), 0.5, dtype=torch.bfloat16, device="cuda:0")
+    bc = one(batch, n)
+    state = one(2, dim, n)
+    idx = torch.full((batch,), -1, dtype=torch.int32, device="cuda:0")
+    idx[0], idx[-1] = 0, 1
+    y = sss.selective_state_update_slots(x, x, -one(dim, n), bc, bc, state=state, state_indices=idx,
+                                         out=torch.empty(batch, dim, dtype=torch.bfloat16, device="cuda:0"))
+    few = one(1, dim, n)
+    want = sss.selective_state_update_slots(x[:2].clone(), x[:2].clone(), -one(dim, n), bc[:2], bc[:2], state=few,
+                                            state_indices=torch.tensor([0, -1], dtype=torch.int32, device="cuda:0")).bfloat16()
+    assert torch.equal(y[0], want[0]) and torch.equal(y[-1], want[0]) and torch.equal(state, few.expand(2, dim, n))
+    assert bool((y[1:-1] == want[1]).all())
+    del x, y
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.gpu
 def test_norm_of_more_than_2_31_threads():
     import torch
