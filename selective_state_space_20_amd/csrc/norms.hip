@@ -523,11 +523,12 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
   const int rpb = sh.tpr < 256 ? 256 / sh.tpr : 1;
   // Four workgroups per CU (two of more than 256 lanes), but six rows for each as long as every CU
   // has one: a workgroup leaves a row of partials for each vector of parameters (3000 x 5121
-  // fp32 with three of them: 108 us with six rows, 121 with three).
+  // fp32 with three of them: 108 us with six rows, 121 with three).  No more than there are sets of
+  // the rows that a workgroup takes at once, 32 of the shortest groups'.
   const int64_t sets = std::max<int64_t>(1, (rows + rpb - 1) / rpb), cus = std::max(num_cus, 1);
   const int64_t want = std::max<int64_t>(1, cus * (sh.tpr > 256 ? 2 : 4) / groups);
   const int64_t one_each = std::max<int64_t>(1, std::min<int64_t>(sets, cus / groups));
-  pl.nblk = (int)std::min<int64_t>(want, std::max<int64_t>(one_each, rows / 6));
+  pl.nblk = (int)std::min({want, sets, std::max<int64_t>(one_each, rows / 6)});
   pl.ws_total = (size_t)pl.nblk * vectors * group * groups * 4;
   return pl;
 }
