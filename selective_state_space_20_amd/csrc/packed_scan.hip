@@ -106,7 +106,7 @@ __global__ __launch_bounds__(128, pscan_min_waves(NS)) void packed_scan_kernel(
 
   float a2[NS], h[NS];
 #pragma unroll
-  for (int n = 0; n < NS; ++n) a2[n] = fmaxf(A[(int64_t)dc * NS + n] * kLog2e, -kFltMax);  // -inf clamped: 0*a2 = 0
+  for (int n = 0; n < NS; ++n) a2[n] = decay_rate(A[(int64_t)dc * NS + n]);
   const float dbv = ((FL & kFront) != 0 && dbias != nullptr) ? dbias[dc] : 0.0f;
   const float Dd = (PASS == 2 && Dsk != nullptr) ? Dsk[dc] : 0.0f;
   constexpr bool has_z = PASS == 2 && HAS_Z, yb = YB;
@@ -431,7 +431,7 @@ static __global__ __launch_bounds__(256) void pscan_carry_kernel(const float* __
   const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= per) return;
   const int n = (int)(idx / D), d = (int)(idx - (int64_t)n * D);
-  const float a2 = fmaxf(A[(int64_t)d * N + n] * kLog2e, -kFltMax);
+  const float a2 = decay_rate(A[(int64_t)d * N + n]);
   const int r0 = (int)blockIdx.y * range, r1 = min(r0 + range, last);  // chunks 0..last-1 have flags
   float h = 0.0f;
   bool on = false;

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256) void slot_update_kernel(const char* __restrict
     float hn[PL], part = 0.0f;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const float a2 = fmaxf(av.get(i) * kLog2e, -kFltMax);  // -inf clamped: 0*a2 = 0
+      const float a2 = decay_rate(av.get(i));
       hn[i] = __builtin_fmaf(fast_exp2(dt * a2), hv[r].get(i), dx * bv[r][i]);
       part = __builtin_fmaf(cv[r][i], hn[i], part);
     }
