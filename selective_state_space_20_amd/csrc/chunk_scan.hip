@@ -82,7 +82,7 @@ __global__ __launch_bounds__(64 * kChunkWaves, 2) void sel_chunk_kernel(ChunkArg
 
   float a2[NS];
 #pragma unroll
-  for (int n = 0; n < NS; ++n) a2[n] = fmaxf(g.A[dc * N + n] * kLog2e, -kFltMax);
+  for (int n = 0; n < NS; ++n) a2[n] = decay_rate(g.A[dc * N + n]);
   const float Dd = g.Dsk ? g.Dsk[dc] : 0.0f;
   // the states this wave scans, and their entering value for the current chunk
   float carry[SPW];

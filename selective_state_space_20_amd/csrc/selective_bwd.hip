@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256) void sel_bwd_carry(const float* __restrict__ A
   if (idx >= batch * per_b) return;
   const int64_t b = idx / per_b, rem = idx - b * per_b;
   const int64_t n = rem / D, d = rem - n * D;
-  const float a2 = fmaxf(A[d * N + n] * kLog2e, -kFltMax);
+  const float a2 = decay_rate(A[d * N + n]);
   float cur = dh_last ? dh_last[(b * D + d) * N + n] : 0.0f;
   const int64_t sstride = batch * per_b, dstride = batch * D;
   float* slot = slots + b * per_b + rem;
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(64, bwd_min_waves(NS)) void sel_bwd_kernel(
   const int64_t mu_stride = g.S > 1 ? g.D : 1;
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
-    a2[n] = fmaxf(A[q.dc * NS + n] * kLog2e, -kFltMax);
+    a2[n] = decay_rate(A[q.dc * NS + n]);
     mu[n] = 0.0f;
     dacc[n] = 0.0f;
   }

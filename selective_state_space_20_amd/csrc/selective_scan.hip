@@ -195,7 +195,7 @@ __global__ __launch_bounds__(256, min_waves_sel(NS, FL, BF16, PASS)) void sel_se
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
     const float an = A[dc * N + n];
-    a2[n] = fmaxf(an * kLog2e, -kFltMax);  // -inf clamped so that 0*a2 = 0
+    a2[n] = decay_rate(an);
     if constexpr (zoh) {
       ia[n] = fabsf(an) >= 0x1p-64f ? 1.0f / an : 0.0f;
       amin = fminf(amin, fabsf(an));
@@ -859,7 +859,7 @@ static __global__ __launch_bounds__(256) void sel_carry_kernel(const float* __re
   const int64_t b = idx / per_b;
   const int64_t rem = idx - b * per_b;
   const int64_t n = rem / g.D, d = rem - n * g.D;
-  const float a2 = fmaxf(A[d * g.N + n] * kLog2e, -kFltMax);
+  const float a2 = decay_rate(A[d * g.N + n]);
   float h = h0 ? h0[(b * g.D + d) * g.N + n] : 0.0f;
   const int64_t sstride = g.batch * per_b, dstride = g.batch * g.D;
   float* slot = slots + b * per_b + rem;              // [s][b][n][d]

@@ -71,10 +71,10 @@ __global__ __launch_bounds__(256) void sel_update_kernel(const void* __restrict_
   if constexpr (PL == 4) {
     const f4v a4 = *reinterpret_cast<const f4v*>(A + (int64_t)d * NS + j * 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) av[i] = fmaxf(a4[i] * kLog2e, -kFltMax);  // -inf clamped: 0*a2 = 0
+    for (int i = 0; i < 4; ++i) av[i] = decay_rate(a4[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < PL; ++i) av[i] = fmaxf(A[(int64_t)d * NS + i] * kLog2e, -kFltMax);
+    for (int i = 0; i < PL; ++i) av[i] = decay_rate(A[(int64_t)d * NS + i]);
   }
   const float dd = Dsk != nullptr ? Dsk[d] : 0.0f;
 

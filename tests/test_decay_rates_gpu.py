@@ -70,3 +70,67 @@ def test_minus_infinity_forgets(fn, chunks, bf16, monkeypatch):
     v["delta"][:, 3] = 0.0
     _, st = fn(v, chunks)
     assert bool((st[:, 3] == (1.0 if fn is slots else 0.0)).all())
+
+
+def dense(v, layout="bld", **kw):
+    """(y, h_last) of the equal-length scan, y as (length, dim)."""
+    import torch
+    import selective_state_space_20_amd as sss
+    bdl = layout == "bdl"
+    lay = lambda t: (t.t() if bdl else t).contiguous()[None]
+    y, h = sss.selective_scan_fwd(lay(v["x"]), lay(v["delta"]), v["A"], lay(v["B"].float()), lay(v["C"].float()), v["D"],
+                                  lay(v["z"]), layout=layout, **kw)
+    return (y[0].t() if bdl else y[0]), h
+
+
+FORMS = {"plain": {}, "channel-major": dict(layout="bdl"), "softplus": dict(delta_softplus=True), "hold": dict(exact_zoh=True),
+         "hold, channel-major": dict(layout="bdl", exact_zoh=True)}
+
+
+@pytest.mark.parametrize("env", [{}, {"SSS_FORCE_SEGMENTS": "3"}, {"SSS_CHUNKED": "1"}])
+@pytest.mark.parametrize("n", [1, 16, 64])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_nan_reaches_its_channel_dense(form, n, env, monkeypatch):
+    for k, s in env.items():
+        monkeypatch.setenv(k, s)
+    v = operands(200, 70, n, True)
+    want, want_h = dense(v, **FORMS[form])
+    v["A"] = v["A"].clone()
+    v["A"][5, n // 2] = v["A"][69, n - 1] = float("nan")
+    y, h = dense(v, **FORMS[form])
+    hit = [5, 69]
+    rest = [d for d in range(70) if d not in hit]
+    assert bool(y[:, hit].isnan().all()) and bool(h[:, 5, n // 2].isnan().all()) and bool(h[:, 69, n - 1].isnan().all())
+    assert bool((y[:, rest] == want[:, rest]).all()) and bool((h[:, rest] == want_h[:, rest]).all())
+
+
+@pytest.mark.parametrize("n", [1, 2, 16])
+def test_nan_reaches_its_channel_in_a_step(n):
+    import torch
+    import selective_state_space_20_amd as sss
+    v = operands(9, 70, n, False)
+    v["A"] = v["A"].clone()
+    v["A"][5, n // 2] = float("nan")
+    st = torch.ones(9, 70, n, device="cuda:0")
+    y = sss.selective_state_update(**v, state=st)
+    assert bool(y[:, 5].isnan().all()) and bool(st[:, 5, n // 2].isnan().all())
+    assert int(y.isnan().sum()) == 9 and int(st.isnan().sum()) == 9
+
+
+@pytest.mark.parametrize("segments", [None, "3"])
+@pytest.mark.parametrize("soft", [False, True])
+def test_nan_reaches_its_gradients(soft, segments, monkeypatch):
+    import torch
+    import selective_state_space_20_amd as sss
+    if segments:
+        monkeypatch.setenv("SSS_FORCE_SEGMENTS", segments)
+    v = operands(200, 70, 16, True)
+    v = {k: (t.float() if k in "BC" else t) for k, t in v.items()}
+    v = {k: (t[None] if k not in ("A", "D") else t) for k, t in v.items()}
+    v["A"] = v["A"].clone()
+    v["A"][5, 3] = float("nan")
+    g = sss.selective_scan_bwd(**v, dy=torch.ones(1, 200, 70, device="cuda:0"), delta_softplus=soft)
+    rest = [d for d in range(70) if d != 5]
+    assert bool(g["dA"][5, 3].isnan()) and bool(g["ddelta"][0, 1:, 5].isnan().all())
+    for k in ("dx", "ddelta", "dz"):
+        assert not bool(g[k][..., rest].isnan().any()), k
