@@ -43,10 +43,12 @@ def _rows(t, name, dtype, rows, dim, index):
     """Checks a (rows, dim) tensor whose rows may be strided; returns (pointer, row stride)."""
     if t.dtype is dtype and t.shape == (rows, dim) and t.get_device() == index >= 0:
         s0, s1 = t.stride()
-        if s1 == 1 and s0 >= dim:
+        if s1 == 1 and s0 >= dim and rows > 1:
             return t.data_ptr(), s0
-        if (s1 == 1 or dim == 1) and (rows <= 1 or s0 >= dim):  # sizes of one: strides without a meaning
-            return t.data_ptr(), max(s0, dim)
+        if rows <= 1 and (s1 == 1 or dim == 1):  # one row: its stride has no meaning, and may be any
+            return t.data_ptr(), dim
+        if dim == 1 and s0 >= 1:
+            return t.data_ptr(), s0
         raise ValueError(f"{name}: rows must be {dim} adjacent elements and not overlap, got strides {(s0, s1)}")
     _refuse(t, name, dtype, (rows, dim), index)
 
@@ -214,11 +216,13 @@ def _blocks(t, name, dtype, shape, index):
     (pointer, batch stride, row stride)."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or index < 0:
         _refuse(t, name, dtype, shape, index)
-    _, rows, dim = shape
+    batch, rows, dim = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and dim != 1) or (rows > 1 and s1 < dim):
         raise ValueError(f"{name}: rows must be {dim} adjacent elements, got strides {(s0, s1, s2)}")
-    return t.data_ptr(), s0, max(s1, dim)
+    if rows <= 1:  # sizes of one: strides without a meaning, which may be any
+        s1 = dim
+    return t.data_ptr(), s0 if batch > 1 else rows * s1, s1
 
 
 def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, workspace=None, stream=None):

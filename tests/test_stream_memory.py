@@ -72,7 +72,7 @@ class Library:
     """Every size is 64 bytes, every call succeeds; the stream is a call's last argument."""
 
     def __init__(self):
-        self.streams = []
+        self.streams, self.calls = [], []
 
     def __getattr__(self, name):
         if name.endswith("_size"):
@@ -80,6 +80,7 @@ class Library:
 
         def call(*a):
             self.streams.append(a[-1])
+            self.calls.append((name, a))
             return 0
         return call
 
