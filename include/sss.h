@@ -298,8 +298,9 @@ size_t causal_conv1d_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t d
 
 /* Gradients of causal_conv1d_fwd: with L = sum(dout * out), dx = dL/dx (batch, seqlen, dim),
  * dweight (dim, width) and dbias (dim) float32.  The pre-activation is recomputed.  x and dx have a
- * row and a batch stride (dx's batch rows may not share elements: SSS_ERR_BAD_DIM); dout is
- * contiguous; dout and dx are each float32 or io_dtype (SSS_ERR_UNSUPPORTED otherwise).
+ * row and a batch stride, batch-major or time-major (rows of dx may not share elements:
+ * SSS_ERR_BAD_DIM); dout is contiguous; dout and dx are each float32 or io_dtype
+ * (SSS_ERR_UNSUPPORTED otherwise).
  * Required: x, weight, dout, dx, dweight; dbias with bias.  The sums over batch and time are
  * formed in a fixed order: results are deterministic. */
 int causal_conv1d_bwd(const void* x, int64_t x_batch_stride, int64_t x_stride, const float* weight, const float* bias,

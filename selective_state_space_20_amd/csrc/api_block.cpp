@@ -453,8 +453,11 @@ int causal_conv1d_bwd(const void* x, int64_t x_batch_stride, int64_t x_stride, c
   if (!stride_ok(x_stride, dim) || !stride_ok(dx_stride, dim) || x_batch_stride < 0 || dx_batch_stride < 0 ||
       x_batch_stride > kMaxBatchStride || dx_batch_stride > kMaxBatchStride)
     return SSS_ERR_BAD_DIM;
-  // batch rows may not share elements of dx
-  if (batch > 1 && dx_batch_stride < (seqlen - 1) * dx_stride + dim) return SSS_ERR_BAD_DIM;
+  // rows of dx may not share elements: one batch entry after the other, or (time-major) one step after
+  // the other with the batch entries inside it
+  if (batch > 1 && dx_batch_stride < (seqlen - 1) * dx_stride + dim &&
+      !(dx_batch_stride >= dim && (seqlen == 1 || dx_stride >= (batch - 1) * dx_batch_stride + dim)))
+    return SSS_ERR_BAD_DIM;
   const int64_t es = dtype_size(io_dtype), dos = dtype_size(dout_dtype), dxs = dtype_size(dx_dtype);
   Regions r;
   r.in(x, (batch - 1) * x_batch_stride * es + span(seqlen, x_stride, dim, es), es);
