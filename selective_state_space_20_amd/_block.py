@@ -15,15 +15,16 @@ from . import _lib
 from ._lib import SSS_BF16, SSS_DELTA_SOFTPLUS, SSS_F32, SSS_NORM_BEFORE_GATE, SSSError, load
 
 
-_torch = None
+_torch = _current_gpu = None
 
 
 def torch_():
     """torch, imported with the first call (as the library is), not with the package."""
-    global _torch
+    global _torch, _current_gpu
     if _torch is None:
         load()
         import torch
+        _current_gpu = torch._C._cuda_getDevice
         _torch = torch
     return _torch
 
@@ -73,7 +74,7 @@ def _new(like, shape, dtype, stream):
 def _out(out, name, like, dtype, shape, index, stream):
     """The given output, checked, or a new one on like's GPU; returns (tensor, pointer)."""
     if out is None:
-        out = _new(like, shape, dtype, stream)
+        out = like.new_empty(shape, dtype=dtype) if stream is None else _new(like, shape, dtype, stream)
         return out, out.data_ptr()
     return out, _dense(out, name, dtype, shape, index)
 
@@ -91,7 +92,7 @@ def _scratch(workspace, nbytes, like, stream):
 def _keep(stream, index, *tensors):
     """Memory of the caller's that work on a given other stream writes: not handed out again before
     that work is done."""
-    if stream is not None and stream != _torch._C._cuda_getCurrentRawStream(index):
+    if stream != _torch._C._cuda_getCurrentRawStream(index):
         s = _lib._stream_of(stream, index)
         for t in tensors:
             if t is not None:
@@ -116,6 +117,25 @@ def _two_d(t, name):
 def _stream(stream, index):
     """The given stream, or the current one of the call's GPU (its handle without a Stream object)."""
     return stream if stream is not None else _torch._C._cuda_getCurrentRawStream(index)
+
+
+class _Elsewhere:
+    """The library with a GPU that is not the current one made current for each call."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __getattr__(self, name):
+        def call(*args):
+            with _torch.cuda.device(self.index):
+                return getattr(_lib._lib, name)(*args)
+        return call
+
+
+def _library(index):
+    """The library, for operands on GPU `index`: its kernels run on the current GPU where the stream is
+    the default one, whose handle is the same on all of them."""
+    return _lib._lib if index == _current_gpu() else _Elsewhere(index)
 
 
 def _cache(state, name, dtype, tail, index):
@@ -170,11 +190,12 @@ def causal_conv1d_packed_fwd(x, weight, bias=None, *, cu_seqlens, conv_state=Non
     o, op = _out(out, "out", x, x.dtype, (tokens, dim), gpu, stream)
     if tokens == 0:
         return o
-    rc = load().causal_conv1d_packed_fwd(xp, xs, wp, bp, sp, cu, idx, ini, op, tokens, nseq, slots if sp else 0, dim,
+    rc = _library(gpu).causal_conv1d_packed_fwd(xp, xs, wp, bp, sp, cu, idx, ini, op, tokens, nseq, slots if sp else 0, dim,
                                          width, code, int(bool(silu)), _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_packed_fwd")
-    _keep(stream, gpu, o)
+    if stream is not None:
+        _keep(stream, gpu, o)
     return o
 
 
@@ -199,11 +220,12 @@ def causal_conv1d_update(x, weight, bias=None, *, conv_state, state_indices=None
     o, op = _out(out, "out", x, x.dtype, (batch, dim), gpu, stream)
     if batch == 0:
         return o
-    rc = load().causal_conv1d_update(xp, xs, wp, bp, sp, idx, op, batch, slots, dim, width, code, int(bool(silu)),
+    rc = _library(gpu).causal_conv1d_update(xp, xs, wp, bp, sp, idx, op, batch, slots, dim, width, code, int(bool(silu)),
                                      _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_update")
-    _keep(stream, gpu, o)
+    if stream is not None:
+        _keep(stream, gpu, o)
     return o
 
 
@@ -257,13 +279,14 @@ def causal_conv1d_bwd(x, weight, bias=None, *, dout, silu=False, dx=None, worksp
         g["dbias"] = _new(x, (dim,), torch.float32, stream)
     need = causal_conv1d_bwd_workspace_size(batch, seqlen, dim, width, code, gpu) if workspace is None else 0
     workspace, wsp, wsn = _scratch(workspace, need, x, stream)
-    rc = load().causal_conv1d_bwd(xp, xb, xr, wp, bp, dp, gp, gb, gr, g["dweight"].data_ptr(),
+    rc = _library(gpu).causal_conv1d_bwd(xp, xb, xr, wp, bp, dp, gp, gb, gr, g["dweight"].data_ptr(),
                                   g["dbias"].data_ptr() if bias is not None else 0, batch, seqlen, dim, width, code,
                                   _code(dout.dtype, "dout"), _code(dx.dtype, "dx"), int(bool(silu)), wsp, wsn,
                                   _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_bwd")
-    _keep(stream, gpu, workspace, *g.values())
+    if stream is not None:
+        _keep(stream, gpu, workspace, *g.values())
     return g
 
 
@@ -312,11 +335,12 @@ def selective_scan_packed_fwd(x, delta, A, B, C, D=None, z=None, *, cu_seqlens, 
         return y
     need = selective_scan_packed_fwd_workspace_size(tokens, dim, n, gpu) if workspace is None else 0
     workspace, wsp, wsn = _scratch(workspace, need, x, stream)
-    rc = load().selective_scan_packed_fwd(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, cu, idx, ini, yp,
+    rc = _library(gpu).selective_scan_packed_fwd(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, cu, idx, ini, yp,
                                           tokens, nseq, slots, dim, n, code, bc, yc, wsp, wsn, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "selective_scan_packed_fwd")
-    _keep(stream, gpu, workspace, y)
+    if stream is not None:
+        _keep(stream, gpu, workspace, y)
     return y
 
 
@@ -338,11 +362,12 @@ def selective_state_update_slots(x, delta, A, B, C, D=None, z=None, *, state, st
     y, yp = _out(out, "out", x, yd, (batch, dim), gpu, stream)
     if batch == 0:
         return y
-    rc = load().selective_state_update_slots(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, idx, yp, batch,
+    rc = _library(gpu).selective_state_update_slots(*ops, SSS_DELTA_SOFTPLUS if delta_softplus else 0, sp, idx, yp, batch,
                                              slots, dim, n, code, bc, yc, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "selective_state_update_slots")
-    _keep(stream, gpu, y)
+    if stream is not None:
+        _keep(stream, gpu, y)
     return y
 
 
@@ -374,12 +399,13 @@ def rms_norm_gated_fwd(x, weight, z=None, *, eps=1e-5, group_size=None, norm_bef
     o, op = _out(out, "out", x, od, (rows, dim), gpu, stream)
     rstd = _new(x, (rows, dim // g), torch.float32, stream) if return_rstd else None
     if rows > 0:
-        rc = load().rms_norm_gated_fwd(xp, xs, wp, zp, zs, op, rstd.data_ptr() if return_rstd else 0, rows, dim, g,
+        rc = _library(gpu).rms_norm_gated_fwd(xp, xs, wp, zp, zs, op, rstd.data_ptr() if return_rstd else 0, rows, dim, g,
                                        float(eps), SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc,
                                        _stream(stream, gpu))
         if rc != 0:
             raise SSSError(rc, "rms_norm_gated_fwd")
-        _keep(stream, gpu, o, rstd)
+        if stream is not None:
+            _keep(stream, gpu, o, rstd)
     return (o, rstd) if return_rstd else o
 
 
@@ -415,12 +441,13 @@ def rms_norm_gated_bwd(dout, x, weight, z=None, *, rstd, group_size=None, norm_b
             gp, gs = _rows(dz, "dz", od, rows, dim, gpu)
     need = rms_norm_gated_bwd_workspace_size(rows, dim, g, gpu) if workspace is None else 0
     workspace, wsp, wsn = _scratch(workspace, need, x, stream)
-    rc = load().rms_norm_gated_bwd(dp, xp, xs, wp, zp, zs, rp, res["dx"].data_ptr(), gp, gs, res["dweight"].data_ptr(),
+    rc = _library(gpu).rms_norm_gated_bwd(dp, xp, xs, wp, zp, zs, rp, res["dx"].data_ptr(), gp, gs, res["dweight"].data_ptr(),
                                    rows, dim, g, SSS_NORM_BEFORE_GATE if norm_before_gate else 0, xc, oc, wsp, wsn,
                                    _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "rms_norm_gated_bwd")
-    _keep(stream, gpu, workspace, *res.values())
+    if stream is not None:
+        _keep(stream, gpu, workspace, *res.values())
     return res
 
 
@@ -452,13 +479,14 @@ def rms_norm_residual_fwd(x, weight, residual=None, *, post_weight=None, scale=N
         rstd = _new(x, (rows,), torch.float32, stream)
         rstd_post = _new(x, (rows,), torch.float32, stream) if post_weight is not None else None
     if rows > 0:
-        rc = load().rms_norm_residual_fwd(xp, xs, hp, hs, pp, sp, wp, op, ho,
+        rc = _library(gpu).rms_norm_residual_fwd(xp, xs, hp, hs, pp, sp, wp, op, ho,
                                           0 if rstd_post is None else rstd_post.data_ptr(),
                                           0 if rstd is None else rstd.data_ptr(), rows, dim, float(alpha), float(eps),
                                           xc, hc, _stream(stream, gpu))
         if rc != 0:
             raise SSSError(rc, "rms_norm_residual_fwd")
-        _keep(stream, gpu, o, h, rstd, rstd_post)
+        if stream is not None:
+            _keep(stream, gpu, o, h, rstd, rstd_post)
     return (o, h, rstd, rstd_post) if return_rstd else (o, h)
 
 
@@ -503,10 +531,11 @@ def rms_norm_residual_bwd(dout, dresidual_out=None, *, residual_out, weight, rst
     ptr = lambda k: res[k].data_ptr() if k in res else 0
     need = rms_norm_residual_bwd_workspace_size(rows, dim, gpu) if workspace is None else 0
     workspace, wsp, wsn = _scratch(workspace, need, dout, stream)
-    rc = load().rms_norm_residual_bwd(dp, ep, xp, xs, hp, pp, sp, wp, rpp, rp, ptr("dx"), ptr("dresidual"),
+    rc = _library(gpu).rms_norm_residual_bwd(dp, ep, xp, xs, hp, pp, sp, wp, rpp, rp, ptr("dx"), ptr("dresidual"),
                                       ptr("dweight"), ptr("dpost_weight"), ptr("dscale"), rows, dim, float(alpha), xc,
                                       hc, wsp, wsn, _stream(stream, gpu))
     if rc != 0:
         raise SSSError(rc, "rms_norm_residual_bwd")
-    _keep(stream, gpu, workspace, *res.values())
+    if stream is not None:
+        _keep(stream, gpu, workspace, *res.values())
     return res

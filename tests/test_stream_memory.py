@@ -16,30 +16,31 @@ F32, BF16, I32 = torch.float32, torch.bfloat16, torch.int32
 
 
 class Gpu:
-    """Streams of one GPU: the raw handles of the current ones, innermost last."""
+    """The GPU that tensors are on, and what is current: raw stream handles and GPUs, innermost last."""
 
-    def __init__(self, current):
-        self.now, self.made = [current], []
+    def __init__(self, current, index=0, device=0):
+        self.now, self.made, self.index, self.devices = [current], [], index, [device]
 
     def torch(self):
         gpu = self
 
         class On:
-            def __init__(self, handle):
-                self.handle = handle
+            def __init__(self, stack, entry):
+                self.stack, self.entry = stack, entry
 
             def __enter__(self):
-                gpu.now.append(self.handle)
+                self.stack.append(self.entry)
 
             def __exit__(self, *a):
-                gpu.now.pop()
+                self.stack.pop()
 
         cuda = types.SimpleNamespace(
-            stream=lambda s: On(s.cuda_stream),
+            stream=lambda s: On(gpu.now, s.cuda_stream),
+            device=lambda d: On(gpu.devices, d if isinstance(d, int) else d.index),
             ExternalStream=lambda h, device=None: types.SimpleNamespace(cuda_stream=h if h != 0 else "a new stream"),
             default_stream=lambda i=None: types.SimpleNamespace(cuda_stream=0),
             current_stream=lambda i=None: types.SimpleNamespace(cuda_stream=gpu.now[-1]))
-        c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: gpu.now[-1], _cuda_getDevice=lambda: 0)
+        c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: gpu.now[-1], _cuda_getDevice=lambda: gpu.devices[-1])
         names = {n: getattr(torch, n) for n in ("float32", "bfloat16", "int32", "uint8", "bool", "device")}
         empty = lambda shape, dtype=F32, device=None: self.tensor(shape, dtype, self.now[-1])
         return types.SimpleNamespace(cuda=cuda, _C=c, Tensor=Tensor, empty=empty, **names)
@@ -52,13 +53,14 @@ class Gpu:
 
 
 class Tensor:
-    is_cuda, device = True, torch.device("cuda", 0)
+    is_cuda = True
 
     def __init__(self, gpu, shape, dtype, stream):
         self.gpu, self.shape, self.dtype, self.stream, self.recorded = gpu, shape, dtype, stream, []
 
     ndim = property(lambda self: len(self.shape))
-    get_device = lambda self: 0
+    device = property(lambda self: torch.device("cuda", self.gpu.index))
+    get_device = lambda self: self.gpu.index
     is_contiguous = lambda self: True
     data_ptr = lambda self: 4096 + id(self) % 4096
     numel = lambda self: math.prod(self.shape)
@@ -72,7 +74,7 @@ class Library:
     """Every size is 64 bytes, every call succeeds; the stream is a call's last argument."""
 
     def __init__(self):
-        self.streams, self.calls = [], []
+        self.streams, self.calls, self.devices, self.gpu = [], [], [], None
 
     def __getattr__(self, name):
         if name.endswith("_size"):
@@ -81,6 +83,7 @@ class Library:
         def call(*a):
             self.streams.append(a[-1])
             self.calls.append((name, a))
+            self.devices.append(self.gpu.devices[-1])
             return 0
         return call
 
@@ -132,13 +135,15 @@ def calls(t):
 
 @pytest.fixture
 def gpu(monkeypatch):
-    def make(current):
-        g, lib = Gpu(current), Library()
+    def make(current, index=0, device=0):
+        g, lib = Gpu(current, index, device), Library()
+        lib.gpu = g
         for m in (_block, _lib):
             monkeypatch.setattr(m, "load", lambda: lib)
         stand_in = g.torch()
         monkeypatch.setitem(sys.modules, "torch", stand_in)
         monkeypatch.setattr(_block, "_torch", stand_in)
+        monkeypatch.setattr(_block, "_current_gpu", stand_in._C._cuda_getDevice)
         monkeypatch.setattr(_block, "torch_", lambda: stand_in)
         monkeypatch.setattr(_lib, "_lib", lib)
         return g, lib
