@@ -248,28 +248,31 @@ def selective_scan_bwd(x, delta, A, B, C, D=None, z=None, h0=None, *, dy, dh_las
     wsp, wsn = _workspace(workspace, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
     if front:
-        rc = selective_scan_bwd_ex_raw(_ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
-                                       _ptr(dy), _ptr(dh_last), _ptr(delta_bias),
-                                       SSS_DELTA_SOFTPLUS if delta_softplus else 0, _ptr(g["dx"]), _ptr(g["ddelta"]),
-                                       _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]),
-                                       _ptr(g["dh0"]), _ptr(g.get("ddelta_bias")), batch, seqlen, dim, dstate, io_code,
-                                       wsp, wsn, st)
+        rc = _run(dev, selective_scan_bwd_ex_raw,
+                  _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
+                  _ptr(dy), _ptr(dh_last), _ptr(delta_bias),
+                  SSS_DELTA_SOFTPLUS if delta_softplus else 0, _ptr(g["dx"]), _ptr(g["ddelta"]),
+                  _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]),
+                  _ptr(g["dh0"]), _ptr(g.get("ddelta_bias")), batch, seqlen, dim, dstate, io_code,
+                  wsp, wsn, st)
         if rc != 0:
             raise SSSError(rc, "selective_scan_bwd_ex")
         return g
     if states is None:
-        rc = selective_scan_bwd_raw(_ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
-                                    _ptr(dy), _ptr(dh_last), _ptr(g["dx"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
-                                    _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]), _ptr(g["dh0"]), batch,
-                                    seqlen, dim, dstate, io_code, wsp, wsn, st)
+        rc = _run(dev, selective_scan_bwd_raw,
+                  _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
+                  _ptr(dy), _ptr(dh_last), _ptr(g["dx"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
+                  _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]), _ptr(g["dh0"]), batch,
+                  seqlen, dim, dstate, io_code, wsp, wsn, st)
         if rc != 0:
             raise SSSError(rc, "selective_scan_bwd")
         return g
     sp, sn = _states_buffer(states, selective_scan_states_size(batch, seqlen, dim, dstate, dev.index or 0), dev)
-    rc = selective_scan_bwd_saved_raw(_ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
-                                      _ptr(dy), _ptr(dh_last), sp, sn, _ptr(g["dx"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
-                                      _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]), _ptr(g["dh0"]), batch,
-                                      seqlen, dim, dstate, io_code, wsp, wsn, st)
+    rc = _run(dev, selective_scan_bwd_saved_raw,
+              _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
+              _ptr(dy), _ptr(dh_last), sp, sn, _ptr(g["dx"]), _ptr(g["ddelta"]), _ptr(g["dA"]),
+              _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]), _ptr(g["dh0"]), batch,
+              seqlen, dim, dstate, io_code, wsp, wsn, st)
     if rc != 0:
         raise SSSError(rc, "selective_scan_bwd_saved")
     return g
@@ -295,8 +298,9 @@ def causal_conv1d_fwd(x, weight, bias=None, *, silu=False, out=None, stream=None
     _need(o, "out", io, (batch, seqlen, dim), dev)
     _on_device(dev, x=x, weight=weight, bias=bias, out=o)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    rc = causal_conv1d_fwd_raw(_ptr(x), _ptr(weight), _ptr(bias), _ptr(o), batch, seqlen, dim, width, io_code,
-                               int(bool(silu)), st)
+    rc = _run(dev, causal_conv1d_fwd_raw,
+              _ptr(x), _ptr(weight), _ptr(bias), _ptr(o), batch, seqlen, dim, width, io_code,
+              int(bool(silu)), st)
     if rc != 0:
         raise SSSError(rc, "causal_conv1d_fwd")
     return o
@@ -349,6 +353,16 @@ def _empty(shape, dtype, device, stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(current)
     return t
+
+
+def _run(device, fn, *args):
+    """fn(*args) with the operands' GPU current: its kernels run on the current one where the stream is
+    the default one, whose handle is the same on all of them."""
+    import torch
+    if device.index == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
 
 
 def _need(t, name, dtype, shape, device):
@@ -443,14 +457,16 @@ def selective_scan_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, return_las
         if flags != 0 or delta_bias is not None:
             raise ValueError("states: the forward that keeps its states is the plain form (no options)")
         sp, sn = _states_buffer(states, selective_scan_states_size(batch, seqlen, dim, dstate, dev.index or 0), dev)
-        rc = selective_scan_fwd_save_raw(_ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
-                                         _ptr(y), _ptr(hl), sp, sn, batch, seqlen, dim, dstate, io_code, wsp, wsn, st)
+        rc = _run(dev, selective_scan_fwd_save_raw,
+                  _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
+                  _ptr(y), _ptr(hl), sp, sn, batch, seqlen, dim, dstate, io_code, wsp, wsn, st)
         if rc != 0:
             raise SSSError(rc, "selective_scan_fwd_save")
         return (y, hl) if return_last or out_last is not None else y
-    rc = selective_scan_fwd_ex_raw(_ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
-                                   _ptr(y), _ptr(hl), _ptr(delta_bias), flags, batch, seqlen, dim, dstate, io_code,
-                                   wsp, wsn, st)
+    rc = _run(dev, selective_scan_fwd_ex_raw,
+              _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0),
+              _ptr(y), _ptr(hl), _ptr(delta_bias), flags, batch, seqlen, dim, dstate, io_code,
+              wsp, wsn, st)
     if rc != 0:
         raise SSSError(rc, "selective_scan_fwd")
     return (y, hl) if return_last or out_last is not None else y
@@ -479,8 +495,9 @@ def selective_state_update(x, delta, A, B, C, D=None, z=None, *, state, out=None
     _need(y, "out", f32, (batch, dim), dev)
     _on_device(dev, x=x, delta=delta, z=z, A=A, B=B, C=C, D=D, state=state, out=y)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    rc = selective_state_update_raw(_ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(state),
-                                    _ptr(y), batch, dim, dstate, io_code, st)
+    rc = _run(dev, selective_state_update_raw,
+              _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(state),
+              _ptr(y), batch, dim, dstate, io_code, st)
     if rc != 0:
         raise SSSError(rc, "selective_state_update")
     return y
@@ -507,8 +524,9 @@ def elementwise_scan(x, A, B, C, h0=None, *, return_last=True, out=None, out_las
         workspace = _empty(wsb, torch.uint8, dev, stream)
     wsp, wsn = _workspace(workspace, dev)
     st = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    rc = elementwise_scan_raw(_ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(h0), _ptr(y), _ptr(hl), batch, seqlen, dim,
-                              wsp, wsn, st)
+    rc = _run(dev, elementwise_scan_raw,
+              _ptr(x), _ptr(A), _ptr(B), _ptr(C), _ptr(h0), _ptr(y), _ptr(hl), batch, seqlen, dim,
+              wsp, wsn, st)
     if rc != 0:
         raise SSSError(rc, "elementwise_scan")
     return (y, hl) if return_last or out_last is not None else y
