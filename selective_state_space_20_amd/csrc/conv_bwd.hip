@@ -23,7 +23,7 @@ constexpr int kCBwdU = 4;  // steps per load batch
 
 struct CBwdGeo {
   int64_t x_row, x_batch, dx_row, dx_batch;  // strides in elements
-  int L, D, seg_len, S, batch, ngroups;
+  int L, D, seg_len, batch, ngroups;
   int dx_bf16;
 };
 
@@ -228,7 +228,6 @@ static hipError_t run_bwd(const ConvBwdArgs& a, const ConvBwdPlan& pl, hipStream
   g.L = (int)a.seqlen;
   g.D = (int)a.dim;
   g.seg_len = (int)pl.seg_len;
-  g.S = pl.segments;
   g.batch = (int)a.batch;
   g.ngroups = (int)((a.dim + 64 * CPL - 1) / (64 * CPL));
   g.dx_bf16 = a.dx_bf16;

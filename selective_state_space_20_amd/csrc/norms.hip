@@ -496,8 +496,15 @@ static hipError_t launch_norm_sum(const void* part, float* out0, float* out1, fl
 // At most three pieces per lane, then 512 lanes: with five of V = 4 the gradients' registers leave few
 // waves (gated forward and gradients of 16384 x 5120 332 us on 512 lanes, 402 on 256, 372 with V =
 // 8 on 256; x 2560 174 on 256 lanes with three pieces, 187 on 512 with two; residual norm x 4096 383 on
-// 512, 421 on 256 with four; bf16 x 8192 forward 185, 188).  Above 6144 elements V = 4 would need 1024
-// lanes.  Fewer than 8 elements: one each, 8 lanes.
+// 512, 421 on 256 with four).  Above 6144 elements V = 4 would need 1024 lanes.  Pieces of V = 8 follow
+// the same rule on the evidence of one forward alone (bf16 x 8192: 185 us on 512 lanes, 188 on 256
+// with four): their residual gradients at 4097 to 6144 elements need 272 to 320 registers, one wave per
+// SIMD, and have not been measured on 512 lanes.  Fewer than 8 elements: one each, 8 lanes.
+//
+// Shapes that do not fit their registers: the residual gradients from 8193 elements on (15 to 145
+// registers of a lane in scratch memory up to 12288, 106 to 497 up to 16384, 391 to 816 above); all
+// other kernels above 16384 (gated forward 16, residual forward 8 to 157, gated gradients 158 to 252),
+// and the gated gradients of two fp32 tensors from 12289 on (4).
 struct NormShape {
   int v, tpr, m;
 };
@@ -533,8 +540,9 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
   return pl;
 }
 
-// CALL(V, TPR, M) of the shape sh; F32: one of the tensors is fp32
-#define SSS_NORM_SMALL(CALL, V)                                                 \
+// CALL(V, TPR, M) of the shape sh, of those that norm_shape gives; F32: one of the tensors is fp32.
+// Each chain ends in an else: no shape is without a kernel.
+#define SSS_NORM_UP_TO_256(CALL, V)                                             \
   if (sh.tpr == 8) { CALL(V, 8, 1); }                                           \
   else if (sh.tpr == 16) { CALL(V, 16, 1); }                                    \
   else if (sh.tpr == 32) { CALL(V, 32, 1); }                                    \
@@ -542,19 +550,24 @@ NormPlan plan_norm_bwd(int64_t rows, int64_t group, int64_t groups, int vectors,
   else if (sh.tpr == 64) { CALL(V, 64, 2); }                                    \
   else if (sh.tpr == 256 && sh.m == 1) { CALL(V, 256, 1); }                     \
   else if (sh.tpr == 256 && sh.m == 2) { CALL(V, 256, 2); }                     \
-  else if (sh.tpr == 256) { CALL(V, 256, 3); }                                  \
-  else if (sh.m == 2) { CALL(V, 512, 2); }                                      \
-  else if (sh.m == 3) { CALL(V, 512, 3); }
+  else if (sh.tpr == 256) { CALL(V, 256, 3); }
 #define SSS_NORM_SHAPES(CALL, F32)                                              \
   do {                                                                          \
     if (sh.v == 1) {                                                            \
       CALL(1, 8, 1);                                                            \
-    } else if (sh.v == 4) {                                                     \
+    } else if (sh.v == 4) { /* up to 1536 pieces, with an fp32 tensor only */   \
       if constexpr (F32) {                                                      \
-        SSS_NORM_SMALL(CALL, 4)                                                 \
+        SSS_NORM_UP_TO_256(CALL, 4)                                             \
+        else if (sh.m == 2) { CALL(4, 512, 2); }                                \
+        else { CALL(4, 512, 3); }                                               \
       }                                                                         \
     } else {                                                                    \
-      SSS_NORM_SMALL(CALL, 8)                                                   \
+      if constexpr (!F32) { /* with one from 769 pieces on only */              \
+        SSS_NORM_UP_TO_256(CALL, 8)                                             \
+        if (sh.tpr <= 256) break;                                               \
+      }                                                                         \
+      if (sh.tpr == 512 && sh.m == 2) { CALL(8, 512, 2); }                      \
+      else if (sh.tpr == 512 && sh.m == 3) { CALL(8, 512, 3); }                 \
       else if (sh.tpr == 512) { CALL(8, 512, 4); }                              \
       else { CALL(8, 1024, 4); }                                                \
     }                                                                           \

@@ -17,8 +17,6 @@
 
 namespace sss {
 
-typedef float slot_f4 __attribute__((ext_vector_type(4)));
-
 template <int CTRL>
 __device__ __forceinline__ float slot_dpp(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
