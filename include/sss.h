@@ -264,9 +264,10 @@ int causal_conv1d_fwd(const void* x, const float* weight, const float* bias, voi
  *
  * Packed prompts: `tokens` rows hold the sequences one after the other; sequence s is rows
  * cu_seqlens[s] .. cu_seqlens[s+1]-1 (nseq + 1 device integers, not decreasing, in [0, tokens]).
- * A sequence may be empty: its slot is then left alone.  Rows outside every sequence are
- * neither read nor written.  The device never reads or writes out of range whatever these
- * integers hold, but the results are only defined as above.
+ * A sequence may be empty: its slot is then left alone.  Rows of the operands outside every
+ * sequence may be loaded, but have no effect; those of the output are not written.  The device
+ * never reads or writes out of range whatever these integers hold, but the results are only
+ * defined as above.
  *
  * Cache slots: sequence (or decode row) s keeps its history or state in slot state_indices[s]
  * of `slots`, or in slot s where state_indices is NULL (then nseq <= slots: SSS_ERR_BAD_DIM).

@@ -18,13 +18,15 @@
 //          entering each chunk;
 //   pass 2 walks every chunk's sequences, writes y, and the final states to the slots.
 // Short sequences thus cost no second pass over their tokens: with lengths well below K nearly
-// nothing runs in pass 1.
+// nothing runs in pass 1.  (9001 tokens x 2048 in 40 sequences has K = 71: 82-87% of the tokens lie in
+// one that goes on, and are walked twice.)
 //
-// Bound by the issue of VALU instructions: 32768 x 5120 x 16 in three sequences takes 394 us (pass
-// 1) + 21 (carry) + 534 (pass 2) on a traced run, 875-890 untraced.  Per wave and step pass 1 issues 17
-// exps, two slots of four clocks each, and 65 other instructions, pass 2 19 and 90: 420 and 549 us at
+// Bound by the issue of VALU instructions: 32768 x 5120 x 16 in three sequences takes 388 us (pass
+// 1) + 21 (carry) + 528 (pass 2) on a traced run, 858-902 untraced.  Per wave and step pass 1 issues 17
+// exps, two slots of four clocks each, and 65 other instructions, pass 2 19 and 90: 421 and 549 us at
 // 2.4 GHz if no two waves' instructions issue together, 292 and 367 if all but the exps do.  The memory
-// traffic, 706 and 1450 MB, would take 133 and 274.
+// traffic, 706 and 1450 MB, would take 133 and 274; 58 MB of the latter are 28 registers per lane that
+// pass 2, at its limit of 128, keeps in scratch memory over the loop over sequences.
 //
 // A slot is read in pass 1 (or in pass 2 by the wave that also writes it), so that it is updated in
 // place.
