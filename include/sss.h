@@ -393,6 +393,71 @@ int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const voi
                           float* dpost_weight, float* dscale, int64_t rows, int64_t dim, float alpha, int io_dtype,
                           int residual_dtype, void* workspace, size_t workspace_bytes, sss_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the scan's head form, with one decay per head (and
+ * token) instead of one per channel and state, and a state S of dk x dv for each head.  With
+ * log decays g and input weights beta (one where NULL), per sequence and head
+ *   S_t = exp(g_t) S_{t-1} + beta_t k_t v_t^T,   out_t = scale q_t S_t + D v_t
+ * (the state-space form: q = C, k = B, v = x, g = delta A, beta = delta).
+ *
+ * q (tokens, q_heads, dk), k (tokens, k_heads, dk), v (tokens, heads, dv) in io_dtype: dk or dv adjacent
+ * elements, any strides >= 0 (elements) between tokens and between heads; q_heads and k_heads divide
+ * heads, adjacent heads share one.  log_decay (tokens, heads) float32 with decay_stride, or
+ * (heads) with decay_stride 0: one decay for each head.  beta (tokens, heads) float32 with
+ * beta_stride, nullable; D_skip (heads) float32, nullable.  A log decay of -1e4 or less, -inf
+ * included, leaves nothing of the state.  state (slots, heads, dk, dv) float32.  dk and dv up to 256
+ * (SSS_ERR_UNSUPPORTED otherwise), heads up to 65536.  Packed prompts, cache slots, alignment and
+ * overlap as above.  Results are deterministic.
+ *
+ * A value that is no number, or an infinity, in a token's k or v reaches the outputs of that token
+ * and of later ones of its sequence; in its v also those of up to 63 tokens before it. */
+
+/* Bytes of workspace linear_attention_packed_fwd needs on `device` (0 on invalid sizes, and where
+ * none is needed); it does not depend on the sequences. */
+size_t linear_attention_packed_fwd_workspace_size(int64_t tokens, int64_t heads, int64_t dk, int64_t dv, int device);
+
+/* Over packed prompts; state nullable (every sequence starts from zero and nothing is kept), updated in
+ * place to each sequence's last state; has_initial as above.  out (tokens, heads, dv) contiguous
+ * in io_dtype.  Required: q, k, v, log_decay, cu_seqlens, out. */
+int linear_attention_packed_fwd(const void* q, int64_t q_stride, int64_t q_head_stride, int64_t q_heads, const void* k,
+                                int64_t k_stride, int64_t k_head_stride, int64_t k_heads, const void* v, int64_t v_stride,
+                                int64_t v_head_stride, const float* log_decay, int64_t decay_stride, const float* beta,
+                                int64_t beta_stride, const float* D_skip, float scale, float* state, const int32_t* cu_seqlens,
+                                const int32_t* state_indices, const uint8_t* has_initial, void* out, int64_t tokens,
+                                int64_t nseq, int64_t slots, int64_t heads, int64_t dk, int64_t dv, int io_dtype,
+                                void* workspace, size_t workspace_bytes, sss_stream_t stream);
+
+/* One token of each row, on states in cache slots (updated in place).  Required: q, k, v, log_decay,
+ * state, out.  No workspace. */
+int linear_attention_update_slots(const void* q, int64_t q_stride, int64_t q_head_stride, int64_t q_heads, const void* k,
+                                  int64_t k_stride, int64_t k_head_stride, int64_t k_heads, const void* v, int64_t v_stride,
+                                  int64_t v_head_stride, const float* log_decay, int64_t decay_stride, const float* beta,
+                                  int64_t beta_stride, const float* D_skip, float scale, float* state,
+                                  const int32_t* state_indices, void* out, int64_t batch, int64_t slots, int64_t heads,
+                                  int64_t dk, int64_t dv, int io_dtype, sss_stream_t stream);
+
+/* Bytes of workspace linear_attention_packed_bwd needs on `device` (0 on invalid sizes). */
+size_t linear_attention_packed_bwd_workspace_size(int64_t tokens, int64_t nseq, int64_t heads, int64_t q_heads,
+                                                  int64_t k_heads, int64_t dk, int64_t dv, int device);
+
+/* Gradients of linear_attention_packed_fwd for L = sum(dout * out) + sum(dfinal_state * last states),
+ * each sequence s starting from initial_state[s] (nseq, heads, dk, dv) float32 (NULL: zero; not
+ * written) and ending in the state whose gradient is dfinal_state[s] (NULL: zero).  dout (tokens,
+ * heads, dv) contiguous in io_dtype.  Outputs, contiguous: dq (tokens, q_heads, dk), dk_out
+ * (tokens, k_heads, dk), dv_out (tokens, heads, dv) in io_dtype; dlog_decay (tokens, heads), or (heads) with
+ * decay_stride 0, dbeta (tokens, heads) with beta, dD (heads) with D_skip, dinitial_state (nseq, heads, dk, dv,
+ * nullable), float32.  The states are recomputed.  Tokens outside every sequence get zero.  Required: q, k, v,
+ * log_decay, dout, cu_seqlens, dq, dk_out, dv_out, dlog_decay, dbeta with beta, dD with D_skip; with no tokens
+ * the sums over them are zero. */
+int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, int64_t q_heads, const void* k,
+                                int64_t k_stride, int64_t k_head_stride, int64_t k_heads, const void* v, int64_t v_stride,
+                                int64_t v_head_stride, const float* log_decay, int64_t decay_stride, const float* beta,
+                                int64_t beta_stride, const float* D_skip, float scale, const void* dout,
+                                const int32_t* cu_seqlens, const float* initial_state, const float* dfinal_state, void* dq,
+                                void* dk_out, void* dv_out, float* dlog_decay, float* dbeta, float* dD, float* dinitial_state,
+                                int64_t tokens, int64_t nseq, int64_t heads, int64_t dk, int64_t dv, int io_dtype,
+                                void* workspace, size_t workspace_bytes, sss_stream_t stream);
+
 /* Bytes of workspace elementwise_scan needs for these sizes on `device`. */
 size_t elementwise_scan_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, int device);
 

@@ -20,6 +20,9 @@ include/sss.h); this package is its thin Python binding:
   * ``rms_norm_gated_fwd`` / ``rms_norm_gated_bwd``: the norm after the scan, fused with the gate;
     ``rms_norm_residual_fwd`` / ``rms_norm_residual_bwd``: the residual addition between blocks,
     fused with a norm of the block's output, its scale and the next block's norm
+  * ``linear_attention_packed_fwd`` / ``linear_attention_update_slots``: linear attention with a decay for
+    each head (the scan's head form), over packed prompts and for single tokens, its states in cache
+    slots; ``linear_attention_packed_bwd``: its gradients
   * ``elementwise_scan(x, A, B, C, h0=None)`` -> (y, h_last)
   * ``*_workspace_size``, raw-pointer variants ``*_raw`` and ``status_string``.
 
@@ -40,6 +43,9 @@ from ._block import (causal_conv1d_bwd, causal_conv1d_bwd_workspace_size, causal
                      rms_norm_residual_bwd, rms_norm_residual_bwd_workspace_size, rms_norm_residual_fwd,
                      selective_scan_packed_fwd, selective_scan_packed_fwd_workspace_size,
                      selective_state_update_slots)
+from ._linear import (linear_attention_packed_bwd, linear_attention_packed_bwd_workspace_size,
+                      linear_attention_packed_fwd, linear_attention_packed_fwd_workspace_size,
+                      linear_attention_update_slots)
 
 __all__ = ["causal_conv1d_packed_fwd", "causal_conv1d_update", "causal_conv1d_bwd", "causal_conv1d_bwd_workspace_size",
            "selective_scan_packed_fwd", "selective_scan_packed_fwd_workspace_size", "selective_state_update_slots",
@@ -52,4 +58,6 @@ __all__ = ["causal_conv1d_packed_fwd", "causal_conv1d_update", "causal_conv1d_bw
            "SSSError", "SSS_F32", "SSS_BF16", "SSS_EXACT_ZOH", "SSS_DELTA_SOFTPLUS", "SSS_LAYOUT_BDL",
            "selective_scan_fwd_ex_workspace_size", "selective_scan_fwd_ex_raw", "selective_scan_fwd_noalloc_raw",
            "selective_scan_states_size", "selective_scan_fwd_save_raw", "selective_scan_bwd_saved_raw",
+           "linear_attention_packed_fwd", "linear_attention_packed_fwd_workspace_size", "linear_attention_update_slots",
+           "linear_attention_packed_bwd", "linear_attention_packed_bwd_workspace_size",
            "LIB_PATH", "EXPORTED", "load"]

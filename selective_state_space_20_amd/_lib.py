@@ -30,7 +30,10 @@ EXPORTED = ("selective_scan_fwd", "selective_scan_fwd_ex", "selective_scan_fwd_w
             "causal_conv1d_bwd_workspace_size", "selective_scan_packed_fwd",
             "selective_scan_packed_fwd_workspace_size", "selective_state_update_slots",
             "rms_norm_gated_fwd", "rms_norm_gated_bwd", "rms_norm_gated_bwd_workspace_size", "rms_norm_residual_fwd",
-            "rms_norm_residual_bwd", "rms_norm_residual_bwd_workspace_size")
+            "rms_norm_residual_bwd", "rms_norm_residual_bwd_workspace_size",
+            "linear_attention_packed_fwd", "linear_attention_packed_fwd_workspace_size",
+            "linear_attention_update_slots", "linear_attention_packed_bwd",
+            "linear_attention_packed_bwd_workspace_size")
 
 
 class SSSError(RuntimeError):
@@ -117,6 +120,17 @@ def load() -> ctypes.CDLL:
         lib.rms_norm_residual_bwd.restype = i32
         lib.rms_norm_residual_bwd_workspace_size.argtypes = [i64] * 2 + [i32]
         lib.rms_norm_residual_bwd_workspace_size.restype = sz
+        heads = [vp, i64, i64, i64] * 2 + [vp, i64, i64, vp, i64, vp, i64, vp, f32]
+        lib.linear_attention_packed_fwd.argtypes = heads + [vp] * 5 + [i64] * 6 + [i32, vp, sz, vp]
+        lib.linear_attention_packed_fwd.restype = i32
+        lib.linear_attention_packed_fwd_workspace_size.argtypes = [i64] * 4 + [i32]
+        lib.linear_attention_packed_fwd_workspace_size.restype = sz
+        lib.linear_attention_update_slots.argtypes = heads + [vp] * 3 + [i64] * 5 + [i32, vp]
+        lib.linear_attention_update_slots.restype = i32
+        lib.linear_attention_packed_bwd.argtypes = heads + [vp] * 11 + [i64] * 5 + [i32, vp, sz, vp]
+        lib.linear_attention_packed_bwd.restype = i32
+        lib.linear_attention_packed_bwd_workspace_size.argtypes = [i64] * 7 + [i32]
+        lib.linear_attention_packed_bwd_workspace_size.restype = sz
         lib.sss_status_string.argtypes = [i32]
         lib.sss_status_string.restype = ctypes.c_char_p
         _lib = lib

@@ -1,8 +1,8 @@
 """Build libsss.so (gfx950) in-tree with hipcc.  No JIT, no torch extension machinery.
 
 Every source is compiled to an object in parallel (the selective scans once per state
-count, see the explicit instances at the end of csrc/selective_scan.hip and packed_scan.hip), then the objects
-are linked into the shared library.  Objects live in _build/ at the repository root.
+count, see the explicit instances at the end of csrc/selective_scan.hip and packed_scan.hip, and
+linear attention once per pair of head sizes), then the objects are linked into the shared library.  Objects live in _build/ at the repository root.
 """
 from __future__ import annotations
 
@@ -22,6 +22,7 @@ PROBE_SRC = os.path.join(CSRC, "probes", "roofline_probes.hip")
 PROBE_LIB = os.path.join(PKG, "libsss_probes.so")
 ARCH = "gfx950"
 STATE_COUNTS = (1, 2, 4, 8, 16, 32, 64)
+HEAD_SIZES = (64, 128, 256)  # rows and columns of linear attention's states, rounded up
 
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -45,6 +46,10 @@ def compile_jobs():
             jobs.append((os.path.join(OBJ, f"{stem}_host.o"), [], src))
             for n in STATE_COUNTS:
                 jobs.append((os.path.join(OBJ, f"{stem}_n{n}.o"), [f"-DSSS_INST_NS={n}"], src))
+        elif stem == "linear_attention":
+            for e in HEAD_SIZES:
+                for f in HEAD_SIZES:
+                    jobs.append((os.path.join(OBJ, f"{stem}_{e}x{f}.o"), [f"-DSSS_INST_E={e}", f"-DSSS_INST_F={f}"], src))
         else:
             jobs.append((os.path.join(OBJ, f"{stem}.o"), [], src))
     return jobs

@@ -1,0 +1,691 @@
+// linear_attention.hip -- gfx950 kernels of linear attention with a decay for each head, over packed
+// sequences: outputs and gradients.  With log decays g_t <= 0 and input weights b_t,
+//   S_t = e^(g_t) S_(t-1) + b_t k_t v_t^T,   o_t = scale q_t S_t + D v_t
+// and for a loss with gradients do_t, the adjoint of the state runs backwards in time:
+//   R_t = scale q_t do_t^T + e^(g_(t+1)) R_(t+1)
+//   dq_t = scale S_t do_t,  dk_t = b_t R_t v_t,  dv_t = b_t R_t^T k_t + D do_t
+//   db_t = k_t R_t v_t,     dg_t = <R_t, e^(g_t) S_(t-1)> = q_t dq_t - k_t dk_t + dg_(t+1)
+//
+// All of them are one walk in tiles of C tokens with a state M (E x F) in the accumulators of the
+// matrix cores, G the sums of g from the tile's first token on:
+//   out_i = sum_j e^(|G_i - G_j|) (x_i . y_j) z_j  +  e^(G_i) x_i M,   M <- e^(G_C) M + sum_j e^(G_C - G_j) y_j z_j^T
+//            walk         x   y   z    M
+//   outputs  forwards     q   k   v    S
+//   dq       forwards     do  v   k    S^T
+//   dk       backwards    v   do  q    R^T  (j >= i, and e^(G_C - G_i), e^(G_j) for the two weights)
+//   dv       backwards    k   q   do   R
+// The scores of a tile go through LDS once (bf16: rounded to bf16 there, an operand like the
+// others); M never leaves the registers of the wave that has its columns: a wave's accumulators of two
+// 16-row tiles are, rounded, the operand of 32 rows of the next product as they lie.
+//
+// The packed axis is cut in segments of K tokens, whatever the sequences; a workgroup takes one
+// segment and head.  The state that enters a segment comes from a first pass (kLaFold*: the update of M
+// alone, for the one sequence that runs across the segment's edge) and a sum over the segments.
+//
+// Sums, decays (64-bit) and M are fp32 or more.  What is rounded to bf16 on the way to a bf16 result:
+// scores and M.  What goes into fp32 results (the states, and the parts of dg, db that come from other
+// tiles) takes M and the weighted z as the sum of two or three bf16 parts, 16 or 24 bits of them.
+#include "linear_attention.h"
+
+#include "seq_walk.h"
+#include "vec.h"
+
+namespace sss {
+
+typedef __bf16 la_bf8 __attribute__((ext_vector_type(8)));
+typedef float la_f4 __attribute__((ext_vector_type(4)));
+typedef short la_s4 __attribute__((ext_vector_type(4)));
+typedef uint32_t la_u4 __attribute__((ext_vector_type(4)));
+
+// Eight values of a lane along a product's inner axis: lane l holds row (or column) l % 16 and
+// inner indices 8 (l / 16) + 0..7 of 32.  fp32 products take eight steps of four inner indices, one
+// element of each lane a step, so that both types have one layout.
+template <bool BF16>
+struct LaFrag;
+template <>
+struct LaFrag<true> {
+  la_u4 u;
+};
+template <>
+struct LaFrag<false> {
+  float f[8];
+};
+
+__device__ __forceinline__ la_f4 la_mma(const LaFrag<true>& a, const LaFrag<true>& b, la_f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(la_bf8, a.u), __builtin_bit_cast(la_bf8, b.u), c, 0, 0,
+                                                 0);
+}
+__device__ __forceinline__ la_f4 la_mma(const LaFrag<false>& a, const LaFrag<false>& b, la_f4 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.f[i], b.f[i], c, 0, 0, 0);
+  return c;
+}
+
+// N parts that add up to v to 8 N bits: each the nearest bf16 to what the ones before leave.
+// fp32: v itself.
+template <int N>
+__device__ __forceinline__ void la_split(const float (&v)[8], LaFrag<true> (&p)[N]) {
+  float rest[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = v[i];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = vec_bf16_pair(rest[2 * i], rest[2 * i + 1]);
+      p[n].u[i] = b;
+      if (n + 1 < N) {
+        rest[2 * i] -= __builtin_bit_cast(float, b << 16);
+        rest[2 * i + 1] -= __builtin_bit_cast(float, b & 0xFFFF0000u);
+      }
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void la_split(const float (&v)[8], LaFrag<false> (&p)[N]) {
+  static_assert(N == 1, "fp32 takes one part");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[0].f[i] = v[i];
+}
+__device__ __forceinline__ void la_widen(const LaFrag<true>& p, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = p.u[i];
+    v[2 * i] = __builtin_bit_cast(float, b << 16);
+    v[2 * i + 1] = __builtin_bit_cast(float, b & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void la_widen(const LaFrag<false>& p, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = p.f[i];
+}
+
+// LDS of one workgroup exchanged between its waves (global memory is not, within a launch)
+__device__ __forceinline__ void la_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// A tile in LDS: C rows of W elements, 16 bytes more between rows (so that 16 rows' pieces of 16
+// bytes fall in different banks).
+template <bool BF16, int W>
+struct LaTile {
+  static constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES, LD = W + VE;
+  // inner axis along the row: row r0 + l % 16, columns c0 + 8 (l / 16) + 0..7
+  static __device__ __forceinline__ LaFrag<BF16> rows(const char* t, int r0, int c0, int lane) {
+    const char* const p = t + ((r0 + (lane & 15)) * LD + c0 + 8 * (lane >> 4)) * ES;
+    LaFrag<BF16> f;
+    if constexpr (BF16) {
+      f.u = *(const la_u4*)p;
+    } else {
+      const la_f4 a = *(const la_f4*)p, b = *(const la_f4*)(p + 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.f[i] = a[i], f.f[4 + i] = b[i];
+    }
+    return f;
+  }
+  // inner axis along the column: rows r0 + 8 (l / 16) + 0..7, for the lane's column: l % 16 = 4 a + b
+  // stands for column c0 + A a + b.  bf16: the transposing read of LDS, in which the 16 lanes of a group
+  // read four rows of 16 elements, lane i four of row i / 4, and lane l gets column l of them.
+  template <int A>
+  static __device__ __forceinline__ LaFrag<BF16> cols(const char* t, int r0, int c0, int lane) {
+    const int l = lane & 15, g = lane >> 4;
+    LaFrag<BF16> f;
+    if constexpr (BF16) {
+      typedef __attribute__((address_space(3))) la_s4* lds_p;
+      const char* const p = t + ((r0 + 8 * g + (l >> 2)) * LD + c0 + A * (l & 3)) * ES;
+      const la_s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)p);
+      const la_s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(p + 4 * LD * ES));
+      const uint64_t lo = __builtin_bit_cast(uint64_t, a), hi = __builtin_bit_cast(uint64_t, b);
+      f.u = la_u4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    } else {
+      const char* const p = t + ((r0 + 8 * g) * LD + c0 + A * (l >> 2) + (l & 3)) * ES;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f.f[i] = *(const float*)(p + i * LD * ES);
+    }
+    return f;
+  }
+};
+
+// A tile on its way from memory to LDS, in registers of NT threads.
+template <bool BF16, int C, int W, int NT>
+struct LaLoad {
+  using T = LaTile<BF16, W>;
+  static constexpr int VE = T::VE, PER = W / VE, N = C * PER / NT;
+  static_assert(N * NT == C * PER, "whole pieces");
+  la_u4 v[N];
+  // rows base + r st, r < nr, of `width` elements; zeros elsewhere
+  __device__ __forceinline__ void load(const char* base, int64_t st, int nr, int width) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int r = n * (NT / PER) + (int)threadIdx.x / PER, c = (int)threadIdx.x % PER * VE;
+      v[n] = la_u4{0, 0, 0, 0};
+      if (r < nr && c < width) {
+        const char* const p = base + (r * st + c) * T::ES;
+        if (c + VE <= width) {
+          const vec_u4 x = *(const vec_u4*)p;
+          v[n] = la_u4{x.x, x.y, x.z, x.w};
+        } else {
+#pragma unroll
+          for (int q = 0; q < VE; ++q) {
+            if (c + q >= width) continue;
+            if constexpr (BF16) v[n][q >> 1] |= (uint32_t)(*(const uint16_t*)(p + 2 * q)) << (16 * (q & 1));
+            else v[n][q] = *(const vec_u1*)(p + 4 * q);
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* t) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int r = n * (NT / PER) + (int)threadIdx.x / PER, c = (int)threadIdx.x % PER * VE;
+      *(la_u4*)(t + (r * T::LD + c) * T::ES) = v[n];
+    }
+  }
+};
+
+// log decays below this leave nothing of a state in fp32; kept finite, so that differences of
+// their sums are numbers (a NaN stays one)
+__device__ __forceinline__ double la_log2_decay(float g) { return (g < -1e4f ? -1e4 : (double)g) * 1.4426950408889634074; }
+
+template <bool BF16, int E, int F, int MODE>
+struct LaShape {
+  static constexpr bool kRev = MODE == kLaFoldRev || MODE == kLaDk || MODE == kLaDv;
+  static constexpr bool kOut = MODE >= kLaFwd;
+  static constexpr bool kDots = MODE == kLaDq || MODE == kLaDk;
+  static constexpr int XM = BF16 && kDots ? 3 : 1;                                 // parts of M as an operand
+  static constexpr int UP = !BF16 ? 1 : MODE == kLaFwd || MODE == kLaDv ? 2 : 3;  // of the weighted z
+  static constexpr int NW = F == 256 ? 8 : 4, NT = NW * 64, NF = F / (16 * NW);
+  static constexpr int C = BF16 ? kLaTile : kLaTile / 2, TI = C / 16, KS = C / 32;
+  static constexpr int WPI = NW / TI, JT = TI / WPI > 0 ? TI / WPI : 1;  // waves per 16 rows of scores; their column tiles
+};
+
+template <bool BF16, int E, int F, int MODE>
+__global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) void la_walk_kernel(LaWalk g) {
+  using S = LaShape<BF16, E, F, MODE>;
+  constexpr int NW = S::NW, NT = S::NT, NF = S::NF, C = S::C, TI = S::TI, KS = S::KS, ET = E / 16, EK = E / 32;
+  constexpr bool kRev = S::kRev, kOut = S::kOut, kDots = S::kDots;
+  constexpr int ES = BF16 ? 2 : 4;
+  using TX = LaTile<BF16, E>;
+  using TZ = LaTile<BF16, F>;
+  using TP = LaTile<BF16, C>;
+  __shared__ __attribute__((aligned(16))) char lx[kOut ? C * TX::LD * ES : 16];
+  __shared__ __attribute__((aligned(16))) char ly[C * TX::LD * ES];
+  __shared__ __attribute__((aligned(16))) char lz[C * TZ::LD * ES];
+  __shared__ __attribute__((aligned(16))) char lw[kDots ? C * TZ::LD * ES : 16];
+  __shared__ __attribute__((aligned(16))) char lp[kOut ? C * TP::LD * ES : 16];
+  __shared__ double lg[C];                 // sums of log2 decays
+  __shared__ __attribute__((aligned(16))) float lsr[C], luw[C], lbeta[C];  // weights: x M, y z^T, beta
+  __shared__ float ltot;
+  __shared__ float lrr[kDots ? NW * C : 1], lri[MODE == kLaDq ? S::WPI * C : 1];
+  __shared__ float lred[NW];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int l16 = lane & 15, l4 = lane >> 4;
+  const unsigned id = xcd_remap(blockIdx.x, gridDim.x);
+  const int h = (int)(id % (unsigned)g.H);
+  int seg = (int)(id / (unsigned)g.H);
+  if constexpr (MODE == kLaFoldRev) ++seg;  // the first segment has no edge on its left
+  const int c0 = seg * g.K, tend = min(c0 + g.K, g.tokens);
+  const int lo = min(max(g.cu[0], 0), g.tokens), hi = min(max(g.cu[g.nseq], 0), g.tokens);
+  const int f0 = wave * (16 * NF);  // the wave's columns
+  const int Ew = g.y.width, Fw = g.z.width;
+  const char* const xp = kOut ? g.x.p + (h / g.x.rep) * g.x.sh * ES : nullptr;
+  const char* const yp = g.y.p + (h / g.y.rep) * g.y.sh * ES;
+  const char* const zp = g.z.p + (h / g.z.rep) * g.z.sh * ES;
+  const char* const wp = kDots ? g.w.p + (h / g.w.rep) * g.w.sh * ES : nullptr;
+
+  la_f4 M[ET][NF];
+  // Element r of a lane's accumulator t is row 32 (t / 2) + 8 (l / 16) + 4 (t % 2) + r of M.  fn(value, offset
+  // in a head's state) for those inside the head's sizes.  The offsets start from values that the compiler
+  // does not know, or it keeps all of them, for every accumulator, in registers over the loops.
+  auto each = [&](auto&& fn) __attribute__((always_inline)) {
+    int e0 = 8 * l4, f1 = f0 + l16;
+    asm volatile("" : "+v"(e0), "+v"(f1));
+    const int se = (int)g.se, sf = (int)g.sf;
+    const int at = e0 * se + f1 * sf;
+#pragma unroll
+    for (int t = 0; t < ET; ++t)
+#pragma unroll
+      for (int nf = 0; nf < NF; ++nf)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int e = 32 * (t >> 1) + 4 * (t & 1) + r;
+          if (e0 < Ew - e && f1 < Fw - 16 * nf) {
+            float v = M[t][nf][r];
+            fn(v, at + e * se + 16 * nf * sf);
+            M[t][nf][r] = v;
+          }
+        }
+  };
+  auto zero = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < ET; ++t)
+#pragma unroll
+      for (int nf = 0; nf < NF; ++nf) M[t][nf] = la_f4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  auto from = [&](const float* p) __attribute__((always_inline)) {
+    zero();
+    each([&](float& v, int o) __attribute__((always_inline)) { v = p[o]; });
+  };
+  auto to = [&](float* p) __attribute__((always_inline)) {
+    each([&](float& v, int o) __attribute__((always_inline)) { p[o] = v; });
+  };
+  const int64_t per = g.hs, at_seg = ((int64_t)seg * g.H + h) * per;
+  auto of_seq = [&](int64_t s) __attribute__((always_inline)) { return (s * g.H + h) * per; };
+
+  double total = 0.0;  // log2 of the decay over a folded part
+  float trace = 0.0f, through = 0.0f;
+
+  // tokens a .. e-1, of one sequence; adj: the adjoint behind them (null: zero), for `through`
+  auto walk = [&](int a, int e, const float* adj) __attribute__((always_inline)) {
+    LaLoad<BF16, C, E, NT> rx, ry;
+    LaLoad<BF16, C, F, NT> rz, rw;
+    float rg = 0.0f, rb = 0.0f;
+    const int ntile = (e - a + C - 1) / C;
+    auto fetch = [&](int m) __attribute__((always_inline)) {
+      const int t = a + m * C, nr = min(C, e - t);
+      if constexpr (kOut) rx.load(xp + (int64_t)t * g.x.st * ES, g.x.st, nr, Ew);
+      ry.load(yp + (int64_t)t * g.y.st * ES, g.y.st, nr, Ew);
+      rz.load(zp + (int64_t)t * g.z.st * ES, g.z.st, nr, Fw);
+      if constexpr (kDots) rw.load(wp + (int64_t)t * g.w.st * ES, g.w.st, nr, Fw);
+      if (wave == 0) {
+        rg = lane < nr ? g.g[(t + lane) * g.g_st + h] : 0.0f;
+        rb = lane >= nr ? 0.0f : g.beta != nullptr ? g.beta[(t + lane) * g.beta_st + h] : 1.0f;
+      }
+    };
+    fetch(kRev ? ntile - 1 : 0);
+    for (int k = 0; k < ntile; ++k) {
+      const int m = kRev ? ntile - 1 - k : k;
+      const int t0 = a + m * C, nr = min(C, e - t0);
+      la_barrier();  // the tile before has been read
+      if constexpr (kOut) rx.store(lx);
+      ry.store(ly);
+      rz.store(lz);
+      if constexpr (kDots) rw.store(lw);
+      if (wave == 0) {
+        double x = la_log2_decay(rg);
+#pragma unroll
+        for (int d = 1; d < C; d *= 2) {
+          const double up = __shfl_up(x, d);
+          if (lane >= d) x += up;
+        }
+        const double tot = __shfl(x, C - 1);
+        if (lane < C) {
+          const float in = fast_exp2((float)x), out = fast_exp2((float)(tot - x));
+          lg[lane] = x;
+          lsr[lane] = kRev ? out : g.scale * in;
+          luw[lane] = kRev ? g.scale * in : rb * out;
+          lbeta[lane] = rb;
+        }
+        if (lane == 0) ltot = fast_exp2((float)tot);
+        total += tot;
+      }
+      la_barrier();
+      if (k + 1 < ntile) fetch(kRev ? m - 1 : m + 1);
+      if constexpr (MODE == kLaDq) {
+        if (k + 1 == ntile) {
+          through = 0.0f;
+          if (adj != nullptr) {
+            each([&](float& v, int o) __attribute__((always_inline)) { through = __builtin_fmaf(v, adj[o], through); });
+            through *= ltot;
+          }
+        }
+      }
+
+      // z by columns, as it is and weighted
+      LaFrag<BF16> zf[KS][NF];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int nf = 0; nf < NF; ++nf) zf[ks][nf] = TZ::template cols<4>(lz, 32 * ks, f0 + 16 * nf, lane);
+
+      if constexpr (kOut) {
+        // scores of 16 rows and the column tiles of this wave, transposed: the lane has row i, columns j + r
+        const int it = wave / S::WPI, jt0 = (wave % S::WPI) * S::JT;
+        const int i = 16 * it + l16;
+        float ri = 0.0f;
+        if (jt0 < TI) {
+          LaFrag<BF16> xf[EK];
+#pragma unroll
+          for (int s = 0; s < EK; ++s) xf[s] = TX::rows(lx, 16 * it, 32 * s, lane);
+          const double gi = lg[i];
+          const float row_w = (kRev ? lbeta[i] : 1.0f) * g.scale;
+#pragma unroll
+          for (int q = 0; q < S::JT; ++q) {
+            const int jt = jt0 + q, j = 16 * jt + 4 * l4;
+            la_f4 sc = {0.0f, 0.0f, 0.0f, 0.0f}, other = sc;
+            float p[4] = {0.0f, 0.0f, 0.0f, 0.0f}, ci[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (kRev ? jt >= it : jt <= it) {
+#pragma unroll
+              for (int s = 0; s < EK; ++s) sc = la_mma(TX::rows(ly, 16 * jt, 32 * s, lane), xf[s], sc);
+              if constexpr (MODE == kLaDq) {  // q k^T
+#pragma unroll
+                for (int s = 0; s < F / 32; ++s)
+                  other = la_mma(TZ::rows(lz, 16 * jt, 32 * s, lane), TZ::rows(lw, 16 * it, 32 * s, lane), other);
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const double d = kRev ? lg[j + r] - gi : gi - lg[j + r];
+                const bool in = kRev ? j + r >= i : j + r <= i;
+                const float wt = in ? row_w * fast_exp2((float)d) : 0.0f;
+                const float b = kRev ? 1.0f : lbeta[j + r];
+                p[r] = in ? wt * b * sc[r] : 0.0f;
+                if constexpr (MODE == kLaDq) {
+                  ci[r] = in ? wt * sc[r] * other[r] : 0.0f;
+                  ri += b * ci[r];
+                  if (j + r == i) trace += sc[r];
+                }
+                if constexpr (MODE == kLaFwd || MODE == kLaDv) {
+                  if (g.D != nullptr && j + r == i) p[r] += g.D[h];
+                }
+              }
+            }
+            char* const to_p = lp + (i * TP::LD + j) * ES;
+            if constexpr (BF16) {
+              typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+              *(u2*)to_p = u2{vec_bf16_pair(p[0], p[1]), vec_bf16_pair(p[2], p[3])};
+            } else {
+              *(la_f4*)to_p = la_f4{p[0], p[1], p[2], p[3]};
+            }
+            if constexpr (MODE == kLaDq) {  // sums over the tile's rows
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                float v = ci[r];
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) v += __shfl_xor(v, d);
+                if (l16 == 0) *(float*)(lp + ((j + r) * TP::LD + C) * ES + 4 * it) = v;  // between the rows of the scores
+              }
+            }
+          }
+        }
+        if constexpr (MODE == kLaDq) {
+          ri += __shfl_xor(ri, 16);
+          ri += __shfl_xor(ri, 32);
+          if (l4 == 0 && jt0 < TI) lri[(wave % S::WPI) * C + i] = ri;
+        }
+        // x M, transposed: the lane has row i of the tokens, columns f + r
+        la_f4 o[TI][NF];
+#pragma unroll
+        for (int t = 0; t < TI; ++t)
+#pragma unroll
+          for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < EK; ++s) {
+          LaFrag<BF16> mf[NF][S::XM];
+#pragma unroll
+          for (int nf = 0; nf < NF; ++nf) {
+            float v[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = M[2 * s][nf][r], v[4 + r] = M[2 * s + 1][nf][r];
+            la_split<S::XM>(v, mf[nf]);
+          }
+#pragma unroll
+          for (int t = 0; t < TI; ++t) {
+            const LaFrag<BF16> xf = TX::rows(lx, 16 * t, 32 * s, lane);
+#pragma unroll
+            for (int nf = 0; nf < NF; ++nf)
+#pragma unroll
+              for (int q = S::XM - 1; q >= 0; --q) o[t][nf] = la_mma(mf[nf][q], xf, o[t][nf]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < TI; ++t) {
+          const float sr = lsr[16 * t + l16], rb_ = kRev ? lbeta[16 * t + l16] : 1.0f;
+          float dot = 0.0f;
+#pragma unroll
+          for (int nf = 0; nf < NF; ++nf) {
+            o[t][nf] *= sr;
+            if constexpr (kDots) {
+              const char* const pw = lw + ((16 * t + l16) * TZ::LD + f0 + 16 * nf + 4 * l4) * ES;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                float v;
+                if constexpr (BF16) v = __builtin_bit_cast(float, (uint32_t)(*(const uint16_t*)(pw + 2 * r)) << 16);
+                else v = *(const float*)(pw + 4 * r);
+                dot = __builtin_fmaf(v, o[t][nf][r], dot);
+              }
+            }
+            if constexpr (kRev) o[t][nf] *= rb_;
+          }
+          if constexpr (kDots) {
+            dot += __shfl_xor(dot, 16);
+            dot += __shfl_xor(dot, 32);
+            if (l4 == 0) lrr[wave * C + 16 * t + l16] = dot;
+          }
+        }
+        la_barrier();  // the scores are there
+        if constexpr (kDots) {
+          if (wave == 0) {  // C tokens, a lane each
+            const int i2 = lane & (C - 1);
+            const bool in = lane < nr;
+            const int64_t at = (int64_t)h * g.tokens + t0 + i2;
+            float v = 0.0f;
+#pragma unroll
+            for (int q = 0; q < NW; ++q) v += lrr[q * C + i2];
+            if (in) (MODE == kLaDq ? g.rows : g.cols2)[at] = v;
+            if constexpr (MODE == kLaDq) {
+              float rs = 0.0f, cs = 0.0f;
+#pragma unroll
+              for (int q = 0; q < S::WPI; ++q)
+                if (q * S::JT < TI) rs += lri[q * C + i2];
+#pragma unroll
+              for (int q = 0; q < TI; ++q) cs += *(const float*)(lp + (i2 * TP::LD + C) * ES + 4 * q);
+              float n = lane < C ? rs - lbeta[i2] * cs : 0.0f;
+#pragma unroll
+              for (int d = 1; d < C; d *= 2) {
+                const float up = __shfl_down(n, d);
+                if (lane + d < C) n += up;
+              }
+              if (in) {
+                g.within[at] = n;
+                g.cols[at] = cs;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < TI; ++t) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            if (kRev ? 2 * ks + 1 < t : 2 * ks > t) continue;
+            const LaFrag<BF16> pf = TP::rows(lp, 16 * t, 32 * ks, lane);
+#pragma unroll
+            for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_mma(zf[ks][nf], pf, o[t][nf]);
+          }
+          const int i2 = 16 * t + l16;
+          if (i2 < nr) {
+#pragma unroll
+            for (int nf = 0; nf < NF; ++nf) {
+              const int f = f0 + 16 * nf + 4 * l4;
+              const int64_t at = (int64_t)(t0 + i2) * g.out_st + h * g.out_sh + f;
+              const float v[4] = {o[t][nf][0], o[t][nf][1], o[t][nf][2], o[t][nf][3]};
+              if (BF16 && !g.out_f32) {
+                Vec<true, 4> r;
+                r.set(v);
+                if (f + 4 <= Fw) r.store(g.out + at * 2);
+                else if (f < Fw) {
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    if (f + q < Fw) ((uint16_t*)g.out)[at + q] = (uint16_t)(r.w[q >> 1] >> (16 * (q & 1)));
+                }
+              } else {
+                Vec<false, 4> r;
+                r.set(v);
+                if (f + 4 <= Fw) r.store(g.out + at * 4);
+                else if (f < Fw) {
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    if (f + q < Fw) ((float*)g.out)[at + q] = v[q];
+                }
+              }
+            }
+          }
+        }
+      }
+
+      // M <- e^(G_C) M + sum_j weight_j y_j z_j^T
+      const float keep = ltot;
+#pragma unroll
+      for (int t = 0; t < ET; ++t)
+#pragma unroll
+        for (int nf = 0; nf < NF; ++nf) M[t][nf] *= keep;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        LaFrag<BF16> wz[NF][S::UP];
+        const la_f4 u0 = *(const la_f4*)(luw + 32 * ks + 8 * l4), u1 = *(const la_f4*)(luw + 32 * ks + 8 * l4 + 4);
+#pragma unroll
+        for (int nf = 0; nf < NF; ++nf) {
+          float v[8];
+          la_widen(zf[ks][nf], v);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] *= u0[r], v[4 + r] *= u1[r];
+          la_split<S::UP>(v, wz[nf]);
+        }
+#pragma unroll
+        for (int t = 0; t < ET; ++t) {
+          const LaFrag<BF16> yf = TX::template cols<8>(ly, 32 * ks, 32 * (t >> 1) + 4 * (t & 1), lane);
+#pragma unroll
+          for (int nf = 0; nf < NF; ++nf)
+#pragma unroll
+            for (int q = S::UP - 1; q >= 0; --q) M[t][nf] = la_mma(yf, wz[nf][q], M[t][nf]);
+        }
+      }
+    }
+  };
+
+  // the same value in every thread
+  auto block_sum = [&](float v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    la_barrier();
+    if (lane == 0) lred[wave] = v;
+    la_barrier();
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) s += lred[q];
+    return s;
+  };
+
+  auto slot_of = [&](int s) __attribute__((always_inline)) {  // -1: none
+    if (g.state == nullptr) return -1;
+    const int slot = g.sidx != nullptr ? g.sidx[s] : s;
+    return (unsigned)slot < (unsigned)g.slots ? slot : -1;
+  };
+
+  if constexpr (!kOut) {
+    // the sequence that runs across this segment's right (left) edge
+    int flag = 0;  // 0: none; 1: it runs across the other edge too; 2: it begins (ends) in the segment
+    const int edge = kRev ? c0 : tend;
+    if (edge > lo && edge < hi) {
+      const int s = min(max(__builtin_amdgcn_readfirstlane(find_seq(g.cu, g.nseq, kRev ? c0 : tend - 1, lane)), 0), g.nseq - 1);
+      const int end = min(g.cu[s + 1], hi);
+      const int beg = max(g.cu[s], 0);
+      if (kRev ? beg < c0 && end > c0 : beg < tend && end > tend) {
+        zero();
+        if constexpr (kRev) {
+          flag = end <= tend ? 2 : 1;
+          if (flag == 2 && g.from != nullptr) from(g.from + of_seq(s));
+        } else {
+          flag = beg >= c0 ? 2 : 1;
+          if (flag == 2) {
+            const int slot = slot_of(s);
+            if (g.from != nullptr) from(g.from + of_seq(s));
+            else if (slot >= 0 && g.init != nullptr && g.init[s] != 0) {
+              from(g.state + of_seq(slot));
+              to(g.begin + at_seg);  // for the second pass: the slot itself is overwritten there, by another workgroup
+            }
+          }
+        }
+        walk(kRev ? c0 : max(beg, c0), kRev ? min(end, tend) : tend, nullptr);
+        to(g.end + at_seg);
+        if (threadIdx.x == 0) g.sum[(int64_t)seg * g.H + h] = (float)total;
+      }
+    }
+    if (h == 0 && threadIdx.x == 0) g.flag[seg] = flag;
+  } else {
+    int t = max(c0, lo);
+    const int stop = min(tend, hi);
+    if constexpr (MODE != kLaFwd) {  // gradients of tokens outside every sequence are zero
+      const int gap0 = min(t, tend), gap1 = max(stop, c0);
+      auto clear = [&](int a, int b) __attribute__((always_inline)) {
+        const int n = (b - a) * Fw;
+        for (int i = threadIdx.x; i < n; i += NT) {
+          const int64_t at = (int64_t)(a + i / Fw) * g.out_st + h * g.out_sh + i % Fw;
+          if (BF16 && !g.out_f32) ((uint16_t*)g.out)[at] = 0;
+          else ((float*)g.out)[at] = 0.0f;
+        }
+      };
+      clear(c0, gap0);
+      clear(max(gap1, gap0), tend);
+    }
+    int s = t < stop ? min(max(__builtin_amdgcn_readfirstlane(find_seq(g.cu, g.nseq, t, lane)), 0), g.nseq - 1) : 0;
+    while (t < stop) {
+      const int end = min(g.cu[s + 1], hi);
+      if (end <= t) {  // past this sequence (or an empty one)
+        if (++s >= g.nseq) break;
+        continue;
+      }
+      const int e = min(end, tend);
+      const bool before = began_before(g.cu[s], c0), after = end > tend;
+      if constexpr (MODE == kLaFwd) {
+        const int slot = slot_of(s);
+        if (before) from(g.enter + at_seg);
+        else if (slot >= 0 && g.init != nullptr && g.init[s] != 0) from(after ? g.begin + at_seg : g.state + of_seq(slot));
+        else zero();
+        walk(t, e, nullptr);
+        if (!after && slot >= 0) to(g.state + of_seq(slot));
+      } else if constexpr (MODE == kLaDq) {
+        if (before) from(g.enter + at_seg);
+        else if (g.from != nullptr) from(g.from + of_seq(s));
+        else zero();
+        const float* const adj = after ? g.back + at_seg : g.dfinal != nullptr ? g.dfinal + of_seq(s) : nullptr;
+        walk(t, e, adj);
+        const float v = adj != nullptr ? block_sum(through) : 0.0f;
+        if (threadIdx.x == 0) (after ? g.edge[(int64_t)seg * g.H + h] : g.last[(int64_t)s * g.H + h]) = v;
+      } else {
+        if (after) from(g.enter + at_seg);
+        else if (g.from != nullptr) from(g.from + of_seq(s));
+        else zero();
+        walk(t, e, nullptr);
+        if (MODE == kLaDk && !before && g.to != nullptr) to(g.to + of_seq(s));
+      }
+      t = e;
+    }
+    if constexpr (MODE == kLaDq) {
+      if (g.trace != nullptr) {
+        const float v = block_sum(trace);
+        if (threadIdx.x == 0) g.trace[(int64_t)seg * g.H + h] = v;
+      }
+    }
+  }
+}
+
+#ifdef SSS_INST_E
+template <int E, int F>
+hipError_t la_run(LaMode mode, bool bf16, const LaWalk& g, unsigned grid, hipStream_t stream) {
+#define SSS_LA_MODE(MODE)                                                                                          \
+  case MODE:                                                                                                       \
+    if (bf16) hipLaunchKernelGGL((la_walk_kernel<true, E, F, MODE>), dim3(grid),                                    \
+                                 dim3(LaShape<true, E, F, MODE>::NT), 0, stream, g);                               \
+    else hipLaunchKernelGGL((la_walk_kernel<false, E, F, MODE>), dim3(grid), dim3(LaShape<false, E, F, MODE>::NT), 0, \
+                            stream, g);                                                                            \
+    return hipGetLastError();
+  switch (mode) {
+    SSS_LA_MODE(kLaFoldFwd)
+    SSS_LA_MODE(kLaFoldRev)
+    SSS_LA_MODE(kLaFwd)
+    SSS_LA_MODE(kLaDq)
+    SSS_LA_MODE(kLaDk)
+    SSS_LA_MODE(kLaDv)
+  }
+#undef SSS_LA_MODE
+  return hipErrorInvalidValue;
+}
+template hipError_t la_run<SSS_INST_E, SSS_INST_F>(LaMode, bool, const LaWalk&, unsigned, hipStream_t);
+#endif
+
+}  // namespace sss

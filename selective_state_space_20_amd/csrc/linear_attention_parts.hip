@@ -1,0 +1,294 @@
+// linear_attention_parts.hip -- gfx950 kernels around the walks of linear_attention.hip: the states that
+// enter segments, the gradients of the decays, sums over shared heads, and the single-token step.
+#include "linear_attention.h"
+
+#include "colsum.h"
+#include "vec.h"
+
+#include <algorithm>
+
+namespace sss {
+
+// Walks are compiled once per pair of sizes (build.py).
+#define SSS_LA_EXTERN(E, F) extern template hipError_t la_run<E, F>(LaMode, bool, const LaWalk&, unsigned, hipStream_t);
+#define SSS_LA_SIZES(CALL) \
+  CALL(64, 64) CALL(64, 128) CALL(64, 256) CALL(128, 64) CALL(128, 128) CALL(128, 256) CALL(256, 64) CALL(256, 128) CALL(256, 256)
+SSS_LA_SIZES(SSS_LA_EXTERN)
+#undef SSS_LA_EXTERN
+
+hipError_t la_launch(int E, int F, LaMode mode, bool bf16, const LaWalk& g, unsigned grid, hipStream_t stream) {
+#define SSS_LA_CALL(E_, F_) \
+  if (E == E_ && F == F_) return la_run<E_, F_>(mode, bf16, g, grid, stream);
+  SSS_LA_SIZES(SSS_LA_CALL)
+#undef SSS_LA_CALL
+  return hipErrorInvalidValue;
+}
+
+// One thread per element of the heads' states, over the segments in turn, the loads of eight at once.
+constexpr int kLaCarryBatch = 8;
+static __global__ __launch_bounds__(256) void la_carry_kernel(const float* __restrict__ end, const float* __restrict__ sum,
+                                                              const int32_t* __restrict__ flag, float* __restrict__ enter,
+                                                              int64_t hs, int H, int nseg, int rev) {
+  const int64_t per = hs * H, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= per) return;
+  const int h = (int)(i / hs), last = nseg - 1;  // segments 0 .. nseg - 2, or backwards nseg - 1 .. 1
+  auto seg = [&](int n) { return rev ? last - n : n; };
+  float v = 0.0f;
+  for (int n0 = 0; n0 < last; n0 += kLaCarryBatch) {
+    float e[kLaCarryBatch], d[kLaCarryBatch];
+    int fl[kLaCarryBatch];
+#pragma unroll
+    for (int q = 0; q < kLaCarryBatch; ++q) fl[q] = n0 + q < last ? flag[seg(n0 + q)] : 0;
+#pragma unroll
+    for (int q = 0; q < kLaCarryBatch; ++q) {
+      e[q] = d[q] = 0.0f;
+      if (fl[q] != 0) {  // else nothing was written
+        e[q] = end[seg(n0 + q) * per + i];
+        d[q] = sum[(int64_t)seg(n0 + q) * H + h];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kLaCarryBatch; ++q) {
+      if (fl[q] == 0) continue;
+      v = fl[q] == 2 ? e[q] : __builtin_fmaf(fast_exp2(d[q]), v, e[q]);
+      enter[(int64_t)(rev ? seg(n0 + q) - 1 : seg(n0 + q) + 1) * per + i] = v;
+    }
+  }
+}
+
+hipError_t la_carry(const float* end, const float* sum, const int32_t* flag, float* enter, int64_t hs, int H, int nseg, bool rev,
+                    hipStream_t stream) {
+  hipLaunchKernelGGL(la_carry_kernel, dim3((unsigned)((hs * H + 255) / 256)), dim3(256), 0, stream, end, sum, flag, enter, hs, H,
+                     nseg, rev ? 1 : 0);
+  return hipGetLastError();
+}
+
+// dg_t, the sum over all pairs of tokens j < t <= i of their parts of the loss' gradient, tile by tile from the
+// right.  Pairs in one tile come summed (within).  The others: with r = q dq from earlier tiles and c = k dk from
+// later ones, those of a tile's own i are the r from t on, those of its own j the c before t, and those with both
+// outside (through) the sum of r of all tiles to the right less that of c from the tile on.  The last tile of a
+// segment's part of a sequence starts that sum with a `through` of its own, formed without a difference.  (Whole dq
+// and dk would do as well, but roundings of pairs that cancel would be carried over the segment.)  A wave per segment
+// and head; the sums are 64-bit.
+static __global__ __launch_bounds__(64) void la_finish_kernel(LaFinish a) {
+  const int lane = threadIdx.x;
+  const int h = (int)(blockIdx.x % (unsigned)a.H), seg = (int)(blockIdx.x / (unsigned)a.H);
+  const int c0 = seg * a.K, tend = min(c0 + a.K, a.tokens);
+  const int lo = min(max(a.cu[0], 0), a.tokens), hi = min(max(a.cu[a.nseq], 0), a.tokens);
+  const int64_t H = a.H;
+  double sum = 0.0;
+  auto clear = [&](int b, int e) {
+    for (int t = b + lane; t < e; t += 64) {
+      if (a.part == nullptr) a.dg[t * H + h] = 0.0f;
+      if (a.dbeta != nullptr) a.dbeta[t * H + h] = 0.0f;
+    }
+  };
+  int t = max(c0, lo);
+  const int stop = min(tend, hi);
+  const int gap = min(t, tend);
+  clear(c0, gap);
+  clear(max(max(stop, c0), gap), tend);
+  int s = t < stop ? min(max(__builtin_amdgcn_readfirstlane(find_seq(a.cu, a.nseq, t, lane)), 0), a.nseq - 1) : 0;
+  while (t < stop) {
+    const int end = min(a.cu[s + 1], hi);
+    if (end <= t) {
+      if (++s >= a.nseq) break;
+      continue;
+    }
+    const int e = min(end, tend);
+    double through = end > tend ? a.edge[seg * H + h] : a.last[s * H + h], x = 0.0;
+    const int last = (e - t - 1) / a.tile;
+    for (int m = last; m >= 0; --m) {
+      const int at = t + a.tile * m + lane;
+      const bool in = lane < a.tile && at < e;
+      float r = 0.0f, c = 0.0f, w = 0.0f;
+      if (in) {
+        const int64_t p = (int64_t)h * a.tokens + at;
+        r = a.rows[p];
+        c = a.cols2[p];
+        w = a.within[p];
+        if (a.dbeta != nullptr) a.dbeta[at * H + h] = a.cols[p] + c;
+        if (a.beta != nullptr) c *= a.beta[at * a.beta_st + h];
+      }
+      double rs = (double)r, cs = (double)c;  // from the lane on; up to the lane
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const double up = __shfl_down(rs, d), dn = __shfl_up(cs, d);
+        if (lane + d < 64) rs += up;
+        if (lane >= d) cs += dn;
+      }
+      if (m != last) through = x - __shfl(cs, 63);
+      x = through + __shfl(rs, 0);
+      if (in) {
+        const double v = through + rs + (cs - (double)c) + (double)w;
+        if (a.part == nullptr) a.dg[at * H + h] = (float)v;
+        else sum += v;
+      }
+    }
+    t = e;
+  }
+  if (a.part != nullptr) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    if (lane == 0) a.part[seg * H + h] = (float)sum;
+  }
+}
+
+static __global__ __launch_bounds__(256) void la_colsum_kernel(const float* __restrict__ part, float* __restrict__ out, int rows,
+                                                               int64_t cols) {
+  column_sums<8>(part, rows, cols, [=](int64_t col, float s) { out[col] = s; });
+}
+
+hipError_t la_finish(const LaFinish& a, hipStream_t stream) {
+  if (a.nseg > 0) hipLaunchKernelGGL(la_finish_kernel, dim3((unsigned)(a.nseg * a.H)), dim3(64), 0, stream, a);
+  if (a.part != nullptr)
+    hipLaunchKernelGGL(la_colsum_kernel, dim3(colsum_blocks(a.H)), dim3(256), 0, stream, a.part, a.dg, a.nseg, (int64_t)a.H);
+  if (a.dD != nullptr)
+    hipLaunchKernelGGL(la_colsum_kernel, dim3(colsum_blocks(a.H)), dim3(256), 0, stream, a.trace, a.dD, a.nseg, (int64_t)a.H);
+  return hipGetLastError();
+}
+
+template <bool BF16>
+static __global__ __launch_bounds__(256) void la_sum_heads_kernel(const float* __restrict__ part, char* __restrict__ out, int64_t n,
+                                                                  int rep, int d) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // an element of out
+  if (i >= n) return;
+  const int64_t row = i / d;
+  const float* p = part + row * rep * d + (i - row * d);
+  float s = 0.0f;
+  for (int r = 0; r < rep; ++r) s += p[(int64_t)r * d];
+  if constexpr (BF16) ((uint16_t*)out)[i] = (uint16_t)vec_bf16_pair(s, 0.0f);
+  else ((float*)out)[i] = s;
+}
+
+hipError_t la_sum_heads(const float* part, void* out, int64_t tokens, int heads, int rep, int d, bool bf16, hipStream_t stream) {
+  const int64_t n = tokens * (heads / rep) * d;
+  const dim3 grid((unsigned)((n + 255) / 256));
+  if (bf16) hipLaunchKernelGGL(la_sum_heads_kernel<true>, grid, dim3(256), 0, stream, part, (char*)out, n, rep, d);
+  else hipLaunchKernelGGL(la_sum_heads_kernel<false>, grid, dim3(256), 0, stream, part, (char*)out, n, rep, d);
+  return hipGetLastError();
+}
+
+static __global__ __launch_bounds__(256) void la_empty_kernel(const int32_t* __restrict__ cu, const float* __restrict__ dfinal,
+                                                              float* __restrict__ dinitial, int nseq, int tokens, int64_t per) {
+  const int64_t s = blockIdx.x;
+  const int lo = min(max(cu[0], 0), tokens), hi = min(max(cu[nseq], 0), tokens);
+  if (min(cu[s + 1], hi) > max(cu[s], lo)) return;
+  for (int64_t i = threadIdx.x; i < per; i += 256) dinitial[s * per + i] = dfinal != nullptr ? dfinal[s * per + i] : 0.0f;
+}
+
+hipError_t la_empty(const int32_t* cu, const float* dfinal, float* dinitial, int nseq, int tokens, int64_t per, hipStream_t stream) {
+  hipLaunchKernelGGL(la_empty_kernel, dim3((unsigned)nseq), dim3(256), 0, stream, cu, dfinal, dinitial, nseq, tokens, per);
+  return hipGetLastError();
+}
+
+// One token of each row: S <- e^g S + beta k v^T in its slot, o = scale q S + D v.  A workgroup takes a row
+// and head: V adjacent columns and every RL-th row of S per thread, eight loads in flight.  Bound by the
+// states, read once and written once.
+template <bool BF16>
+__device__ __forceinline__ float la_get(const char* p, int64_t i) {
+  if constexpr (BF16) return __builtin_bit_cast(float, (uint32_t)((const uint16_t*)p)[i] << 16);
+  else return ((const float*)p)[i];
+}
+
+template <bool BF16, int V, int CG>
+static __global__ __launch_bounds__(256) void la_step_kernel(LaStep a) {
+  constexpr int RL = 256 / CG, ES = BF16 ? 2 : 4;
+  constexpr int G = CG < 64 ? 4 : RL;  // partial sums of an output
+  __shared__ float lq[256], lk[256], lo[G * CG * V];
+  const int tid = threadIdx.x;
+  const int64_t b = blockIdx.x / (unsigned)a.H;
+  const int h = (int)(blockIdx.x - (unsigned)b * (unsigned)a.H);
+  const int dk = a.q.width, dv = a.v.width;
+  const int c = (tid % CG) * V, rl = tid / CG;
+  const int slot = a.sidx != nullptr ? a.sidx[b] : (int)b;
+  const bool kept = (unsigned)slot < (unsigned)a.slots, in = c < dv;
+  float* const S = kept ? a.state + ((int64_t)slot * a.H + h) * dk * dv + c : nullptr;
+  constexpr int B = 8;
+  Vec<false, V> s[B];
+  auto load = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int e = e0 + i * RL;
+      if (kept && in && e < dk) s[i].template load<true>(S + (int64_t)e * dv);
+      else s[i].zero();
+    }
+  };
+  load(rl);
+  if (tid < dk) {
+    const char* const q = a.q.p + ((h / a.q.rep) * a.q.sh + b * a.q.st) * ES;
+    const char* const k = a.k.p + ((h / a.k.rep) * a.k.sh + b * a.k.st) * ES;
+    lq[tid] = la_get<BF16>(q, tid) * a.scale;
+    lk[tid] = la_get<BF16>(k, tid) * (a.beta != nullptr ? a.beta[b * a.beta_st + h] : 1.0f);
+  }
+  const float gv = a.g[b * a.g_st + h];
+  const float decay = fast_exp2((float)((double)(gv < -1e4f ? -1e4f : gv) * 1.4426950408889634074));
+  const char* const vp = a.v.p + ((h / a.v.rep) * a.v.sh + b * a.v.st) * ES;
+  float v[V], o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = in ? la_get<BF16>(vp, c + i) : 0.0f;
+    o[i] = 0.0f;
+  }
+  __syncthreads();
+  for (int e0 = rl; e0 < dk; e0 += B * RL) {
+    if (e0 != rl) load(e0);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int e = e0 + i * RL;
+      if (e >= dk) continue;
+      const float kk = lk[e], qq = lq[e];
+      float n[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        n[j] = __builtin_fmaf(decay, s[i].get(j), kk * v[j]);
+        o[j] = __builtin_fmaf(qq, n[j], o[j]);
+      }
+      if (kept && in) {
+        Vec<false, V> r;
+        r.set(n);
+        r.template store<true>(S + (int64_t)e * dv);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int d = CG; d < 64; d *= 2) o[j] += __shfl_xor(o[j], d);
+    if (CG >= 64 || (tid & 63) < CG) lo[(CG < 64 ? tid / 64 : rl) * (CG * V) + c + j] = o[j];
+  }
+  __syncthreads();
+  for (int f = tid; f < dv; f += 256) {
+    float r = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G; ++i) r += lo[i * (CG * V) + f];
+    if (a.D != nullptr) r += a.D[h] * la_get<BF16>(vp, f);
+    const int64_t at = (b * a.H + h) * dv + f;
+    if constexpr (BF16) ((uint16_t*)a.out)[at] = (uint16_t)vec_bf16_pair(r, 0.0f);
+    else ((float*)a.out)[at] = r;
+  }
+}
+
+template <bool BF16>
+static hipError_t la_step_of(const LaStep& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.rows * a.H));
+  const int dv = a.v.width;
+#define SSS_LA_STEP(V, CG) hipLaunchKernelGGL((la_step_kernel<BF16, V, CG>), grid, dim3(256), 0, stream, a)
+  if (dv % 4 == 0) {  // 16 adjacent bytes per lane
+    if (dv <= 64) SSS_LA_STEP(4, 16);
+    else if (dv <= 128) SSS_LA_STEP(4, 32);
+    else SSS_LA_STEP(4, 64);
+  } else {
+    if (dv <= 64) SSS_LA_STEP(1, 64);
+    else if (dv <= 128) SSS_LA_STEP(1, 128);
+    else SSS_LA_STEP(1, 256);
+  }
+#undef SSS_LA_STEP
+  return hipGetLastError();
+}
+
+hipError_t la_step(const LaStep& a, bool bf16, hipStream_t stream) {
+  return bf16 ? la_step_of<true>(a, stream) : la_step_of<false>(a, stream);
+}
+
+}  // namespace sss
