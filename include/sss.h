@@ -36,6 +36,10 @@
  *      the scan, fused with the gate, and between blocks, fused with the residual addition, a
  *      norm of the block's output and its scale.
  *
+ *  layer_norm_fwd / _bwd -- the layer norm over rows or groups of channels, alone or after the residual
+ *      addition; linear_attention_packed_fwd, _update_slots, _packed_bwd -- linear attention with a decay
+ *      for each head, the scan's head form.
+ *
  *  elementwise_scan -- the per-channel form of "15. Selective (Data-Dependent) SSM
  *      Scan" (Reference solution): h = A_t*h + B_t*x_t, y_t = C_t*h.
  *
@@ -392,6 +396,33 @@ int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const voi
                           const float* rstd_post, const float* rstd, void* dx, void* dresidual, float* dweight,
                           float* dpost_weight, float* dscale, int64_t rows, int64_t dim, float alpha, int io_dtype,
                           int residual_dtype, void* workspace, size_t workspace_bytes, sss_stream_t stream);
+
+/* Layer norm over groups of `group` adjacent channels (a divisor of dim, at most 32768:
+ * SSS_ERR_UNSUPPORTED otherwise), alone or after the residual addition:
+ *   h = x + residual  (or x),  out = (h - mean(h)) rstd(h) weight + bias,
+ *   rstd(h) = (mean((h - mean(h))^2) + eps)^-1/2.
+ * x (rows, dim) and out (contiguous) in io_dtype; residual and residual_out (contiguous: h) in
+ * residual_dtype (ignored where neither is given); weight, bias (dim) float32; mean, rstd (rows,
+ * dim / group) float32: outputs for the gradients call.  Nullable: residual (zero), weight (one), bias (zero), residual_out, mean, rstd.
+ * out is of h before it is rounded to residual_dtype.  residual_out may be residual itself
+ * (contiguous), no other overlap.  Required: x, out. */
+int layer_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const float* weight,
+                   const float* bias, void* out, void* residual_out, float* mean, float* rstd, int64_t rows, int64_t dim,
+                   int64_t group, float eps, int io_dtype, int residual_dtype, sss_stream_t stream);
+
+/* Bytes of workspace layer_norm_bwd needs on `device` (0 on invalid sizes). */
+size_t layer_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, int device);
+
+/* Its gradients for L = sum(dout * out) + sum(dresidual_out * residual_out) (dresidual_out nullable:
+ * zero).  x (rows, dim) in x_dtype is what was normed: the forward call's x, or its residual_out; mean, rstd as
+ * it left them.  dout and dx (rows, dim) in io_dtype, dresidual_out and dresidual (nullable) in x_dtype, all
+ * contiguous; dx and dresidual are the same gradient (of x and of the residual).  dweight (dim), required
+ * with weight, and dbias (dim), nullable, float32, are summed over the rows in a fixed order; with no
+ * rows they are zero. */
+int layer_norm_bwd(const void* dout, const void* dresidual_out, const void* x, int64_t x_stride, const float* weight,
+                   const float* mean, const float* rstd, void* dx, void* dresidual, float* dweight, float* dbias,
+                   int64_t rows, int64_t dim, int64_t group, int io_dtype, int x_dtype, void* workspace,
+                   size_t workspace_bytes, sss_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * Linear attention with a decay for each head: the scan's head form, with one decay per head (and

@@ -20,6 +20,8 @@ include/sss.h); this package is its thin Python binding:
   * ``rms_norm_gated_fwd`` / ``rms_norm_gated_bwd``: the norm after the scan, fused with the gate;
     ``rms_norm_residual_fwd`` / ``rms_norm_residual_bwd``: the residual addition between blocks,
     fused with a norm of the block's output, its scale and the next block's norm
+  * ``layer_norm_fwd`` / ``layer_norm_bwd``: the layer norm over rows or groups of channels (heads), alone or
+    after the residual addition
   * ``linear_attention_packed_fwd`` / ``linear_attention_update_slots``: linear attention with a decay for
     each head (the scan's head form), over packed prompts and for single tokens, its states in cache
     slots; ``linear_attention_packed_bwd``: its gradients
@@ -38,7 +40,7 @@ from ._lib import (EXPORTED, LIB_PATH, SSSError, SSS_BF16, SSS_DELTA_SOFTPLUS, S
                    selective_scan_fwd_workspace_size, selective_scan_fwd_ex_workspace_size,
                    selective_state_update, selective_state_update_raw,
                    status_string)
-from ._block import (causal_conv1d_bwd, causal_conv1d_bwd_workspace_size, causal_conv1d_packed_fwd,
+from ._block import (layer_norm_bwd, layer_norm_bwd_workspace_size, layer_norm_fwd, causal_conv1d_bwd, causal_conv1d_bwd_workspace_size, causal_conv1d_packed_fwd,
                      causal_conv1d_update, rms_norm_gated_bwd, rms_norm_gated_bwd_workspace_size, rms_norm_gated_fwd,
                      rms_norm_residual_bwd, rms_norm_residual_bwd_workspace_size, rms_norm_residual_fwd,
                      selective_scan_packed_fwd, selective_scan_packed_fwd_workspace_size,
@@ -59,5 +61,6 @@ __all__ = ["causal_conv1d_packed_fwd", "causal_conv1d_update", "causal_conv1d_bw
            "selective_scan_fwd_ex_workspace_size", "selective_scan_fwd_ex_raw", "selective_scan_fwd_noalloc_raw",
            "selective_scan_states_size", "selective_scan_fwd_save_raw", "selective_scan_bwd_saved_raw",
            "linear_attention_packed_fwd", "linear_attention_packed_fwd_workspace_size", "linear_attention_update_slots",
+           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_size",
            "linear_attention_packed_bwd", "linear_attention_packed_bwd_workspace_size",
            "LIB_PATH", "EXPORTED", "load"]

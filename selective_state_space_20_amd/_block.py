@@ -539,3 +539,84 @@ def rms_norm_residual_bwd(dout, dresidual_out=None, *, residual_out, weight, rst
     if stream is not None:
         _keep(stream, gpu, workspace, *res.values())
     return res
+
+
+def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, group_size=None, eps=1e-5, out=None, residual_out=None,
+                   return_stats=False, stream=None):
+    """Layer norm over rows, or over groups of group_size channels, alone or after the residual addition:
+    out = (h - mean(h)) * rstd(h) * weight + bias with h = x, or residual + x.
+
+    x (rows, dim) float32 or bfloat16, residual (rows, dim) float32 or bfloat16, rows may be strided;
+    weight, bias (dim) float32.  Returns out in x's dtype; with a residual (or residual_out) also
+    residual_out = h in its dtype, which may be the residual itself; and with return_stats the (rows,
+    groups) float32 mean and rstd that layer_norm_bwd takes."""
+    torch = torch_()
+    gpu = x.get_device()
+    rows, dim = _two_d(x, "x")
+    xc = _code(x.dtype, "x")
+    g = _group(dim, group_size)
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, gpu)
+    wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
+    bp = _dense(bias, "bias", torch.float32, (dim,), gpu)
+    o, op = _out(out, "out", x, x.dtype, (rows, dim), gpu, stream)
+    hp, hs, h, ho, hc = 0, 0, None, 0, xc
+    if residual is not None or residual_out is not None:
+        hd = residual.dtype if residual is not None else residual_out.dtype
+        hc = _code(hd, "residual")
+        if residual is not None:
+            hp, hs = _rows(residual, "residual", hd, rows, dim, gpu)
+        h, ho = _out(residual_out, "residual_out", x, hd, (rows, dim), gpu, stream)
+    mean, rstd = (_new(x, (rows, dim // g), torch.float32, stream) for _ in range(2)) if return_stats else (None, None)
+    if rows > 0:
+        rc = _library(gpu).layer_norm_fwd(xp, xs, hp, hs, wp, bp, op, ho, mean.data_ptr() if return_stats else 0,
+                                          rstd.data_ptr() if return_stats else 0, rows, dim, g, float(eps), xc, hc,
+                                          _stream(stream, gpu))
+        if rc != 0:
+            raise SSSError(rc, "layer_norm_fwd")
+        if stream is not None:
+            _keep(stream, gpu, o, h, mean, rstd)
+    if not return_stats:
+        return o if h is None else (o, h)
+    return (o, mean, rstd) if h is None else (o, h, mean, rstd)
+
+
+def layer_norm_bwd_workspace_size(rows, dim, group_size=None, device=0) -> int:
+    return int(load().layer_norm_bwd_workspace_size(rows, dim, _group(dim, group_size), device))
+
+
+def layer_norm_bwd(dout, x, weight=None, *, mean, rstd, bias=False, dresidual_out=None, want_dresidual=None, group_size=None,
+                   workspace=None, stream=None):
+    """Gradients of sum(dout * out) + sum(dresidual_out * residual_out) of layer_norm_fwd.
+
+    x (rows, dim) is what was normed, the forward call's x or its residual_out, rows may be strided; mean,
+    rstd as it returned them; dout (rows, dim) in the forward x's dtype and dresidual_out (or None) in x's,
+    contiguous.  Returns a dict of dx (dout's dtype), dweight with weight, dbias with bias=True, float32, and
+    dresidual (x's dtype; by default with dresidual_out)."""
+    torch = torch_()
+    gpu = x.get_device()
+    rows, dim = _two_d(x, "x")
+    xc, dc = _code(x.dtype, "x"), _code(dout.dtype, "dout")
+    g = _group(dim, group_size)
+    dp = _dense(dout, "dout", dout.dtype, (rows, dim), gpu)
+    ep = _dense(dresidual_out, "dresidual_out", x.dtype, (rows, dim), gpu)
+    xp, xs = _rows(x, "x", x.dtype, rows, dim, gpu)
+    wp = _dense(weight, "weight", torch.float32, (dim,), gpu)
+    mp = _dense(mean, "mean", torch.float32, (rows, dim // g), gpu)
+    rp = _dense(rstd, "rstd", torch.float32, (rows, dim // g), gpu)
+    res = {"dx": _new(x, (rows, dim), dout.dtype, stream)}
+    if want_dresidual if want_dresidual is not None else dresidual_out is not None:
+        res["dresidual"] = _new(x, (rows, dim), x.dtype, stream)
+    if weight is not None:
+        res["dweight"] = _new(x, (dim,), torch.float32, stream)
+    if bias:
+        res["dbias"] = _new(x, (dim,), torch.float32, stream)
+    ptr = lambda k: res[k].data_ptr() if k in res else 0
+    need = layer_norm_bwd_workspace_size(rows, dim, g, gpu) if workspace is None else 0
+    workspace, wsp, wsn = _scratch(workspace, need, x, stream)
+    rc = _library(gpu).layer_norm_bwd(dp, ep, xp, xs, wp, mp, rp, ptr("dx"), ptr("dresidual"), ptr("dweight"), ptr("dbias"),
+                                      rows, dim, g, dc, xc, wsp, wsn, _stream(stream, gpu))
+    if rc != 0:
+        raise SSSError(rc, "layer_norm_bwd")
+    if stream is not None:
+        _keep(stream, gpu, workspace, *res.values())
+    return res

@@ -33,7 +33,8 @@ EXPORTED = ("selective_scan_fwd", "selective_scan_fwd_ex", "selective_scan_fwd_w
             "rms_norm_residual_bwd", "rms_norm_residual_bwd_workspace_size",
             "linear_attention_packed_fwd", "linear_attention_packed_fwd_workspace_size",
             "linear_attention_update_slots", "linear_attention_packed_bwd",
-            "linear_attention_packed_bwd_workspace_size")
+            "linear_attention_packed_bwd_workspace_size",
+            "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_size")
 
 
 class SSSError(RuntimeError):
@@ -120,6 +121,12 @@ def load() -> ctypes.CDLL:
         lib.rms_norm_residual_bwd.restype = i32
         lib.rms_norm_residual_bwd_workspace_size.argtypes = [i64] * 2 + [i32]
         lib.rms_norm_residual_bwd_workspace_size.restype = sz
+        lib.layer_norm_fwd.argtypes = [vp, i64, vp, i64] + [vp] * 6 + [i64] * 3 + [f32, i32, i32, vp]
+        lib.layer_norm_fwd.restype = i32
+        lib.layer_norm_bwd.argtypes = [vp] * 3 + [i64] + [vp] * 7 + [i64] * 3 + [i32, i32, vp, sz, vp]
+        lib.layer_norm_bwd.restype = i32
+        lib.layer_norm_bwd_workspace_size.argtypes = [i64] * 3 + [i32]
+        lib.layer_norm_bwd_workspace_size.restype = sz
         heads = [vp, i64, i64, i64] * 2 + [vp, i64, i64, vp, i64, vp, i64, vp, f32]
         lib.linear_attention_packed_fwd.argtypes = heads + [vp] * 5 + [i64] * 6 + [i32, vp, sz, vp]
         lib.linear_attention_packed_fwd.restype = i32

@@ -531,4 +531,108 @@ int selective_state_update_slots(const void* x, int64_t x_stride, const void* de
                    bc_dtype, y_dtype, nullptr, 0, true, stream);
 }
 
+int layer_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const float* weight,
+                   const float* bias, void* out, void* residual_out, float* mean, float* rstd, int64_t rows, int64_t dim,
+                   int64_t group, float eps, int io_dtype, int residual_dtype, sss_stream_t stream) {
+  if (!x || !out) return SSS_ERR_NULL_ARG;
+  const bool stream_used = residual || residual_out;
+  const int hd = stream_used ? residual_dtype : io_dtype;
+  const bool fp32 = io_dtype == SSS_F32 || hd == SSS_F32;
+  const int st = norm_dims(rows, dim, group, fp32);
+  if (st != SSS_OK) return st;
+  if (!dtype_ok(io_dtype) || !dtype_ok(hd)) return SSS_ERR_UNSUPPORTED;
+  if (!stride_ok(x_stride, dim) || (residual && !stride_ok(residual_stride, dim))) return SSS_ERR_BAD_DIM;
+  const int64_t es = dtype_size(io_dtype), hs = dtype_size(hd);
+  // the residual stream may be updated in place: the same rows, or no shared memory at all
+  const bool in_place = residual && residual == residual_out && (residual_stride == dim || rows <= 1);
+  Regions r;
+  r.in(x, span(rows, x_stride, dim, es), es);
+  if (!in_place) r.in(residual, span(rows, residual_stride, dim, hs), hs);
+  r.in(weight, dim * 4, 4);
+  r.in(bias, dim * 4, 4);
+  r.output(out, rows * dim * es, es);
+  r.output(residual_out, rows * dim * hs, hs);
+  r.output(mean, rows * (dim / group) * 4, 4);
+  r.output(rstd, rows * (dim / group) * 4, 4);
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  if (rows == 0) return SSS_OK;
+  LayerNormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.b = bias;
+  a.out = out;
+  a.residual_out = residual_out;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.group = group;
+  a.groups = dim / group;
+  a.sx = x_stride;
+  a.sr = residual ? residual_stride : 0;
+  a.eps = eps;
+  a.x_bf16 = io_dtype == SSS_BF16;
+  a.h_bf16 = hd == SSS_BF16;
+  return status_of(launch_layer_norm_fwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t layer_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, int device) {
+  return norm_bwd_bytes(rows, dim, group, 2, device);
+}
+
+int layer_norm_bwd(const void* dout, const void* dresidual_out, const void* x, int64_t x_stride, const float* weight,
+                   const float* mean, const float* rstd, void* dx, void* dresidual, float* dweight, float* dbias,
+                   int64_t rows, int64_t dim, int64_t group, int io_dtype, int x_dtype, void* workspace,
+                   size_t workspace_bytes, sss_stream_t stream) {
+  if ((rows != 0 && (!dout || !x || !mean || !rstd || !dx)) || (weight && !dweight)) return SSS_ERR_NULL_ARG;
+  const bool fp32 = io_dtype == SSS_F32 || x_dtype == SSS_F32;
+  const int st = norm_bwd_dims(rows, dim, group, fp32);
+  if (st != SSS_OK) return st;
+  if (!dtype_ok(io_dtype) || !dtype_ok(x_dtype)) return SSS_ERR_UNSUPPORTED;
+  if (!stride_ok(x_stride, dim)) return SSS_ERR_BAD_DIM;
+  const int64_t es = dtype_size(io_dtype), hs = dtype_size(x_dtype);
+  Regions r;
+  r.in(dout, rows * dim * es, es);
+  r.in(dresidual_out, rows * dim * hs, hs);
+  r.in(x, span(rows, x_stride, dim, hs), hs);
+  r.in(weight, dim * 4, 4);
+  r.in(mean, rows * (dim / group) * 4, 4);
+  r.in(rstd, rows * (dim / group) * 4, 4);
+  r.output(dx, rows * dim * es, es);
+  r.output(dresidual, rows * dim * hs, hs);
+  r.output(dweight, dim * 4, 4);
+  r.output(dbias, dim * 4, 4);
+  if (workspace && !aligned16(workspace)) return SSS_ERR_UNSUPPORTED;
+  if (!r.aligned) return SSS_ERR_UNSUPPORTED;
+  if (!r.ok()) return SSS_ERR_ALIAS;
+  const int cus = current_device_cus();
+  if (cus <= 0) return SSS_ERR_HIP;
+  const NormPlan pl = plan_norm_bwd(rows, group, dim / group, (dweight ? 1 : 0) + (dbias ? 1 : 0), fp32, cus);
+  if (pl.ws_total > 0) {
+    if (workspace == nullptr || workspace_bytes < pl.ws_total) return SSS_ERR_WORKSPACE;
+    r.output(workspace, (int64_t)pl.ws_total, 16);
+    if (!r.ok()) return SSS_ERR_ALIAS;
+  }
+  LayerNormArgs a{};
+  a.x = x;
+  a.w = weight;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.dout = dout;
+  a.dres_out = dresidual_out;
+  a.dx = dx;
+  a.dres = dresidual;
+  a.dw = dweight;
+  a.db = dbias;
+  a.workspace = workspace;
+  a.rows = rows;
+  a.group = group;
+  a.groups = dim / group;
+  a.sx = x_stride;
+  a.x_bf16 = io_dtype == SSS_BF16;
+  a.h_bf16 = x_dtype == SSS_BF16;
+  return status_of(launch_layer_norm_bwd(a, pl, reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -294,6 +294,32 @@ hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, const NormPlan& plan, h
 hipError_t launch_res_norm_fwd(const ResNormArgs& a, hipStream_t stream);
 hipError_t launch_res_norm_bwd(const ResNormArgs& a, const NormPlan& plan, hipStream_t stream);
 
+// Layer norm (layer_norm.hip).
+struct LayerNormArgs {
+  const void* x;         // backward: what was normed (the forward's x or residual_out), of the stream's type
+  const void* residual;  // nullable: zero
+  const float* w;        // nullable: one
+  const float* b;        // nullable: zero
+  void* out;
+  void* residual_out;  // nullable
+  float* mean;         // (rows, groups): nullable outputs of the forward, inputs of the backward
+  float* rstd;
+  const void* dout;
+  const void* dres_out;  // nullable: zero
+  void* dx;
+  void* dres;  // nullable
+  float* dw;   // nullable
+  float* db;   // nullable
+  void* workspace;
+  int64_t rows, group, groups;
+  int64_t sx, sr;  // elements between rows
+  float eps;
+  int x_bf16, h_bf16;  // x, out, dout and dx; the residual stream and its gradients
+};
+
+hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, hipStream_t stream);
+hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, const NormPlan& plan, hipStream_t stream);
+
 int env_int(const char* name, int dflt);
 
 }  // namespace sss

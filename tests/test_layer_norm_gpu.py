@@ -1,0 +1,161 @@
+"""The layer norm and its gradients on the GPU, against the definition in 64 bits of the same inputs.
+
+Error bounds, fixed beforehand, eps = 2^-24.  A sum over a row is formed from at most 32 elements per lane and 10
+levels of lanes and waves: 64 eps of the sum of absolute values with the roundings of its terms.  So the mean and each
+deviation are within d = 64 eps max|h|, hat within e = rstd d (1 + |hat|) + 64 eps |hat|, and out within |w| e and
+64 eps of its two terms.  Gradients: rstd times 64 eps of each of the three terms, and what e does to them.
+Parameter gradients: sums over rows in pieces of at most a few hundred, 600 eps of the absolute terms, and e in
+each.  bf16 results: half a step, 2^-8 of the value."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+EPS = 2.0 ** -24
+DEV = "cuda:0"
+# every shape of the kernels, in both types: lanes per row, pieces per lane, rows that no piece divides
+GROUPS = [1, 5, 8, 33, 64, 120, 250, 300, 500, 777, 1024, 2047, 2560, 4100, 6145, 9000, 16385, 32768]
+
+
+def reference(x, res, w, b, eps, groups, dout=None, dres=None):
+    """out, h, mean, rstd, and with dout the gradients; each with its bound, in 64 bits."""
+    import torch
+    x = x.cpu().double()
+    rows, dim = x.shape
+    h = x if res is None else x + res.cpu().double()
+    u = h.reshape(rows, groups, -1)
+    full = lambda t: t.expand(u.shape).reshape(h.shape)
+    mean = u.mean(-1, keepdim=True)
+    rstd = 1.0 / torch.sqrt((u - mean).square().mean(-1, keepdim=True) + eps)
+    hat = (u - mean) * rstd
+    d = 64 * EPS * u.abs().amax(-1, keepdim=True)
+    e = rstd * d * (1 + hat.abs()) + 64 * EPS * hat.abs()
+    one = torch.ones(dim).double()
+    wv, bv = one if w is None else w.cpu().double(), 0 * one if b is None else b.cpu().double()
+    hf, ef = hat.reshape(h.shape), e.reshape(h.shape)
+    r = {"out": (hf * wv + bv, ef * wv.abs() + 64 * EPS * ((hf * wv).abs() + bv.abs())), "h": (h, EPS * (h.abs() + x.abs())),
+         "mean": (mean[..., 0], d[..., 0]), "rstd": (rstd[..., 0], (rstd * (rstd * d + 64 * EPS))[..., 0])}
+    if dout is not None:
+        do = dout.cpu().double()
+        gr = (do * wv).reshape(u.shape)
+        s, q = gr.mean(-1, keepdim=True), (gr * hat).mean(-1, keepdim=True)
+        dh = rstd * (gr - s - hat * q)
+        ma, mq, me = (t.mean(-1, keepdim=True) for t in (gr.abs(), (gr * hat).abs(), gr.abs() * e))
+        slack = rstd * (64 * EPS * (gr.abs() + ma + hat.abs() * mq) + e * mq + hat.abs() * me
+                        + (rstd * d + 64 * EPS) * (gr.abs() + ma + hat.abs() * mq))
+        up = 0 * h if dres is None else dres.cpu().double()
+        grad = dh.reshape(h.shape) + up
+        bound = slack.reshape(h.shape) + 4 * EPS * (grad.abs() + up.abs())
+        r["dx"] = r["dresidual"] = (grad, bound)
+        r["dweight"] = ((do * hf).sum(0), 600 * EPS * (do * hf).abs().sum(0) + (do.abs() * ef).sum(0))
+        r["dbias"] = (do.sum(0), 600 * EPS * do.abs().sum(0))
+    return r
+
+
+def check(got, ref, name):
+    import torch
+    want, bound = ref[name]
+    if got.dtype == torch.bfloat16:
+        bound = bound + 2.0 ** -8 * want.abs()
+    err = (got.detach().cpu().double() - want).abs()
+    bad = ~(err <= bound)
+    assert not bool(bad.any()), (name, int(bad.sum()), float(err.max()), float((err - bound).max()))
+
+
+def rnd(seed, *shape, dtype=None, scale=1.0, shift=0.0):
+    import torch
+    t = torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale + shift
+    return t.to(dtype or torch.float32)
+
+
+@pytest.mark.parametrize("types", ["fp32", "bf16", "bf16 stream fp32", "bf16 stream bf16", "fp32 stream bf16"])
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("groups", [1, 3])
+def test_forward_and_gradients(group, groups, types):
+    import torch
+    import selective_state_space_20_amd as sss
+    kind = {"fp32": torch.float32, "bf16": torch.bfloat16}
+    parts = types.split()
+    dt, hd = kind[parts[0]], kind[parts[2]] if len(parts) > 1 else None
+    rows, dim = (70 if group < 600 else 6), group * groups
+    x = rnd(1, rows, dim, dtype=dt, shift=3.0)
+    res = rnd(2, rows, dim, dtype=hd, scale=2.0) if hd else None
+    w, b = rnd(3, dim, scale=0.3, shift=1.0), rnd(4, dim)
+    dout, dres = rnd(5, rows, dim, dtype=dt), rnd(6, rows, dim, dtype=hd) if hd else None
+    dev = lambda t: None if t is None else t.to(DEV)
+    got = sss.layer_norm_fwd(dev(x), dev(w), dev(b), dev(res), group_size=group, eps=1e-3, return_stats=True)
+    ref = reference(x, res, w, b, 1e-3, groups)
+    for n, t in zip(("out", "h", "mean", "rstd") if hd else ("out", "mean", "rstd"), got):
+        check(t, ref, n)
+    h, mean, rstd = (got[1] if hd else dev(x)), got[-2], got[-1]
+    # the gradients of the norm of what is kept (a bf16 stream: of the rounded sum, its own mean and deviation)
+    if hd is torch.bfloat16:
+        _, mean, rstd = sss.layer_norm_fwd(h.float(), dev(w), dev(b), group_size=group, eps=1e-3, return_stats=True)
+    ref = reference(h, None, w, b, 1e-3, groups, dout, dres)
+    g = sss.layer_norm_bwd(dev(dout), h, dev(w), mean=mean, rstd=rstd, bias=True, dresidual_out=dev(dres), group_size=group)
+    assert set(g) == {"dx", "dweight", "dbias"} | ({"dresidual"} if hd else set())
+    for n, t in g.items():
+        check(t, ref, n)
+    again = sss.layer_norm_bwd(dev(dout), h, dev(w), mean=mean, rstd=rstd, bias=True, dresidual_out=dev(dres), group_size=group)
+    assert all(torch.equal(g[n], again[n]) for n in g)
+
+
+def test_many_rows_and_no_parameters():
+    import torch
+    import selective_state_space_20_amd as sss
+    for rows, dim, dt in ((5003, 96, torch.bfloat16), (3001, 1300, torch.float32)):
+        x, w, dout = rnd(1, rows, dim, dtype=dt), rnd(2, dim), rnd(3, rows, dim, dtype=dt)
+        for use in (True, False):
+            wt = w if use else None
+            out, mean, rstd = sss.layer_norm_fwd(x.to(DEV), wt.to(DEV) if use else None, return_stats=True)
+            ref = reference(x, None, wt, None, 1e-5, 1, dout)
+            check(out, ref, "out")
+            g = sss.layer_norm_bwd(dout.to(DEV), x.to(DEV), wt.to(DEV) if use else None, mean=mean, rstd=rstd, bias=not use)
+            assert set(g) == ({"dx", "dweight"} if use else {"dx", "dbias"})
+            for n, t in g.items():
+                check(t, ref, n)
+        g = sss.layer_norm_bwd(dout.to(DEV), x.to(DEV), mean=mean, rstd=rstd)
+        assert set(g) == {"dx"}
+        check(g["dx"], ref, "dx")
+
+
+def test_strided_in_place_and_large_mean():
+    import torch
+    import selective_state_space_20_amd as sss
+    rows, dim = 37, 301
+    for dt in (torch.float32, torch.bfloat16):
+        wide = torch.full((rows, 2 * dim + 1), float("nan"), dtype=dt, device=DEV)
+        x, w, b = rnd(1, rows, dim, dtype=dt), rnd(2, dim), rnd(3, dim)
+        wide[:, 1:1 + dim] = x.to(DEV)
+        res = rnd(4, rows, dim, shift=1000.0)  # a mean far above the deviations
+        stream = res.to(DEV)
+        out, h = sss.layer_norm_fwd(wide[:, 1:1 + dim], w.to(DEV), b.to(DEV), stream, residual_out=stream)
+        assert h is stream
+        ref = reference(x, res, w, b, 1e-5, 1)
+        check(out, ref, "out")
+        check(h, ref, "h")
+        # the sum kept without a residual
+        kept = torch.empty(rows, dim, device=DEV)
+        out2, h2 = sss.layer_norm_fwd(wide[:, 1:1 + dim], w.to(DEV), b.to(DEV), residual_out=kept)
+        assert torch.equal(h2, x.to(DEV).float())
+        check(out2, reference(x, None, w, b, 1e-5, 1), "out")
+        # gradients of a strided x
+        do = rnd(5, rows, dim, dtype=dt)
+        _, mean, rstd = sss.layer_norm_fwd(wide[:, 1:1 + dim], w.to(DEV), return_stats=True)
+        g = sss.layer_norm_bwd(do.to(DEV), wide[:, 1:1 + dim], w.to(DEV), mean=mean, rstd=rstd)
+        ref = reference(x, None, w, None, 1e-5, 1, do)
+        check(g["dx"], ref, "dx")
+        check(g["dweight"], ref, "dweight")
+
+
+def test_rows_apart_and_none():
+    import torch
+    import selective_state_space_20_amd as sss
+    x = rnd(1, 5, 100).to(DEV)
+    x[2, 7], x[3, 9] = float("nan"), float("inf")
+    out = sss.layer_norm_fwd(x)
+    assert bool(out[[0, 1, 4]].isfinite().all()) and bool(out[2].isnan().all()) and bool(out[3].isnan().any())
+    constant = sss.layer_norm_fwd(torch.full((3, 64), 2.5, device=DEV), bias=torch.ones(64, device=DEV))
+    assert bool((constant == 1).all())  # no deviation: the bias alone
+    none = torch.empty(0, 64, device=DEV)
+    out, mean, rstd = sss.layer_norm_fwd(none, return_stats=True)
+    g = sss.layer_norm_bwd(none, none, torch.ones(64, device=DEV), mean=mean, rstd=rstd, bias=True)
+    assert out.shape == (0, 64) and bool((g["dweight"] == 0).all()) and bool((g["dbias"] == 0).all())
