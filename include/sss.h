@@ -432,7 +432,7 @@ int layer_norm_bwd(const void* dout, const void* dresidual_out, const void* x, i
  * (the state-space form: q = C, k = B, v = x, g = delta A, beta = delta).
  *
  * q (tokens, q_heads, dk), k (tokens, k_heads, dk), v (tokens, heads, dv) in io_dtype: dk or dv adjacent
- * elements, any strides >= 0 (elements) between tokens and between heads; q_heads and k_heads divide
+ * elements, any strides >= 0 (elements; up to 2^24 between tokens) between tokens and between heads; q_heads and k_heads divide
  * heads, adjacent heads share one.  log_decay (tokens, heads) float32 with decay_stride, or
  * (heads) with decay_stride 0: one decay for each head.  beta (tokens, heads) float32 with
  * beta_stride, nullable; D_skip (heads) float32, nullable.  A log decay of -1e4 or less, -inf

@@ -18,7 +18,8 @@ namespace {
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // token numbers are 32-bit on the device
 constexpr int64_t kMaxHeads = (int64_t)1 << 16;
 constexpr int64_t kMaxHeadDim = 256;
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 24;      // between tokens
+constexpr int64_t kMaxHeadStride = (int64_t)1 << 40;  // between heads
 constexpr double kMaxThreads = 4294967295.0;  // of a launch
 
 int64_t dtype_size(int t) { return t == SSS_BF16 ? 2 : 4; }
@@ -40,7 +41,7 @@ struct Side {
   const void* p;
   int64_t st, sh, heads, width;
   bool ok(int64_t rows) const {
-    return st >= 0 && sh >= 0 && st <= kMaxStride && sh <= kMaxStride &&
+    return st >= 0 && sh >= 0 && st <= kMaxStride && sh <= kMaxHeadStride &&
            (double)rows * (double)st + (double)heads * (double)sh < 1.0e18;
   }
   int64_t bytes(int64_t rows, int64_t es) const {

@@ -148,43 +148,93 @@ struct LaTile {
   }
 };
 
-// A tile on its way from memory to LDS, in registers of NT threads.
+// A tile on its way from memory to LDS, in registers of NT threads: pieces of 16 bytes, all loaded without a
+// branch, so that they are in flight together.  Where a piece would lie outside the tile, the nearest one inside is
+// loaded; what does not belong there is cleared when the tile is stored.
 template <bool BF16, int C, int W, int NT>
 struct LaLoad {
   using T = LaTile<BF16, W>;
   static constexpr int VE = T::VE, PER = W / VE, N = C * PER / NT;
   static_assert(N * NT == C * PER, "whole pieces");
   la_u4 v[N];
-  // rows base + r st, r < nr, of `width` elements; zeros elsewhere
-  __device__ __forceinline__ void load(const char* base, int64_t st, int nr, int width) {
+  static constexpr int RPT = NT / PER;  // rows at a time
+  // rows first + r, r < nr, of `width` elements (strides are at most 2^24 elements: offsets in a tile fit 32 bits)
+  __device__ __forceinline__ void load(int tid, const char* base, int64_t first, int64_t st, int nr, int width) {
+    if (width < VE) return;  // store() does all
+    const row_ptr p = row_at(base, first * st * T::ES);
+    const uint32_t rb = (uint32_t)st * T::ES, c = (uint32_t)min(tid % PER * VE, width - VE) * T::ES;
+    const uint32_t at = (uint32_t)(tid / PER) * rb + c, last = (uint32_t)(nr - 1) * rb + c;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = n * (NT / PER) + (int)threadIdx.x / PER, c = (int)threadIdx.x % PER * VE;
-      v[n] = la_u4{0, 0, 0, 0};
-      if (r < nr && c < width) {
-        const char* const p = base + (r * st + c) * T::ES;
-        if (c + VE <= width) {
-          const vec_u4 x = *(const vec_u4*)p;
-          v[n] = la_u4{x.x, x.y, x.z, x.w};
-        } else {
-#pragma unroll
-          for (int q = 0; q < VE; ++q) {
-            if (c + q >= width) continue;
-            if constexpr (BF16) v[n][q >> 1] |= (uint32_t)(*(const uint16_t*)(p + 2 * q)) << (16 * (q & 1));
-            else v[n][q] = *(const vec_u1*)(p + 4 * q);
-          }
-        }
-      }
+      const vec_u4 x = vec_get16<false>(p + min(at + (uint32_t)(n * RPT) * rb, last));
+      v[n] = la_u4{x.x, x.y, x.z, x.w};
     }
   }
-  __device__ __forceinline__ void store(char* t) const {
+  __device__ __forceinline__ void store(int tid, char* t, const char* base, int64_t first, int64_t st, int nr, int width) const {
+    const int r0 = tid / PER, c = tid % PER * VE;
+    char* const to = t + (r0 * T::LD + c) * T::ES;
+    constexpr int step = RPT * T::LD * T::ES;
+    if (nr == C && width == W) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) *(la_u4*)(to + n * step) = v[n];
+      return;
+    }
+    if (width < VE) {  // heads of a few elements: one by one
+      for (int n = 0; n < N; ++n) {
+        for (int i = 0; i < VE; ++i) {
+          const bool in = r0 + n * RPT < nr && c + i < width;
+          const char* const p = base + (first + min(r0 + n * RPT, nr - 1)) * st * T::ES + min(c + i, width - 1) * T::ES;
+          if constexpr (BF16) ((uint16_t*)(to + n * step))[i] = in ? *(const uint16_t*)p : (uint16_t)0;
+          else ((float*)(to + n * step))[i] = in ? *(const float*)p : 0.0f;
+        }
+      }
+      return;
+    }
+    const int bits = c < width ? 8 * T::ES * max(c - (width - VE), 0) : 0;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = n * (NT / PER) + (int)threadIdx.x / PER, c = (int)threadIdx.x % PER * VE;
-      *(la_u4*)(t + (r * T::LD + c) * T::ES) = v[n];
+      la_u4 x = v[n];
+      if (width % VE != 0) {  // the row's last piece was loaded from before its place
+        uint64_t lo = (uint64_t)x[1] << 32 | x[0], hi = (uint64_t)x[3] << 32 | x[2];
+        if (bits >= 64) lo = hi >> (bits & 63), hi = 0;
+        else if (bits > 0) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+        x = la_u4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+      }
+      const bool in = r0 + n * RPT < nr && c < width;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = in ? x[i] : 0u;
+      *(la_u4*)(to + n * step) = x;
     }
   }
 };
+
+// Sums of a wave's lanes up to each lane, in the lanes' order.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double la_dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+}
+__device__ __forceinline__ double la_prefix(double v) {
+  v += la_dpp<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8: within 16 lanes
+  v += la_dpp<0x112, 0xF>(v);
+  v += la_dpp<0x114, 0xF>(v);
+  v += la_dpp<0x118, 0xF>(v);
+  v += la_dpp<0x142, 0xA>(v);  // row_bcast 15: the sum of the 16 lanes before
+  v += la_dpp<0x143, 0xC>(v);  // row_bcast 31: of the 32 before
+  return v;
+}
+template <int CTRL>
+__device__ __forceinline__ float la_dpp32(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ double la_lane(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 
 // log decays below this leave nothing of a state in fp32; kept finite, so that differences of
 // their sums are numbers (a NaN stays one)
@@ -196,10 +246,10 @@ struct LaShape {
   static constexpr bool kOut = MODE >= kLaFwd;
   static constexpr bool kDots = MODE == kLaDq || MODE == kLaDk;
   static constexpr int XM = BF16 && kDots ? 3 : 1;                                 // parts of M as an operand
-  static constexpr int UP = !BF16 ? 1 : MODE == kLaFwd || MODE == kLaDv ? 2 : 3;  // of the weighted z
+  static constexpr int UP = !BF16 ? 1 : MODE == kLaDv ? 2 : 3;  // of the weighted z
   static constexpr int NW = F == 256 ? 8 : 4, NT = NW * 64, NF = F / (16 * NW);
   static constexpr int C = BF16 ? kLaTile : kLaTile / 2, TI = C / 16, KS = C / 32;
-  static constexpr int WPI = NW / TI, JT = TI / WPI > 0 ? TI / WPI : 1;  // waves per 16 rows of scores; their column tiles
+  static constexpr int NS = TI * (TI + 1) / 2, SPW = (NS + NW - 1) / NW;  // tiles of scores that are not zero; per wave
 };
 
 template <bool BF16, int E, int F, int MODE>
@@ -218,25 +268,30 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
   __shared__ __attribute__((aligned(16))) char lp[kOut ? C * TP::LD * ES : 16];
   __shared__ double lg[C];                 // sums of log2 decays
   __shared__ __attribute__((aligned(16))) float lsr[C], luw[C], lbeta[C];  // weights: x M, y z^T, beta
-  __shared__ float ltot;
-  __shared__ float lrr[kDots ? NW * C : 1], lri[MODE == kLaDq ? S::WPI * C : 1];
+  __shared__ float lrr[kDots ? NW * C : 1];
   __shared__ float lred[NW];
 
+  auto uni = [](int v) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(v); };
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave_id = uni((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, l4 = lane >> 4;
   const unsigned id = xcd_remap(blockIdx.x, gridDim.x);
-  const int h = (int)(id % (unsigned)g.H);
-  int seg = (int)(id / (unsigned)g.H);
+  const int h = uni((int)(id % (unsigned)g.H));
+  int seg = uni((int)(id / (unsigned)g.H));
   if constexpr (MODE == kLaFoldRev) ++seg;  // the first segment has no edge on its left
   const int c0 = seg * g.K, tend = min(c0 + g.K, g.tokens);
-  const int lo = min(max(g.cu[0], 0), g.tokens), hi = min(max(g.cu[g.nseq], 0), g.tokens);
-  const int f0 = wave * (16 * NF);  // the wave's columns
+  const int lo = uni(min(max(g.cu[0], 0), g.tokens));
+  const int hi = uni(min(max(g.cu[g.nseq], 0), g.tokens));
+  const int f0 = wave_id * (16 * NF);  // the wave's columns
   const int Ew = g.y.width, Fw = g.z.width;
-  const char* const xp = kOut ? g.x.p + (h / g.x.rep) * g.x.sh * ES : nullptr;
-  const char* const yp = g.y.p + (h / g.y.rep) * g.y.sh * ES;
-  const char* const zp = g.z.p + (h / g.z.rep) * g.z.sh * ES;
-  const char* const wp = kDots ? g.w.p + (h / g.w.rep) * g.w.sh * ES : nullptr;
+  const char* const xp = kOut ? g.x.p + uni(h / g.x.rep) * g.x.sh * ES : nullptr;
+  const char* const yp = g.y.p + uni(h / g.y.rep) * g.y.sh * ES;
+  const char* const zp = g.z.p + uni(h / g.z.rep) * g.z.sh * ES;
+  const char* const wp = kDots ? g.w.p + uni(h / g.w.rep) * g.w.sh * ES : nullptr;
+
+  const float* const gp = g.g + h;
+  const float* const bp = g.beta != nullptr ? g.beta + h : nullptr;
+  const float skip = (MODE == kLaFwd || MODE == kLaDv) && g.D != nullptr ? g.D[h] : 0.0f;
 
   la_f4 M[ET][NF];
   // Element r of a lane's accumulator t is row 32 (t / 2) + 8 (l / 16) + 4 (t % 2) + r of M.  fn(value, offset
@@ -267,9 +322,32 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
 #pragma unroll
       for (int nf = 0; nf < NF; ++nf) M[t][nf] = la_f4{0.0f, 0.0f, 0.0f, 0.0f};
   };
-  auto from = [&](const float* p) __attribute__((always_inline)) {
-    zero();
-    each([&](float& v, int o) __attribute__((always_inline)) { v = p[o]; });
+  // all loads in flight together: what lies outside the head's sizes is loaded from inside and cleared
+  auto peek = [&](const float* p, auto&& fn) __attribute__((always_inline)) {
+    int e0 = 8 * l4, f1 = f0 + l16;
+    asm volatile("" : "+v"(e0), "+v"(f1));
+    const int se = (int)g.se, sf = (int)g.sf;
+    la_f4 v[ET][NF];
+#pragma unroll
+    for (int t = 0; t < ET; ++t)
+#pragma unroll
+      for (int nf = 0; nf < NF; ++nf)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[t][nf][r] = p[min(e0 + 32 * (t >> 1) + 4 * (t & 1) + r, Ew - 1) * se + min(f1 + 16 * nf, Fw - 1) * sf];
+#pragma unroll
+    for (int t = 0; t < ET; ++t)
+#pragma unroll
+      for (int nf = 0; nf < NF; ++nf)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool in = e0 < Ew - (32 * (t >> 1) + 4 * (t & 1) + r) && f1 < Fw - 16 * nf;
+          M[t][nf][r] = fn(M[t][nf][r], in ? v[t][nf][r] : 0.0f);
+        }
+  };
+  auto from = [&](const float* p) __attribute__((always_inline)) {  // null: zero
+    if (p == nullptr) zero();
+    else peek(p, [](float, float v) __attribute__((always_inline)) { return v; });
   };
   auto to = [&](float* p) __attribute__((always_inline)) {
     each([&](float& v, int o) __attribute__((always_inline)) { p[o] = v; });
@@ -286,126 +364,128 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
     LaLoad<BF16, C, F, NT> rz, rw;
     float rg = 0.0f, rb = 0.0f;
     const int ntile = (e - a + C - 1) / C;
-    auto fetch = [&](int m) __attribute__((always_inline)) {
+    auto fetch = [&](int tid, int m) __attribute__((always_inline)) {
+      const int lane = tid & 63;
       const int t = a + m * C, nr = min(C, e - t);
-      if constexpr (kOut) rx.load(xp + (int64_t)t * g.x.st * ES, g.x.st, nr, Ew);
-      ry.load(yp + (int64_t)t * g.y.st * ES, g.y.st, nr, Ew);
-      rz.load(zp + (int64_t)t * g.z.st * ES, g.z.st, nr, Fw);
-      if constexpr (kDots) rw.load(wp + (int64_t)t * g.w.st * ES, g.w.st, nr, Fw);
-      if (wave == 0) {
-        rg = lane < nr ? g.g[(t + lane) * g.g_st + h] : 0.0f;
-        rb = lane >= nr ? 0.0f : g.beta != nullptr ? g.beta[(t + lane) * g.beta_st + h] : 1.0f;
-      }
+      // first, so that waiting for them does not wait for the tiles: vector loads return in order
+      const int r = t + min(lane, nr - 1);
+      rg = gp[r * g.g_st];
+      rb = bp != nullptr ? bp[r * g.beta_st] : 1.0f;
+      if constexpr (kOut) rx.load(tid, xp, t, g.x.st, nr, Ew);
+      ry.load(tid, yp, t, g.y.st, nr, Ew);
+      rz.load(tid, zp, t, g.z.st, nr, Fw);
+      if constexpr (kDots) rw.load(tid, wp, t, g.w.st, nr, Fw);
     };
-    fetch(kRev ? ntile - 1 : 0);
+    fetch((int)threadIdx.x, kRev ? ntile - 1 : 0);
     for (int k = 0; k < ntile; ++k) {
       const int m = kRev ? ntile - 1 - k : k;
       const int t0 = a + m * C, nr = min(C, e - t0);
+      // addresses in a tile start from values that the compiler does not know, or it keeps them all in registers
+      // over the loop, and these are short
+      int tid = (int)threadIdx.x, wave = wave_id;
+      asm volatile("" : "+v"(tid), "+s"(wave));
+      const int lane = tid & 63, l16 = tid & 15, l4 = lane >> 4, f0 = wave * (16 * NF);
       la_barrier();  // the tile before has been read
-      if constexpr (kOut) rx.store(lx);
-      ry.store(ly);
-      rz.store(lz);
-      if constexpr (kDots) rw.store(lw);
-      if (wave == 0) {
-        double x = la_log2_decay(rg);
-#pragma unroll
-        for (int d = 1; d < C; d *= 2) {
-          const double up = __shfl_up(x, d);
-          if (lane >= d) x += up;
-        }
-        const double tot = __shfl(x, C - 1);
-        if (lane < C) {
-          const float in = fast_exp2((float)x), out = fast_exp2((float)(tot - x));
-          lg[lane] = x;
-          lsr[lane] = kRev ? out : g.scale * in;
-          luw[lane] = kRev ? g.scale * in : rb * out;
-          lbeta[lane] = rb;
-        }
-        if (lane == 0) ltot = fast_exp2((float)tot);
-        total += tot;
+      const bool alive = lane < nr;
+      const double x = la_prefix(la_log2_decay(alive ? rg : 0.0f)), tot = la_lane(x, 63);
+      const float b = alive ? rb : 0.0f, keep = fast_exp2((float)tot);
+      if constexpr (!kOut) total += tot;
+      if (wave == 0 && lane < C) {
+        const float in = fast_exp2((float)x), out = fast_exp2((float)(tot - x));
+        lg[lane] = x;
+        lsr[lane] = kRev ? out : g.scale * in;
+        luw[lane] = kRev ? g.scale * in : b * out;
+        lbeta[lane] = b;
       }
+      if constexpr (kOut) rx.store(tid, lx, xp, t0, g.x.st, nr, Ew);
+      ry.store(tid, ly, yp, t0, g.y.st, nr, Ew);
+      rz.store(tid, lz, zp, t0, g.z.st, nr, Fw);
+      if constexpr (kDots) rw.store(tid, lw, wp, t0, g.w.st, nr, Fw);
       la_barrier();
-      if (k + 1 < ntile) fetch(kRev ? m - 1 : m + 1);
+      if (k + 1 < ntile) fetch(tid, kRev ? m - 1 : m + 1);
       if constexpr (MODE == kLaDq) {
         if (k + 1 == ntile) {
           through = 0.0f;
           if (adj != nullptr) {
-            each([&](float& v, int o) __attribute__((always_inline)) { through = __builtin_fmaf(v, adj[o], through); });
-            through *= ltot;
+            peek(adj, [&](float m, float v) __attribute__((always_inline)) {
+              through = __builtin_fmaf(m, v, through);
+              return m;
+            });
+            through *= keep;
           }
         }
       }
 
-      // z by columns, as it is and weighted
-      LaFrag<BF16> zf[KS][NF];
+      LaFrag<BF16> zf[KS][NF];  // z by columns
+      auto take_z = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int nf = 0; nf < NF; ++nf) zf[ks][nf] = TZ::template cols<4>(lz, 32 * ks, f0 + 16 * nf, lane);
-
+          for (int nf = 0; nf < NF; ++nf) zf[ks][nf] = TZ::template cols<4>(lz, 32 * ks, f0 + 16 * nf, lane);
+      };
       if constexpr (kOut) {
-        // scores of 16 rows and the column tiles of this wave, transposed: the lane has row i, columns j + r
-        const int it = wave / S::WPI, jt0 = (wave % S::WPI) * S::JT;
-        const int i = 16 * it + l16;
-        float ri = 0.0f;
-        if (jt0 < TI) {
-          LaFrag<BF16> xf[EK];
+        // Scores, transposed: the lane has row i, columns j + r.  The waves share the 16 x 16 tiles on and below
+        // (backwards: above) the diagonal.
 #pragma unroll
-          for (int s = 0; s < EK; ++s) xf[s] = TX::rows(lx, 16 * it, 32 * s, lane);
+        for (int q = 0; q < S::SPW; ++q) {
+          const int n = wave + q * NW;
+          if (n >= S::NS) break;
+          const int big = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, small = n - big * (big + 1) / 2;
+          const int it = kRev ? TI - 1 - big : big, jt = kRev ? TI - 1 - small : small;
+          const int i = 16 * it + l16, j = 16 * jt + 4 * l4;
+          la_f4 sc = {0.0f, 0.0f, 0.0f, 0.0f}, other = sc;
+#pragma unroll
+          for (int s = 0; s < EK; ++s) sc = la_mma(TX::rows(ly, 16 * jt, 32 * s, lane), TX::rows(lx, 16 * it, 32 * s, lane), sc);
+          if constexpr (MODE == kLaDq) {  // q k^T
+#pragma unroll
+            for (int s = 0; s < F / 32; ++s)
+              other = la_mma(TZ::rows(lz, 16 * jt, 32 * s, lane), TZ::rows(lw, 16 * it, 32 * s, lane), other);
+          }
           const double gi = lg[i];
-          const float row_w = (kRev ? lbeta[i] : 1.0f) * g.scale;
+          const float row_w = kRev ? lbeta[i] * g.scale : g.scale;
+          const la_f4 bj = *(const la_f4*)(lbeta + j);
+          float p[4], ci[4], ri = 0.0f;
 #pragma unroll
-          for (int q = 0; q < S::JT; ++q) {
-            const int jt = jt0 + q, j = 16 * jt + 4 * l4;
-            la_f4 sc = {0.0f, 0.0f, 0.0f, 0.0f}, other = sc;
-            float p[4] = {0.0f, 0.0f, 0.0f, 0.0f}, ci[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (kRev ? jt >= it : jt <= it) {
-#pragma unroll
-              for (int s = 0; s < EK; ++s) sc = la_mma(TX::rows(ly, 16 * jt, 32 * s, lane), xf[s], sc);
-              if constexpr (MODE == kLaDq) {  // q k^T
-#pragma unroll
-                for (int s = 0; s < F / 32; ++s)
-                  other = la_mma(TZ::rows(lz, 16 * jt, 32 * s, lane), TZ::rows(lw, 16 * it, 32 * s, lane), other);
-              }
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const double d = kRev ? lg[j + r] - gi : gi - lg[j + r];
-                const bool in = kRev ? j + r >= i : j + r <= i;
-                const float wt = in ? row_w * fast_exp2((float)d) : 0.0f;
-                const float b = kRev ? 1.0f : lbeta[j + r];
-                p[r] = in ? wt * b * sc[r] : 0.0f;
-                if constexpr (MODE == kLaDq) {
-                  ci[r] = in ? wt * sc[r] * other[r] : 0.0f;
-                  ri += b * ci[r];
-                  if (j + r == i) trace += sc[r];
-                }
-                if constexpr (MODE == kLaFwd || MODE == kLaDv) {
-                  if (g.D != nullptr && j + r == i) p[r] += g.D[h];
-                }
-              }
+          for (int r = 0; r < 4; ++r) {
+            const double d = kRev ? lg[j + r] - gi : gi - lg[j + r];
+            const bool in = kRev ? j + r >= i : j + r <= i;
+            const float wt = row_w * fast_exp2((float)d), b = kRev ? 1.0f : bj[r];
+            p[r] = in ? wt * b * sc[r] : 0.0f;
+            if constexpr (MODE == kLaDq) {
+              ci[r] = in ? wt * sc[r] * other[r] : 0.0f;
+              ri += b * ci[r];
+              trace += j + r == i ? sc[r] : 0.0f;
             }
-            char* const to_p = lp + (i * TP::LD + j) * ES;
+            if constexpr (MODE == kLaFwd || MODE == kLaDv) p[r] += j + r == i ? skip : 0.0f;
+          }
+          auto put = [&](int tile, const float (&v)[4]) __attribute__((always_inline)) {
+            char* const to_p = lp + (i * TP::LD + 16 * tile + 4 * l4) * ES;
             if constexpr (BF16) {
               typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-              *(u2*)to_p = u2{vec_bf16_pair(p[0], p[1]), vec_bf16_pair(p[2], p[3])};
+              *(u2*)to_p = u2{vec_bf16_pair(v[0], v[1]), vec_bf16_pair(v[2], v[3])};
             } else {
-              *(la_f4*)to_p = la_f4{p[0], p[1], p[2], p[3]};
+              *(la_f4*)to_p = la_f4{v[0], v[1], v[2], v[3]};
             }
-            if constexpr (MODE == kLaDq) {  // sums over the tile's rows
+          };
+          put(jt, p);
+          if (it == jt && (kRev ? it & 1 : !(it & 1))) {  // the other half of the product's 32 columns
+            const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            put(it ^ 1, none);
+          }
+          if constexpr (MODE == kLaDq) {  // sums over the tile's columns and rows, kept between the rows of x and of the scores
+            ri += __shfl_xor(ri, 16);
+            ri += __shfl_xor(ri, 32);
+            if (l4 == 0) *(float*)(lx + (i * TX::LD + E) * ES + 4 * jt) = ri;
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                float v = ci[r];
-#pragma unroll
-                for (int d = 1; d < 16; d *= 2) v += __shfl_xor(v, d);
-                if (l16 == 0) *(float*)(lp + ((j + r) * TP::LD + C) * ES + 4 * it) = v;  // between the rows of the scores
-              }
+            for (int r = 0; r < 4; ++r) {
+              float v = ci[r];
+              v += la_dpp32<0xB1>(v);   // quad_perm [1,0,3,2]
+              v += la_dpp32<0x4E>(v);   // quad_perm [2,3,0,1]
+              v += la_dpp32<0x141>(v);  // row_half_mirror
+              v += la_dpp32<0x140>(v);  // row_mirror
+              if (l16 == 0) *(float*)(lp + ((j + r) * TP::LD + C) * ES + 4 * it) = v;
             }
           }
-        }
-        if constexpr (MODE == kLaDq) {
-          ri += __shfl_xor(ri, 16);
-          ri += __shfl_xor(ri, 32);
-          if (l4 == 0 && jt0 < TI) lri[(wave % S::WPI) * C + i] = ri;
         }
         // x M, transposed: the lane has row i of the tokens, columns f + r
         la_f4 o[TI][NF];
@@ -457,6 +537,7 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
             if (l4 == 0) lrr[wave * C + 16 * t + l16] = dot;
           }
         }
+        take_z();
         la_barrier();  // the scores are there
         if constexpr (kDots) {
           if (wave == 0) {  // C tokens, a lane each
@@ -470,10 +551,10 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
             if constexpr (MODE == kLaDq) {
               float rs = 0.0f, cs = 0.0f;
 #pragma unroll
-              for (int q = 0; q < S::WPI; ++q)
-                if (q * S::JT < TI) rs += lri[q * C + i2];
-#pragma unroll
-              for (int q = 0; q < TI; ++q) cs += *(const float*)(lp + (i2 * TP::LD + C) * ES + 4 * q);
+              for (int q = 0; q < TI; ++q) {
+                rs += q <= i2 / 16 ? *(const float*)(lx + (i2 * TX::LD + E) * ES + 4 * q) : 0.0f;
+                cs += q >= i2 / 16 ? *(const float*)(lp + (i2 * TP::LD + C) * ES + 4 * q) : 0.0f;
+              }
               float n = lane < C ? rs - lbeta[i2] * cs : 0.0f;
 #pragma unroll
               for (int d = 1; d < C; d *= 2) {
@@ -487,6 +568,9 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
             }
           }
         }
+        const bool wide = !BF16 || (kDots && g.out_f32);
+        const uint32_t out_es = wide ? 4 : 2, out_row = (uint32_t)g.out_st * out_es;
+        const row_ptr to_out = row_at(g.out, ((int64_t)t0 * g.out_st + h * g.out_sh) * out_es);
 #pragma unroll
         for (int t = 0; t < TI; ++t) {
 #pragma unroll
@@ -497,38 +581,29 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
             for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_mma(zf[ks][nf], pf, o[t][nf]);
           }
           const int i2 = 16 * t + l16;
-          if (i2 < nr) {
+          if (i2 >= nr) continue;
 #pragma unroll
-            for (int nf = 0; nf < NF; ++nf) {
-              const int f = f0 + 16 * nf + 4 * l4;
-              const int64_t at = (int64_t)(t0 + i2) * g.out_st + h * g.out_sh + f;
-              const float v[4] = {o[t][nf][0], o[t][nf][1], o[t][nf][2], o[t][nf][3]};
-              if (BF16 && !g.out_f32) {
-                Vec<true, 4> r;
-                r.set(v);
-                if (f + 4 <= Fw) r.store(g.out + at * 2);
-                else if (f < Fw) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    if (f + q < Fw) ((uint16_t*)g.out)[at + q] = (uint16_t)(r.w[q >> 1] >> (16 * (q & 1)));
-                }
-              } else {
-                Vec<false, 4> r;
-                r.set(v);
-                if (f + 4 <= Fw) r.store(g.out + at * 4);
-                else if (f < Fw) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    if (f + q < Fw) ((float*)g.out)[at + q] = v[q];
-                }
-              }
+          for (int nf = 0; nf < NF; ++nf) {
+            const int f = f0 + 16 * nf + 4 * l4;
+            const uint32_t at = (uint32_t)i2 * out_row + (uint32_t)f * out_es;
+            const float v[4] = {o[t][nf][0], o[t][nf][1], o[t][nf][2], o[t][nf][3]};
+            if (BF16 && !wide) {
+              Vec<true, 4> r;
+              r.set(v);
+              if (Fw == F || f + 4 <= Fw) r.store(to_out, at);
+              else r.store_first(to_out, at, Fw - f);
+            } else {
+              Vec<false, 4> r;
+              r.set(v);
+              if (Fw == F || f + 4 <= Fw) r.store(to_out, at);
+              else r.store_first(to_out, at, Fw - f);
             }
           }
         }
       }
 
+      if constexpr (!kOut) take_z();
       // M <- e^(G_C) M + sum_j weight_j y_j z_j^T
-      const float keep = ltot;
 #pragma unroll
       for (int t = 0; t < ET; ++t)
 #pragma unroll
@@ -562,7 +637,7 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
     la_barrier();
-    if (lane == 0) lred[wave] = v;
+    if (lane == 0) lred[wave_id] = v;
     la_barrier();
     float s = 0.0f;
 #pragma unroll
@@ -581,25 +656,18 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
     int flag = 0;  // 0: none; 1: it runs across the other edge too; 2: it begins (ends) in the segment
     const int edge = kRev ? c0 : tend;
     if (edge > lo && edge < hi) {
-      const int s = min(max(__builtin_amdgcn_readfirstlane(find_seq(g.cu, g.nseq, kRev ? c0 : tend - 1, lane)), 0), g.nseq - 1);
-      const int end = min(g.cu[s + 1], hi);
-      const int beg = max(g.cu[s], 0);
+      const int s = min(max(uni(find_seq(g.cu, g.nseq, kRev ? c0 : tend - 1, lane)), 0), g.nseq - 1);
+      const int end = uni(min(g.cu[s + 1], hi)), beg = uni(max(g.cu[s], 0));
       if (kRev ? beg < c0 && end > c0 : beg < tend && end > tend) {
-        zero();
-        if constexpr (kRev) {
-          flag = end <= tend ? 2 : 1;
-          if (flag == 2 && g.from != nullptr) from(g.from + of_seq(s));
-        } else {
-          flag = beg >= c0 ? 2 : 1;
-          if (flag == 2) {
-            const int slot = slot_of(s);
-            if (g.from != nullptr) from(g.from + of_seq(s));
-            else if (slot >= 0 && g.init != nullptr && g.init[s] != 0) {
-              from(g.state + of_seq(slot));
-              to(g.begin + at_seg);  // for the second pass: the slot itself is overwritten there, by another workgroup
-            }
-          }
+        flag = (kRev ? end <= tend : beg >= c0) ? 2 : 1;
+        const float* src = nullptr;
+        if (flag == 2) {
+          if (g.from != nullptr) src = g.from + of_seq(s);
+          else if (g.init != nullptr && slot_of(s) >= 0 && g.init[s] != 0) src = g.state + of_seq(slot_of(s));
         }
+        from(src);
+        // for the second pass: the slot itself is overwritten there, by another workgroup
+        if (src != nullptr && g.begin != nullptr) to(g.begin + at_seg);
         walk(kRev ? c0 : max(beg, c0), kRev ? min(end, tend) : tend, nullptr);
         to(g.end + at_seg);
         if (threadIdx.x == 0) g.sum[(int64_t)seg * g.H + h] = (float)total;
@@ -622,9 +690,9 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
       clear(c0, gap0);
       clear(max(gap1, gap0), tend);
     }
-    int s = t < stop ? min(max(__builtin_amdgcn_readfirstlane(find_seq(g.cu, g.nseq, t, lane)), 0), g.nseq - 1) : 0;
+    int s = t < stop ? min(max(uni(find_seq(g.cu, g.nseq, t, lane)), 0), g.nseq - 1) : 0;
     while (t < stop) {
-      const int end = min(g.cu[s + 1], hi);
+      const int end = uni(min(g.cu[s + 1], hi));
       if (end <= t) {  // past this sequence (or an empty one)
         if (++s >= g.nseq) break;
         continue;
@@ -633,23 +701,18 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
       const bool before = began_before(g.cu[s], c0), after = end > tend;
       if constexpr (MODE == kLaFwd) {
         const int slot = slot_of(s);
-        if (before) from(g.enter + at_seg);
-        else if (slot >= 0 && g.init != nullptr && g.init[s] != 0) from(after ? g.begin + at_seg : g.state + of_seq(slot));
-        else zero();
+        const bool old = slot >= 0 && g.init != nullptr && g.init[s] != 0;
+        from(before ? g.enter + at_seg : !old ? nullptr : after ? g.begin + at_seg : g.state + of_seq(slot));
         walk(t, e, nullptr);
         if (!after && slot >= 0) to(g.state + of_seq(slot));
       } else if constexpr (MODE == kLaDq) {
-        if (before) from(g.enter + at_seg);
-        else if (g.from != nullptr) from(g.from + of_seq(s));
-        else zero();
+        from(before ? g.enter + at_seg : g.from != nullptr ? g.from + of_seq(s) : nullptr);
         const float* const adj = after ? g.back + at_seg : g.dfinal != nullptr ? g.dfinal + of_seq(s) : nullptr;
         walk(t, e, adj);
         const float v = adj != nullptr ? block_sum(through) : 0.0f;
         if (threadIdx.x == 0) (after ? g.edge[(int64_t)seg * g.H + h] : g.last[(int64_t)s * g.H + h]) = v;
       } else {
-        if (after) from(g.enter + at_seg);
-        else if (g.from != nullptr) from(g.from + of_seq(s));
-        else zero();
+        from(after ? g.enter + at_seg : g.from != nullptr ? g.from + of_seq(s) : nullptr);
         walk(t, e, nullptr);
         if (MODE == kLaDk && !before && g.to != nullptr) to(g.to + of_seq(s));
       }

@@ -168,6 +168,15 @@ struct Vec {
       part_as(p + off, skip);
     }
   }
+  // elements 0..n-1 only
+  __device__ __forceinline__ void store_first(row_ptr p, uint32_t off, int n) const {
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      if (c >= n) continue;
+      if constexpr (BF16) vec_put2<false>(p + off + 2 * c, (uint16_t)((c & 1) ? w[c >> 1] >> 16 : w[c >> 1]));
+      else vec_put4<false>(p + off + 4 * c, w[c]);
+    }
+  }
   template <typename P>
   __device__ __forceinline__ void part_as(P p, int skip) const {
 #pragma unroll
