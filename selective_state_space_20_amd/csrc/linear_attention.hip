@@ -253,7 +253,7 @@ struct LaShape {
 };
 
 template <bool BF16, int E, int F, int MODE>
-__global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) void la_walk_kernel(LaWalk g) {
+__global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F == 64 && MODE <= kLaFwd ? 3 : 2) void la_walk_kernel(LaWalk g) {
   using S = LaShape<BF16, E, F, MODE>;
   constexpr int NW = S::NW, NT = S::NT, NF = S::NF, C = S::C, TI = S::TI, KS = S::KS, ET = E / 16, EK = E / 32;
   constexpr bool kRev = S::kRev, kOut = S::kOut, kDots = S::kDots;
@@ -266,10 +266,13 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
   __shared__ __attribute__((aligned(16))) char lz[C * TZ::LD * ES];
   __shared__ __attribute__((aligned(16))) char lw[kDots ? C * TZ::LD * ES : 16];
   __shared__ __attribute__((aligned(16))) char lp[kOut ? C * TP::LD * ES : 16];
-  __shared__ double lg[C];                 // sums of log2 decays
-  __shared__ __attribute__((aligned(16))) float lsr[C], luw[C], lbeta[C];  // weights: x M, y z^T, beta
+  __shared__ __attribute__((aligned(16))) float luw[C], lbeta[C];  // weights of y z^T, beta
+  // between the rows of z: the sums of log2 decays; of y: the weights of x M, and the waves' parts of a sum (128 x 64:
+  // 53760 bytes in all, of which three workgroups fit a CU, with its pieces of 1280)
+  auto lg = [&](int i) __attribute__((always_inline)) { return (double*)(lz + (i * TZ::LD + F) * ES); };
+  auto lsr = [&](int i) __attribute__((always_inline)) { return (float*)(ly + (i * TX::LD + E) * ES); };
+  auto lred = [&](int i) __attribute__((always_inline)) { return (float*)(ly + (i * TX::LD + E) * ES + 4); };
   __shared__ float lrr[kDots ? NW * C : 1];
-  __shared__ float lred[NW];
 
   auto uni = [](int v) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(v); };
   const int lane = threadIdx.x & 63;
@@ -328,13 +331,23 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
     asm volatile("" : "+v"(e0), "+v"(f1));
     const int se = (int)g.se, sf = (int)g.sf;
     la_f4 v[ET][NF];
+    if (kDots && Ew % 4 == 0) {  // se is 1: four rows are 16 adjacent bytes
 #pragma unroll
-    for (int t = 0; t < ET; ++t)
+      for (int t = 0; t < ET; ++t)
 #pragma unroll
-      for (int nf = 0; nf < NF; ++nf)
+        for (int nf = 0; nf < NF; ++nf) {
+          const vec_u4 x = *(const vec_u4*)(p + (min(e0 + 32 * (t >> 1) + 4 * (t & 1), Ew - 4) + min(f1 + 16 * nf, Fw - 1) * sf));
+          v[t][nf] = __builtin_bit_cast(la_f4, x);
+        }
+    } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[t][nf][r] = p[min(e0 + 32 * (t >> 1) + 4 * (t & 1) + r, Ew - 1) * se + min(f1 + 16 * nf, Fw - 1) * sf];
+      for (int t = 0; t < ET; ++t)
+#pragma unroll
+        for (int nf = 0; nf < NF; ++nf)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[t][nf][r] = p[min(e0 + 32 * (t >> 1) + 4 * (t & 1) + r, Ew - 1) * se + min(f1 + 16 * nf, Fw - 1) * sf];
+    }
 #pragma unroll
     for (int t = 0; t < ET; ++t)
 #pragma unroll
@@ -392,8 +405,8 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
       if constexpr (!kOut) total += tot;
       if (wave == 0 && lane < C) {
         const float in = fast_exp2((float)x), out = fast_exp2((float)(tot - x));
-        lg[lane] = x;
-        lsr[lane] = kRev ? out : g.scale * in;
+        *lg(lane) = x;
+        *lsr(lane) = kRev ? out : g.scale * in;
         luw[lane] = kRev ? g.scale * in : b * out;
         lbeta[lane] = b;
       }
@@ -441,13 +454,13 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
             for (int s = 0; s < F / 32; ++s)
               other = la_mma(TZ::rows(lz, 16 * jt, 32 * s, lane), TZ::rows(lw, 16 * it, 32 * s, lane), other);
           }
-          const double gi = lg[i];
+          const double gi = *lg(i);
           const float row_w = kRev ? lbeta[i] * g.scale : g.scale;
           const la_f4 bj = *(const la_f4*)(lbeta + j);
           float p[4], ci[4], ri = 0.0f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const double d = kRev ? lg[j + r] - gi : gi - lg[j + r];
+            const double d = kRev ? *lg(j + r) - gi : gi - *lg(j + r);
             const bool in = kRev ? j + r >= i : j + r <= i;
             const float wt = row_w * fast_exp2((float)d), b = kRev ? 1.0f : bj[r];
             p[r] = in ? wt * b * sc[r] : 0.0f;
@@ -514,7 +527,7 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
         }
 #pragma unroll
         for (int t = 0; t < TI; ++t) {
-          const float sr = lsr[16 * t + l16], rb_ = kRev ? lbeta[16 * t + l16] : 1.0f;
+          const float sr = *lsr(16 * t + l16), rb_ = kRev ? lbeta[16 * t + l16] : 1.0f;
           float dot = 0.0f;
 #pragma unroll
           for (int nf = 0; nf < NF; ++nf) {
@@ -637,11 +650,11 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
     la_barrier();
-    if (lane == 0) lred[wave_id] = v;
+    if (lane == 0) *lred(wave_id) = v;
     la_barrier();
     float s = 0.0f;
 #pragma unroll
-    for (int q = 0; q < NW; ++q) s += lred[q];
+    for (int q = 0; q < NW; ++q) s += *lred(q);
     return s;
   };
 
