@@ -440,8 +440,8 @@ int layer_norm_bwd(const void* dout, const void* dresidual_out, const void* x, i
  * (SSS_ERR_UNSUPPORTED otherwise), heads up to 65536.  Packed prompts, cache slots, alignment and
  * overlap as above.  Results are deterministic.
  *
- * A value that is no number, or an infinity, in a token's k or v reaches the outputs of that token
- * and of later ones of its sequence; in its v also those of up to 63 tokens before it. */
+ * A value that is not finite reaches the results that it is a part of, as an infinity or as no number,
+ * and no others: nothing of tokens before it, of other sequences or heads. */
 
 /* Bytes of workspace linear_attention_packed_fwd needs on `device` (0 on invalid sizes, and where
  * none is needed); it does not depend on the sequences. */

@@ -100,6 +100,12 @@ __device__ __forceinline__ void la_widen(const LaFrag<false>& p, float (&v)[8]) 
   for (int i = 0; i < 8; ++i) v[i] = p.f[i];
 }
 
+template <bool BF16>
+__device__ __forceinline__ float la_get(const char* p) {
+  if constexpr (BF16) return __builtin_bit_cast(float, (uint32_t)(*(const uint16_t*)p) << 16);
+  else return *(const float*)p;
+}
+
 // LDS of one workgroup exchanged between its waves (global memory is not, within a launch)
 __device__ __forceinline__ void la_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -169,6 +175,18 @@ struct LaLoad {
       const vec_u4 x = vec_get16<false>(p + min(at + (uint32_t)(n * RPT) * rb, last));
       v[n] = la_u4{x.x, x.y, x.z, x.w};
     }
+  }
+  // whether a value among those loaded is an infinity or no number (also one that the tile does not take)
+  __device__ __forceinline__ bool wild() const {
+    uint32_t any = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) any |= ((v[n][i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;  // an exponent of ones
+        else any |= ((v[n][i] & 0x7F800000u) + 0x00800000u) & 0x80000000u;
+      }
+    return any != 0;
   }
   __device__ __forceinline__ void store(int tid, char* t, const char* base, int64_t first, int64_t st, int nr, int width) const {
     const int r0 = tid / PER, c = tid % PER * VE;
@@ -253,7 +271,7 @@ struct LaShape {
 };
 
 template <bool BF16, int E, int F, int MODE>
-__global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F == 64 && MODE <= kLaFwd ? 3 : 2) void la_walk_kernel(LaWalk g) {
+__global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) void la_walk_kernel(LaWalk g) {
   using S = LaShape<BF16, E, F, MODE>;
   constexpr int NW = S::NW, NT = S::NT, NF = S::NF, C = S::C, TI = S::TI, KS = S::KS, ET = E / 16, EK = E / 32;
   constexpr bool kRev = S::kRev, kOut = S::kOut, kDots = S::kDots;
@@ -267,8 +285,9 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F =
   __shared__ __attribute__((aligned(16))) char lw[kDots ? C * TZ::LD * ES : 16];
   __shared__ __attribute__((aligned(16))) char lp[kOut ? C * TP::LD * ES : 16];
   __shared__ __attribute__((aligned(16))) float luw[C], lbeta[C];  // weights of y z^T, beta
-  // between the rows of z: the sums of log2 decays; of y: the weights of x M, and the waves' parts of a sum (128 x 64:
-  // 53760 bytes in all, of which three workgroups fit a CU, with its pieces of 1280)
+  __shared__ int lwild[2];  // a tile's z has a value that is not finite (alternating tiles)
+  // between the rows of z: the sums of log2 decays; of y: the weights of x M, and the waves' parts of a
+  // sum
   auto lg = [&](int i) __attribute__((always_inline)) { return (double*)(lz + (i * TZ::LD + F) * ES); };
   auto lsr = [&](int i) __attribute__((always_inline)) { return (float*)(ly + (i * TX::LD + E) * ES); };
   auto lred = [&](int i) __attribute__((always_inline)) { return (float*)(ly + (i * TX::LD + E) * ES + 4); };
@@ -368,6 +387,9 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F =
   const int64_t per = g.hs, at_seg = ((int64_t)seg * g.H + h) * per;
   auto of_seq = [&](int64_t s) __attribute__((always_inline)) { return (s * g.H + h) * per; };
 
+  if (threadIdx.x == 0) lwild[0] = lwild[1] = 0;
+  int turn = 0;
+
   double total = 0.0;  // log2 of the decay over a folded part
   float trace = 0.0f, through = 0.0f;
 
@@ -413,6 +435,10 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F =
       if constexpr (kOut) rx.store(tid, lx, xp, t0, g.x.st, nr, Ew);
       ry.store(tid, ly, yp, t0, g.y.st, nr, Ew);
       rz.store(tid, lz, zp, t0, g.z.st, nr, Fw);
+      if constexpr (kOut) {
+        turn ^= 1;
+        if (Fw < TZ::VE || rz.wild()) lwild[turn] = 1;
+      }
       if constexpr (kDots) rw.store(tid, lw, wp, t0, g.w.st, nr, Fw);
       la_barrier();
       if (k + 1 < ntile) fetch(tid, kRev ? m - 1 : m + 1);
@@ -536,10 +562,7 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F =
               const char* const pw = lw + ((16 * t + l16) * TZ::LD + f0 + 16 * nf + 4 * l4) * ES;
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                float v;
-                if constexpr (BF16) v = __builtin_bit_cast(float, (uint32_t)(*(const uint16_t*)(pw + 2 * r)) << 16);
-                else v = *(const float*)(pw + 4 * r);
-                dot = __builtin_fmaf(v, o[t][nf][r], dot);
+                dot = __builtin_fmaf(la_get<BF16>(pw + ES * r), o[t][nf][r], dot);
               }
             }
             if constexpr (kRev) o[t][nf] *= rb_;
@@ -551,7 +574,9 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F =
           }
         }
         take_z();
+        if (threadIdx.x == 0) lwild[turn ^ 1] = 0;  // last read before this tile
         la_barrier();  // the scores are there
+        const bool wild = uni(lwild[turn]) != 0;
         if constexpr (kDots) {
           if (wave == 0) {  // C tokens, a lane each
             const int i2 = lane & (C - 1);
@@ -586,14 +611,29 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : F =
         const row_ptr to_out = row_at(g.out, ((int64_t)t0 * g.out_st + h * g.out_sh) * out_es);
 #pragma unroll
         for (int t = 0; t < TI; ++t) {
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            if (kRev ? 2 * ks + 1 < t : 2 * ks > t) continue;
-            const LaFrag<BF16> pf = TP::rows(lp, 16 * t, 32 * ks, lane);
-#pragma unroll
-            for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_mma(zf[ks][nf], pf, o[t][nf]);
-          }
           const int i2 = 16 * t + l16;
+          if (!wild) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              if (kRev ? 2 * ks + 1 < t : 2 * ks > t) continue;
+              const LaFrag<BF16> pf = TP::rows(lp, 16 * t, 32 * ks, lane);
+#pragma unroll
+              for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_mma(zf[ks][nf], pf, o[t][nf]);
+            }
+          } else {
+            // a score of zero times an infinity or no number of a token that this row does not see would be no number:
+            // the products that count, one by one
+#pragma unroll 1
+            for (int j = 0; j < C; ++j) {
+              if (kRev ? j < i2 : j > i2) continue;
+              const float p = la_get<BF16>(lp + (i2 * TP::LD + j) * ES);
+#pragma unroll
+              for (int nf = 0; nf < NF; ++nf)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  o[t][nf][r] = __builtin_fmaf(p, la_get<BF16>(lz + (j * TZ::LD + f0 + 16 * nf + 4 * l4 + r) * ES), o[t][nf][r]);
+            }
+          }
           if (i2 >= nr) continue;
 #pragma unroll
           for (int nf = 0; nf < NF; ++nf) {

@@ -219,3 +219,82 @@ def check_gradients(shape, bf16, segments, lengths, kind, carried, monkeypatch):
         # and as a whole, near what roundings of either sign leave
         rel = float((got[name].cpu().double() - x).norm() / x.norm().clamp(min=1e-30))
         assert rel <= (5e-3 if bf16 and name in ("dq", "dk", "dv") else 1e-5), (name, rel)
+
+
+# ------------------------------------------------------------------------------ what is not finite
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dv", [4, 40])
+def test_later_tokens_do_not_reach_earlier_ones(value, bf16, dv):
+    """A value that is not finite, in q, k, v, beta or the decays of one token, changes nothing before it (but the
+    order of the sums in its tile: both results are within the bound)."""
+    import torch
+    import selective_state_space_20_amd as sss
+    cu, at = [0, 100, 170], 41
+    c = make(4, 170, 2, 2, 2, 2, 24, dv, bf16, "ssm", cu)
+    clean = sss.linear_attention_packed_fwd(*ops(c), cu_seqlens=i32(cu), **opt(c))
+    mag, _ = ref.attention(*of_ref(c, True), cu, torch.zeros(2, 2, 24, dv).double())
+    slack = 2 * roundings(c, cu) * EPS * mag + (2.0 ** -7 * mag if bf16 else 0)
+    for name in ("q", "k", "v", "beta", "g"):
+        d = dict(c)
+        d[name] = c[name].clone()
+        d[name][at, 1] = value
+        out = sss.linear_attention_packed_fwd(*ops(d), cu_seqlens=i32(cu), **opt(d))
+        same = torch.ones_like(out, dtype=torch.bool)
+        same[at:100, 1] = False  # the token's head, from it on to the end of its sequence
+        close(out[:at], clean[:at].cpu().double(), slack[:at], name)
+        same[:at, 1] = False
+        assert torch.equal(out[same], clean[same]), name
+        if name == "q":
+            assert torch.equal(out[at + 1:], clean[at + 1:])
+        if name == "g" and value < 0:  # everything forgotten: as if the sequence began there
+            assert bool(out.isfinite().all())
+        elif not (name == "g" and value > 0):
+            assert not bool(out[at, 1].isfinite().any()), name
+        if name in ("v", "k") or value != value and name != "q":
+            assert not bool(out[at:100, 1].isfinite().any()), name
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gradients_apart(bf16):
+    """Sequences have nothing to do with each other, nor do heads; and a token's value that is not finite reaches, in
+    dv, only the tokens that it adds to."""
+    import torch
+    import selective_state_space_20_amd as sss
+    cu, at = [0, 60, 130], 80
+    c = make(5, 130, 2, 2, 2, 2, 24, 40, bf16, "gate", cu)
+    grads = lambda x: sss.linear_attention_packed_bwd(*ops(x), dout=x["dout"].to(DEV), cu_seqlens=i32(cu), **opt(x))
+    clean = grads(c)
+    zero = torch.zeros(2, 2, 24, 40).double()
+    mag = ref.gradients(*of_ref(c, True), cu, zero, ref.wide(c["dout"]).abs(), zero)
+    near = lambda got, n, rows: close(got[n][rows], clean[n][rows].cpu().double(), (
+        2 * roundings(c, cu) * EPS * mag[n] + (2.0 ** -7 * mag[n] if bf16 else 0))[rows], n)
+    for name in ("q", "k", "v", "dout"):
+        d = dict(c)
+        d[name] = c[name].clone()
+        d[name][at, 1] = float("nan")
+        got = grads(d)
+        for n, t in got.items():
+            assert torch.equal(t[:60], clean[n][:60]) and torch.equal(t[:, 0], clean[n][:, 0]), (name, n)
+        if name in ("q", "dout"):  # later tokens' dk and dv have no part of it
+            near(got, "dv", slice(at + 1, None))
+            near(got, "dk", slice(at + 1, None))
+        else:  # nor have earlier tokens' dq
+            near(got, "dq", slice(None, at))
+
+
+def test_strong_decays_and_forgetting():
+    """Log decays of zero, far below zero and -inf, beside each other, against the definition."""
+    import torch
+    import selective_state_space_20_amd as sss
+    for bf16 in (False, True):
+        cu = [0, 150]
+        c = make(6, 150, 1, 2, 1, 1, 32, 32, bf16, "gate", cu)
+        c["g"][::7], c["g"][3::11], c["g"][5::29], c["g"][20:40] = 0.0, -30.0, -float("inf"), -1e-4
+        c["g"][77] = -3e38
+        out = sss.linear_attention_packed_fwd(*ops(c), cu_seqlens=i32(cu), **opt(c))
+        zero = torch.zeros(1, 2, 32, 32).double()
+        want, _ = ref.attention(*of_ref(c), cu, zero)
+        mag, _ = ref.attention(*of_ref(c, True), cu, zero)
+        fp = (roundings(c, cu) + 64) * EPS  # exponents up to 30 log2(e) beside the decay's own rounding
+        close(out, want, fp * mag + (2 * 2.0 ** -8 * mag + 2.0 ** -8 * want.abs() if bf16 else 0), "out")
