@@ -479,7 +479,7 @@ size_t linear_attention_packed_bwd_workspace_size(int64_t tokens, int64_t nseq, 
  * decay_stride 0, dbeta (tokens, heads) with beta, dD (heads) with D_skip, dinitial_state (nseq, heads, dk, dv,
  * nullable), float32.  The states are recomputed.  Tokens outside every sequence get zero.  Required: q, k, v,
  * log_decay, dout, cu_seqlens, dq, dk_out, dv_out, dlog_decay, dbeta with beta, dD with D_skip; with no tokens
- * the sums over them are zero. */
+ * what has none may be NULL, and the sums over them are zero. */
 int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_stride, int64_t q_heads, const void* k,
                                 int64_t k_stride, int64_t k_head_stride, int64_t k_heads, const void* v, int64_t v_stride,
                                 int64_t v_head_stride, const float* log_decay, int64_t decay_stride, const float* beta,

@@ -305,8 +305,8 @@ int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_
                                 void* dk_out, void* dv_out, float* dlog_decay, float* dbeta, float* dD, float* dinitial_state,
                                 int64_t tokens, int64_t nseq, int64_t heads, int64_t dk, int64_t dv, int io_dtype,
                                 void* workspace, size_t workspace_bytes, sss_stream_t stream) {
-  if (!q || !k || !v || !log_decay || !dout || !cu_seqlens || !dq || !dk_out || !dv_out || !dlog_decay || (beta && !dbeta) ||
-      (D_skip && !dD))
+  if (!cu_seqlens || (D_skip && !dD) || (decay_stride == 0 && (!log_decay || !dlog_decay)) ||
+      (tokens != 0 && (!q || !k || !v || !log_decay || !dout || !dq || !dk_out || !dv_out || !dlog_decay || (beta && !dbeta))))
     return SSS_ERR_NULL_ARG;
   const int st = dims_status(tokens, nseq, 0, heads, q_heads, k_heads, dk, dv);
   if (st != SSS_OK) return st;
