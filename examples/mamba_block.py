@@ -1,4 +1,4 @@
-"""One Mamba block around the library's operators, served and trained.
+"""Mamba blocks around the library's operators, served and trained.
 
     python examples/mamba_block.py
 
@@ -12,6 +12,10 @@ torch; the directional derivative of the loss is compared with a difference of t
 
 The block:  x, z = in_proj(u);  x = silu(conv(x));  dt, B, C = x_proj(x);  y = scan(x, dt, A, B, C, D);
 h = residual + scale * norm(out_proj(norm(y * silu(z))));  the next block's input is norm(h).
+
+HeadBlock is the same with heads: one step size and decay for each head, y = linear attention of the
+queries C, keys B and values x with the decays dt A; each head's output is layer normed and gated, and
+layer norms stand between the blocks:  h = residual + out_proj(layernorm(y) * silu(z)).
 """
 import os
 import sys
@@ -128,9 +132,109 @@ class Block:
         return d
 
 
-def serve(model_dim=256, lengths=(37, 1, 130, 64), new_tokens=6, dtype=torch.float32, device="cuda:0"):
+class HeadBlock:
+    def __init__(self, model_dim, dtype, seed=0, device="cuda:0", head_dim=32):
+        g = torch.Generator(device=device).manual_seed(seed)
+        rnd = lambda *s, scale=1.0: torch.randn(*s, device=device, generator=g) * scale
+        inner = 2 * model_dim
+        self.model_dim, self.inner, self.heads, self.head_dim, self.dtype = model_dim, inner, inner // head_dim, head_dim, dtype
+        self.in_proj = rnd(model_dim, 2 * inner, scale=model_dim ** -0.5).to(dtype)
+        self.x_proj = rnd(inner, self.heads + 2 * STATES, scale=inner ** -0.5).to(dtype)
+        self.out_proj = rnd(inner, model_dim, scale=inner ** -0.5).to(dtype)
+        self.conv_w, self.conv_b = rnd(inner, WIDTH, scale=0.5), rnd(inner, scale=0.1)
+        self.A = -torch.exp(torch.rand(self.heads, device=device, generator=g) * 2.77)
+        self.D, self.dt_bias = rnd(self.heads), rnd(self.heads, scale=0.5) - 2.0
+        self.head_w, self.head_b, self.next_w, self.next_b = 1 + rnd(inner, scale=0.1), rnd(inner, scale=0.1), \
+            1 + rnd(model_dim, scale=0.1), rnd(model_dim, scale=0.1)
+
+    def cache(self, slots):
+        dev = self.A.device
+        return (torch.zeros(slots, WIDTH - 1, self.inner, dtype=self.dtype, device=dev),
+                torch.zeros(slots, self.heads, STATES, self.head_dim, device=dev))
+
+    def _split(self, u):
+        xz = u @ self.in_proj
+        return xz[:, :self.inner], xz[:, self.inner:]
+
+    def _operands(self, x):
+        """Queries, keys, values, log decays and step sizes (and the projection's rows) of x (rows, inner)."""
+        rows = x @ self.x_proj
+        step = torch.nn.functional.softplus(rows[:, :self.heads].float() + self.dt_bias)
+        k = rows[:, self.heads:self.heads + STATES].unflatten(1, (1, STATES))  # B and C, shared by all heads
+        q = rows[:, self.heads + STATES:].unflatten(1, (1, STATES))
+        return q, k, x.unflatten(1, (self.heads, self.head_dim)), step * self.A, step, rows
+
+    def _finish(self, y, z, residual):
+        y = sss.layer_norm_fwd(y.flatten(1), self.head_w, self.head_b, group_size=self.head_dim)
+        return sss.layer_norm_fwd((y * torch.nn.functional.silu(z)) @ self.out_proj, self.next_w, self.next_b, residual)
+
+    def prompts(self, u, residual, cu_seqlens, cache, slots, continued):
+        x, z = self._split(u)
+        x = sss.causal_conv1d_packed_fwd(x, self.conv_w, self.conv_b, cu_seqlens=cu_seqlens, conv_state=cache[0],
+                                         state_indices=slots, has_initial=continued, silu=True)
+        q, k, v, g, step, _ = self._operands(x)
+        y = sss.linear_attention_packed_fwd(q, k, v, g, cu_seqlens=cu_seqlens, beta=step, D=self.D, state=cache[1],
+                                            state_indices=slots, has_initial=continued)
+        return self._finish(y, z, residual)
+
+    def step(self, u, residual, cache, slots):
+        x, z = self._split(u)
+        x = sss.causal_conv1d_update(x, self.conv_w, self.conv_b, conv_state=cache[0], state_indices=slots, silu=True)
+        q, k, v, g, step, _ = self._operands(x)
+        y = sss.linear_attention_update_slots(q, k, v, g, beta=step, D=self.D, state=cache[1], state_indices=slots)
+        return self._finish(y, z, residual)
+
+    def forward(self, u, residual):
+        bt, length, _ = u.shape
+        flat = lambda v: v.reshape(bt * length, v.shape[-1])
+        k = {"u": u, "cu": torch.arange(bt + 1, dtype=torch.int32, device=u.device) * length}
+        k["xz"] = u @ self.in_proj
+        k["conv_in"] = k["xz"][..., :self.inner].contiguous()
+        k["x"] = flat(sss.causal_conv1d_fwd(k["conv_in"], self.conv_w, self.conv_b, silu=True))
+        k["ops"] = self._operands(k["x"])
+        q, key, v, g, step, _ = k["ops"]
+        k["y"] = sss.linear_attention_packed_fwd(q, key, v, g, cu_seqlens=k["cu"], beta=step, D=self.D).flatten(1)
+        k["n"], *k["head_stats"] = sss.layer_norm_fwd(k["y"], self.head_w, self.head_b, group_size=self.head_dim, return_stats=True)
+        k["z"] = flat(k["xz"])[:, self.inner:]
+        k["gated"] = k["n"] * torch.nn.functional.silu(k["z"])
+        out, h, *k["stats"] = sss.layer_norm_fwd(k["gated"] @ self.out_proj, self.next_w, self.next_b, flat(residual),
+                                                 return_stats=True)
+        k["h"] = h
+        return out.view(bt, length, -1), h.view(bt, length, -1), k
+
+    def backward(self, dout, dh, k):
+        bt, length, _ = dout.shape
+        flat = lambda v: v.reshape(bt * length, v.shape[-1])
+        d = {}
+        r = sss.layer_norm_bwd(flat(dout), k["h"], self.next_w, mean=k["stats"][0], rstd=k["stats"][1], bias=True,
+                               dresidual_out=flat(dh))
+        d["next_w"], d["next_b"], d["residual"] = r["dweight"], r["dbias"], r["dresidual"]
+        d["out_proj"] = k["gated"].t() @ r["dx"]
+        dgated, sg = r["dx"] @ self.out_proj.t(), torch.sigmoid(k["z"])
+        dxz = torch.empty_like(k["xz"])
+        flat(dxz)[:, self.inner:] = dgated * k["n"] * sg * (1 + k["z"] * (1 - sg))
+        n = sss.layer_norm_bwd((dgated * k["z"] * sg).contiguous(), k["y"], self.head_w, mean=k["head_stats"][0],
+                               rstd=k["head_stats"][1], bias=True, group_size=self.head_dim)
+        d["head_w"], d["head_b"] = n["dweight"], n["dbias"]
+        q, key, v, g, step, rows = k["ops"]
+        a = sss.linear_attention_packed_bwd(q, key, v, g, dout=n["dx"].unflatten(1, (self.heads, self.head_dim)), cu_seqlens=k["cu"],
+                                            beta=step, D=self.D)
+        d["D"], d["A"] = a["dD"], (a["dlog_decay"] * step).sum(0)
+        ddt = (a["dbeta"] + a["dlog_decay"] * self.A) * torch.sigmoid(rows[:, :self.heads].float() + self.dt_bias)
+        d["dt_bias"] = ddt.sum(0)
+        drows = torch.cat([ddt.to(self.dtype), a["dk"].flatten(1), a["dq"].flatten(1)], -1)
+        d["x_proj"] = k["x"].t() @ drows
+        c = sss.causal_conv1d_bwd(k["conv_in"], self.conv_w, self.conv_b, silu=True, dx=dxz[..., :self.inner],
+                                  dout=(a["dv"].flatten(1) + drows @ self.x_proj.t()).view_as(k["conv_in"]))
+        d["conv_w"], d["conv_b"] = c["dweight"], c["dbias"]
+        d["in_proj"] = flat(k["u"]).t() @ flat(dxz)
+        d["u"] = dxz @ self.in_proj.t()
+        return d
+
+
+def serve(model_dim=256, lengths=(37, 1, 130, 64), new_tokens=6, dtype=torch.float32, device="cuda:0", kind=Block):
     """The largest difference between generated and whole-prompt outputs, relative to the largest value."""
-    block, n = Block(model_dim, dtype, device=device), len(lengths)
+    block, n = kind(model_dim, dtype, device=device), len(lengths)
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=device)
     starts = lambda ls: i32([sum(ls[:i]) for i in range(len(ls) + 1)])
     g = torch.Generator(device=device).manual_seed(1)
@@ -157,9 +261,9 @@ def serve(model_dim=256, lengths=(37, 1, 130, 64), new_tokens=6, dtype=torch.flo
     return float((got.float() - want.float()).abs().max() / want.float().abs().max())
 
 
-def train(model_dim=96, batch=2, length=50, device="cuda:0"):
+def train(model_dim=96, batch=2, length=50, device="cuda:0", kind=Block):
     """{parameter: (directional derivative by backward, by central differences)}."""
-    block = Block(model_dim, torch.float32, seed=3, device=device)
+    block = kind(model_dim, torch.float32, seed=3, device=device)
     g = torch.Generator(device=device).manual_seed(4)
     rnd = lambda *s: torch.randn(*s, device=device, generator=g)
     u, residual = rnd(batch, length, model_dim), rnd(batch, length, model_dim)
@@ -188,7 +292,10 @@ def train(model_dim=96, batch=2, length=50, device="cuda:0"):
 
 
 if __name__ == "__main__":
-    for dt in (torch.float32, torch.bfloat16):
-        print(f"serve {dt}: generated against whole prompts, relative difference {serve(dtype=dt):.2e}")
-    for name, (by_backward, by_difference) in train().items():
-        print(f"train {name:9s} derivative along the gradient {by_backward:.6g}, by differences {by_difference:.6g}")
+    for block in (Block, HeadBlock):
+        for dt in (torch.float32, torch.bfloat16):
+            print(f"{block.__name__} serve {dt}: generated against whole prompts, relative difference "
+                  f"{serve(dtype=dt, kind=block):.2e}")
+        for name, (by_backward, by_difference) in train(kind=block).items():
+            print(f"{block.__name__} train {name:9s} derivative along the gradient {by_backward:.6g}, by differences "
+                  f"{by_difference:.6g}")
