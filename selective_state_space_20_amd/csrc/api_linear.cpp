@@ -240,7 +240,7 @@ int linear_attention_packed_fwd(const void* q, int64_t q_stride, int64_t q_head_
     w.sum = at(p.sum);
     w.flag = reinterpret_cast<int32_t*>(ws + p.flag);
     hipError_t e = la_launch(pad(dk), pad(dv), kLaFoldFwd, bf16, w, (unsigned)((p.nseg - 1) * heads), s);
-    if (e == hipSuccess) e = la_carry(w.end, w.sum, w.flag, at(p.enter), w.hs, (int)heads, p.nseg, false, s);
+    if (e == hipSuccess) e = la_carry({w.end, w.sum, w.flag, at(p.enter)}, nullptr, w.hs, (int)heads, p.nseg, s);
     if (e != hipSuccess) return SSS_ERR_HIP;
   }
   return status_of(la_launch(pad(dk), pad(dv), kLaFwd, bf16, w, (unsigned)(p.nseg * heads), s));
@@ -336,7 +336,7 @@ int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_
   const int cus = current_device_cus();
   if (cus <= 0) return SSS_ERR_HIP;
   const Plan p = plan(tokens, nseq, heads, q_heads, k_heads, dk, dv, true, cus);
-  if (!launch_ok(p.nseg * heads) || !launch_ok(nseq) || (double)tokens * (double)heads * (double)dk + 256.0 > kMaxThreads)
+  if (!launch_ok(3 * p.nseg * heads) || !launch_ok(nseq) || (double)tokens * (double)heads * (double)dk + 256.0 > kMaxThreads)
     return SSS_ERR_BAD_DIM;
   if (p.total > 0) {
     if (workspace == nullptr || workspace_bytes < p.total) return SSS_ERR_WORKSPACE;
@@ -368,16 +368,16 @@ int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_
     a.end = at(p.end);
     a.sum = at(p.sum);
     a.flag = reinterpret_cast<int32_t*>(ws + p.flag);
-    e = la_launch(ek, ev, kLaFoldFwd, bf16, a, folds, s);
-    if (e == hipSuccess) e = la_carry(a.end, a.sum, a.flag, at(p.enter), w.hs, H, p.nseg, false, s);
-    a.y = sq;
-    a.z = so;
-    a.from = dfinal_state;
-    a.end = at(p.rend);
-    a.sum = at(p.rsum);
-    a.flag = reinterpret_cast<int32_t*>(ws + p.rflag);
-    if (e == hipSuccess) e = la_launch(ek, ev, kLaFoldRev, bf16, a, folds, s);
-    if (e == hipSuccess) e = la_carry(a.end, a.sum, a.flag, at(p.renter), w.hs, H, p.nseg, true, s);
+    LaWalk b = a;
+    b.y = sq;
+    b.z = so;
+    b.from = dfinal_state;
+    b.end = at(p.rend);
+    b.sum = at(p.rsum);
+    b.flag = reinterpret_cast<int32_t*>(ws + p.rflag);
+    e = la_launch_folds(ek, ev, bf16, a, b, folds, s);
+    const LaCarry back{b.end, b.sum, b.flag, at(p.renter)};
+    if (e == hipSuccess) e = la_carry({a.end, a.sum, a.flag, at(p.enter)}, &back, w.hs, H, p.nseg, s);
   }
   if (e == hipSuccess && p.nseg > 0) {
     LaWalk a = w;  // dq
@@ -400,28 +400,29 @@ int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_
     a.edge = at(p.edge);
     a.last = at(p.last);
     a.trace = D_skip ? at(p.trace) : nullptr;
-    e = la_launch(ev, ek, kLaDq, bf16, a, grid, s);
-    a.x = sv;  // dk
-    a.y = so;
-    a.z = sq;
-    a.w = sk;
-    a.out_f32 = k_heads < heads;
-    a.out = a.out_f32 ? ws + p.dk : static_cast<char*>(dk_out);
-    a.from = dfinal_state;
-    a.to = dinitial_state;
-    a.enter = at(p.renter);
-    a.cols2 = at(p.cols2);
-    if (e == hipSuccess) e = la_launch(ev, ek, kLaDk, bf16, a, grid, s);
-    a.x = sk;  // dv
-    a.y = sq;
-    a.z = so;
-    a.out_f32 = 0;
-    a.out = static_cast<char*>(dv_out);
-    a.out_st = heads * dv;
-    a.out_sh = dv;
-    a.se = dv;
-    a.sf = 1;
-    if (e == hipSuccess) e = la_launch(ek, ev, kLaDv, bf16, a, grid, s);
+    LaWalk b = a;  // dk
+    b.x = sv;
+    b.y = so;
+    b.z = sq;
+    b.w = sk;
+    b.out_f32 = k_heads < heads;
+    b.out = b.out_f32 ? ws + p.dk : static_cast<char*>(dk_out);
+    b.from = dfinal_state;
+    b.to = dinitial_state;
+    b.enter = at(p.renter);
+    b.cols2 = at(p.cols2);
+    LaWalk c = b;  // dv
+    c.x = sk;
+    c.y = sq;
+    c.z = so;
+    c.out_f32 = 0;
+    c.out = static_cast<char*>(dv_out);
+    c.out_st = heads * dv;
+    c.out_sh = dv;
+    c.se = dv;
+    c.sf = 1;
+    e = la_launch_grads(ev, ek, bf16, a, b, c, grid, s);
+    if (e == hipSuccess && ek != ev) e = la_launch(ek, ev, kLaDv, bf16, c, grid, s);
     if (e == hipSuccess && q_heads < heads)
       e = la_sum_heads(at(p.dq), dq, tokens, H, (int)(heads / q_heads), (int)dk, bf16, s);
     if (e == hipSuccess && k_heads < heads)

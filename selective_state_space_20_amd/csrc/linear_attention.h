@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "vec.h"
+
 namespace sss {
 
 constexpr int kLaTile = 64;  // tokens of a tile (bf16); fp32 takes 32
@@ -63,10 +65,19 @@ enum LaMode { kLaFoldFwd, kLaFoldRev, kLaFwd, kLaDq, kLaDk, kLaDv };
 // E: rows of the walk's state (the width of x and y), F: its columns (that of z and out), rounded
 // up to 64, 128 or 256.
 hipError_t la_launch(int E, int F, LaMode mode, bool bf16, const LaWalk& g, unsigned grid, hipStream_t stream);
+// Both folds (kLaFoldFwd, kLaFoldRev), n workgroups each; and dq and dk, and where E is F also dv.
+hipError_t la_launch_folds(int E, int F, bool bf16, const LaWalk& fwd, const LaWalk& rev, unsigned n, hipStream_t stream);
+hipError_t la_launch_grads(int E, int F, bool bf16, const LaWalk& dq, const LaWalk& dk, const LaWalk& dv, unsigned n,
+                           hipStream_t stream);
 
-// state between segments: enter[c + 1] (rev: enter[c - 1]) from end, sum and flag of segment c
-hipError_t la_carry(const float* end, const float* sum, const int32_t* flag, float* enter, int64_t hs, int H, int nseg, bool rev,
-                    hipStream_t stream);
+// States between segments: enter[c + 1] from end, sum and flag of segment c; of a second set, if any, enter[c - 1].
+struct LaCarry {
+  const float* end;
+  const float* sum;
+  const int32_t* flag;
+  float* enter;
+};
+hipError_t la_carry(const LaCarry& fwd, const LaCarry* rev, int64_t hs, int H, int nseg, hipStream_t stream);
 
 // dlog_decay and dbeta from what the walks leave, and dD: see linear_attention_parts.hip
 struct LaFinish {
@@ -110,6 +121,32 @@ struct LaStep {
 hipError_t la_step(const LaStep& a, bool bf16, hipStream_t stream);
 
 template <int E, int F>
+hipError_t la_run_folds(bool bf16, const LaWalk& fwd, const LaWalk& rev, unsigned n, hipStream_t stream);
+template <int E, int F>
+hipError_t la_run_grads(bool bf16, const LaWalk& dq, const LaWalk& dk, const LaWalk& dv, unsigned n, hipStream_t stream);
+template <int E, int F>
 hipError_t la_run(LaMode mode, bool bf16, const LaWalk& g, unsigned grid, hipStream_t stream);
+
+#ifdef __HIPCC__
+// The boundaries of a packed batch, in a wave's lanes where there are at most 64, so that a walk over its sequences
+// waits for memory once.  All lanes take part in each call; s and t are the same in all.
+struct LaBounds {
+  const int32_t* cu;
+  int nseq, lane, mine;
+  __device__ __forceinline__ LaBounds(const int32_t* cu_, int nseq_, int lane_) : cu(cu_), nseq(nseq_), lane(lane_) {
+    mine = cu[min(lane, nseq)];
+  }
+  __device__ __forceinline__ int at(int s) const {
+    return nseq < 64 ? __builtin_amdgcn_readlane(mine, s) : __builtin_amdgcn_readfirstlane(cu[s]);
+  }
+  // the last sequence that begins at t or before
+  __device__ __forceinline__ int find(int t) const {
+    const int s = nseq < 64 ? __builtin_popcountll(__builtin_amdgcn_ballot_w64(lane <= nseq && mine <= t)) - 1
+                            : __builtin_amdgcn_readfirstlane(find_seq(cu, nseq, t, lane));
+    return min(max(s, 0), nseq - 1);
+  }
+};
+
+#endif
 
 }  // namespace sss

@@ -268,10 +268,16 @@ struct LaShape {
   static constexpr int NW = F == 256 ? 8 : 4, NT = NW * 64, NF = F / (16 * NW);
   static constexpr int C = BF16 ? kLaTile : kLaTile / 2, TI = C / 16, KS = C / 32;
   static constexpr int NS = TI * (TI + 1) / 2, SPW = (NS + NW - 1) / NW;  // tiles of scores that are not zero; per wave
+  // LDS: the tiles x, y, z, w and scores, weights of y z^T, beta, sums of the columns' waves, two flags
+  static constexpr int ROWX = LaTile<BF16, E>::LD * (BF16 ? 2 : 4) * C, ROWZ = LaTile<BF16, F>::LD * (BF16 ? 2 : 4) * C;
+  static constexpr int kY = kOut ? ROWX : 0, kZ = kY + ROWX, kW = kZ + ROWZ, kP = kW + (kDots ? ROWZ : 0);
+  static constexpr int kU = kP + (kOut ? LaTile<BF16, C>::LD * (BF16 ? 2 : 4) * C : 0), kB = kU + 4 * C, kR = kB + 4 * C;
+  static constexpr int kWild = kR + (kDots ? 4 * NW * C : 0), kBytes = kWild + 16;
 };
 
+// One segment and head; id: of the workgroup among those of the walk.
 template <bool BF16, int E, int F, int MODE>
-__global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) void la_walk_kernel(LaWalk g) {
+__device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id) {
   using S = LaShape<BF16, E, F, MODE>;
   constexpr int NW = S::NW, NT = S::NT, NF = S::NF, C = S::C, TI = S::TI, KS = S::KS, ET = E / 16, EK = E / 32;
   constexpr bool kRev = S::kRev, kOut = S::kOut, kDots = S::kDots;
@@ -279,31 +285,37 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
   using TX = LaTile<BF16, E>;
   using TZ = LaTile<BF16, F>;
   using TP = LaTile<BF16, C>;
-  __shared__ __attribute__((aligned(16))) char lx[kOut ? C * TX::LD * ES : 16];
-  __shared__ __attribute__((aligned(16))) char ly[C * TX::LD * ES];
-  __shared__ __attribute__((aligned(16))) char lz[C * TZ::LD * ES];
-  __shared__ __attribute__((aligned(16))) char lw[kDots ? C * TZ::LD * ES : 16];
-  __shared__ __attribute__((aligned(16))) char lp[kOut ? C * TP::LD * ES : 16];
-  __shared__ __attribute__((aligned(16))) float luw[C], lbeta[C];  // weights of y z^T, beta
-  __shared__ int lwild[2];  // a tile's z has a value that is not finite (alternating tiles)
+  char* const lx = smem;
+  char* const ly = smem + S::kY;
+  char* const lz = smem + S::kZ;
+  char* const lw = smem + S::kW;
+  char* const lp = smem + S::kP;
+  float* const luw = (float*)(smem + S::kU);    // weights of y z^T
+  float* const lbeta = (float*)(smem + S::kB);  // beta
+  float* const lrr = (float*)(smem + S::kR);    // sums over the columns of each wave
+  int* const lwild = (int*)(smem + S::kWild);   // a tile's z has a value that is not finite (alternating tiles)
   // between the rows of z: the sums of log2 decays; of y: the weights of x M, and the waves' parts of a
   // sum
   auto lg = [&](int i) __attribute__((always_inline)) { return (double*)(lz + (i * TZ::LD + F) * ES); };
   auto lsr = [&](int i) __attribute__((always_inline)) { return (float*)(ly + (i * TX::LD + E) * ES); };
   auto lred = [&](int i) __attribute__((always_inline)) { return (float*)(ly + (i * TX::LD + E) * ES + 4); };
-  __shared__ float lrr[kDots ? NW * C : 1];
 
   auto uni = [](int v) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(v); };
   const int lane = threadIdx.x & 63;
   const int wave_id = uni((int)(threadIdx.x >> 6));
   const int l16 = lane & 15, l4 = lane >> 4;
-  const unsigned id = xcd_remap(blockIdx.x, gridDim.x);
   const int h = uni((int)(id % (unsigned)g.H));
   int seg = uni((int)(id / (unsigned)g.H));
   if constexpr (MODE == kLaFoldRev) ++seg;  // the first segment has no edge on its left
   const int c0 = seg * g.K, tend = min(c0 + g.K, g.tokens);
-  const int lo = uni(min(max(g.cu[0], 0), g.tokens));
-  const int hi = uni(min(max(g.cu[g.nseq], 0), g.tokens));
+  const LaBounds cu(g.cu, g.nseq, lane);
+  // slots and starts of the first 64 sequences, with the boundaries
+  int my_slot = lane, my_init = 0;
+  if (g.state != nullptr && g.nseq > 0) {
+    if (g.sidx != nullptr) my_slot = g.sidx[min(lane, g.nseq - 1)];
+    if (g.init != nullptr) my_init = g.init[min(lane, g.nseq - 1)];
+  }
+  const int lo = min(max(cu.at(0), 0), g.tokens), hi = min(max(cu.at(g.nseq), 0), g.tokens);
   const int f0 = wave_id * (16 * NF);  // the wave's columns
   const int Ew = g.y.width, Fw = g.z.width;
   const char* const xp = kOut ? g.x.p + uni(h / g.x.rep) * g.x.sh * ES : nullptr;
@@ -700,8 +712,12 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
 
   auto slot_of = [&](int s) __attribute__((always_inline)) {  // -1: none
     if (g.state == nullptr) return -1;
-    const int slot = g.sidx != nullptr ? g.sidx[s] : s;
+    const int slot = g.nseq <= 64 ? __builtin_amdgcn_readlane(my_slot, s) : g.sidx != nullptr ? uni(g.sidx[s]) : s;
     return (unsigned)slot < (unsigned)g.slots ? slot : -1;
+  };
+  auto continues = [&](int s) __attribute__((always_inline)) {  // its slot's state
+    if (g.state == nullptr || g.init == nullptr) return false;
+    return (g.nseq <= 64 ? __builtin_amdgcn_readlane(my_init, s) : uni(g.init[s])) != 0;
   };
 
   if constexpr (!kOut) {
@@ -709,14 +725,14 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
     int flag = 0;  // 0: none; 1: it runs across the other edge too; 2: it begins (ends) in the segment
     const int edge = kRev ? c0 : tend;
     if (edge > lo && edge < hi) {
-      const int s = min(max(uni(find_seq(g.cu, g.nseq, kRev ? c0 : tend - 1, lane)), 0), g.nseq - 1);
-      const int end = uni(min(g.cu[s + 1], hi)), beg = uni(max(g.cu[s], 0));
+      const int s = cu.find(kRev ? c0 : tend - 1);
+      const int end = min(cu.at(s + 1), hi), beg = max(cu.at(s), 0);
       if (kRev ? beg < c0 && end > c0 : beg < tend && end > tend) {
         flag = (kRev ? end <= tend : beg >= c0) ? 2 : 1;
         const float* src = nullptr;
         if (flag == 2) {
           if (g.from != nullptr) src = g.from + of_seq(s);
-          else if (g.init != nullptr && slot_of(s) >= 0 && g.init[s] != 0) src = g.state + of_seq(slot_of(s));
+          else if (slot_of(s) >= 0 && continues(s)) src = g.state + of_seq(slot_of(s));
         }
         from(src);
         // for the second pass: the slot itself is overwritten there, by another workgroup
@@ -743,18 +759,18 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
       clear(c0, gap0);
       clear(max(gap1, gap0), tend);
     }
-    int s = t < stop ? min(max(uni(find_seq(g.cu, g.nseq, t, lane)), 0), g.nseq - 1) : 0;
+    int s = t < stop ? cu.find(t) : 0;
     while (t < stop) {
-      const int end = uni(min(g.cu[s + 1], hi));
+      const int end = min(cu.at(s + 1), hi);
       if (end <= t) {  // past this sequence (or an empty one)
         if (++s >= g.nseq) break;
         continue;
       }
       const int e = min(end, tend);
-      const bool before = began_before(g.cu[s], c0), after = end > tend;
+      const bool before = began_before(cu.at(s), c0), after = end > tend;
       if constexpr (MODE == kLaFwd) {
         const int slot = slot_of(s);
-        const bool old = slot >= 0 && g.init != nullptr && g.init[s] != 0;
+        const bool old = slot >= 0 && continues(s);
         from(before ? g.enter + at_seg : !old ? nullptr : after ? g.begin + at_seg : g.state + of_seq(slot));
         walk(t, e, nullptr);
         if (!after && slot >= 0) to(g.state + of_seq(slot));
@@ -780,28 +796,77 @@ __global__ __launch_bounds__(F == 256 ? 512 : 256, E == 256 && F < 256 ? 1 : 2) 
   }
 }
 
+template <int E, int F>
+constexpr int kLaThreads = F == 256 ? 512 : 256;
+template <int E, int F>
+constexpr int kLaWaves = E == 256 && F < 256 ? 1 : 2;  // per SIMD, at least
+
+template <bool BF16, int E, int F, int MODE>
+__global__ __launch_bounds__((kLaThreads<E, F>), (kLaWaves<E, F>)) void la_walk_kernel(LaWalk g) {
+  __shared__ __attribute__((aligned(16))) char smem[LaShape<BF16, E, F, MODE>::kBytes];
+  la_walk<BF16, E, F, MODE>(g, smem, xcd_remap(blockIdx.x, gridDim.x));
+}
+
+// The gradients' walks in one launch each for what does not wait for each other: both folds, and dq with dk, and dv where
+// its state has the same sizes.  n: workgroups of each.
+constexpr int la_most(int a, int b) { return a > b ? a : b; }
+
+template <bool BF16, int E, int F>
+__global__ __launch_bounds__((kLaThreads<E, F>), (kLaWaves<E, F>)) void la_folds_kernel(LaWalk fwd, LaWalk rev, unsigned n) {
+  __shared__ __attribute__((aligned(16)))
+  char smem[la_most(LaShape<BF16, E, F, kLaFoldFwd>::kBytes, LaShape<BF16, E, F, kLaFoldRev>::kBytes)];
+  if (blockIdx.x < n) la_walk<BF16, E, F, kLaFoldFwd>(fwd, smem, xcd_remap(blockIdx.x, n));
+  else la_walk<BF16, E, F, kLaFoldRev>(rev, smem, xcd_remap(blockIdx.x - n, n));
+}
+
+template <bool BF16, int E, int F>
+__global__ __launch_bounds__((kLaThreads<E, F>), (kLaWaves<E, F>)) void la_grads_kernel(LaWalk dq, LaWalk dk, LaWalk dv, unsigned n) {
+  __shared__ __attribute__((aligned(16)))
+  char smem[la_most(LaShape<BF16, E, F, kLaDq>::kBytes, LaShape<BF16, E, F, kLaDk>::kBytes)];
+  static_assert(LaShape<BF16, E, F, kLaDv>::kBytes <= sizeof(smem), "dv's tiles are fewer");
+  if (blockIdx.x < n) la_walk<BF16, E, F, kLaDq>(dq, smem, xcd_remap(blockIdx.x, n));
+  else if (blockIdx.x < 2 * n) la_walk<BF16, E, F, kLaDk>(dk, smem, xcd_remap(blockIdx.x - n, n));
+  else if constexpr (E == F) la_walk<BF16, E, F, kLaDv>(dv, smem, xcd_remap(blockIdx.x - 2 * n, n));
+}
+
 #ifdef SSS_INST_E
 template <int E, int F>
 hipError_t la_run(LaMode mode, bool bf16, const LaWalk& g, unsigned grid, hipStream_t stream) {
+  const dim3 block(kLaThreads<E, F>);
 #define SSS_LA_MODE(MODE)                                                                                          \
-  case MODE:                                                                                                       \
-    if (bf16) hipLaunchKernelGGL((la_walk_kernel<true, E, F, MODE>), dim3(grid),                                    \
-                                 dim3(LaShape<true, E, F, MODE>::NT), 0, stream, g);                               \
-    else hipLaunchKernelGGL((la_walk_kernel<false, E, F, MODE>), dim3(grid), dim3(LaShape<false, E, F, MODE>::NT), 0, \
-                            stream, g);                                                                            \
-    return hipGetLastError();
-  switch (mode) {
-    SSS_LA_MODE(kLaFoldFwd)
-    SSS_LA_MODE(kLaFoldRev)
-    SSS_LA_MODE(kLaFwd)
-    SSS_LA_MODE(kLaDq)
-    SSS_LA_MODE(kLaDk)
+  if (mode == MODE) {                                                                                              \
+    if (bf16) hipLaunchKernelGGL((la_walk_kernel<true, E, F, MODE>), dim3(grid), block, 0, stream, g);             \
+    else hipLaunchKernelGGL((la_walk_kernel<false, E, F, MODE>), dim3(grid), block, 0, stream, g);                 \
+    return hipGetLastError();                                                                                      \
+  }
+  SSS_LA_MODE(kLaFoldFwd)
+  SSS_LA_MODE(kLaFwd)
+  if constexpr (E != F) {
     SSS_LA_MODE(kLaDv)
   }
 #undef SSS_LA_MODE
   return hipErrorInvalidValue;
 }
+
+template <int E, int F>
+hipError_t la_run_folds(bool bf16, const LaWalk& fwd, const LaWalk& rev, unsigned n, hipStream_t stream) {
+  const dim3 block(kLaThreads<E, F>);
+  if (bf16) hipLaunchKernelGGL((la_folds_kernel<true, E, F>), dim3(2 * n), block, 0, stream, fwd, rev, n);
+  else hipLaunchKernelGGL((la_folds_kernel<false, E, F>), dim3(2 * n), block, 0, stream, fwd, rev, n);
+  return hipGetLastError();
+}
+
+template <int E, int F>
+hipError_t la_run_grads(bool bf16, const LaWalk& dq, const LaWalk& dk, const LaWalk& dv, unsigned n, hipStream_t stream) {
+  const dim3 block(kLaThreads<E, F>), grid((E == F ? 3 : 2) * n);
+  if (bf16) hipLaunchKernelGGL((la_grads_kernel<true, E, F>), grid, block, 0, stream, dq, dk, dv, n);
+  else hipLaunchKernelGGL((la_grads_kernel<false, E, F>), grid, block, 0, stream, dq, dk, dv, n);
+  return hipGetLastError();
+}
+
 template hipError_t la_run<SSS_INST_E, SSS_INST_F>(LaMode, bool, const LaWalk&, unsigned, hipStream_t);
+template hipError_t la_run_folds<SSS_INST_E, SSS_INST_F>(bool, const LaWalk&, const LaWalk&, unsigned, hipStream_t);
+template hipError_t la_run_grads<SSS_INST_E, SSS_INST_F>(bool, const LaWalk&, const LaWalk&, const LaWalk&, unsigned, hipStream_t);
 #endif
 
 }  // namespace sss

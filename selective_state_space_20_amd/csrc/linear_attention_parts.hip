@@ -10,56 +10,78 @@
 namespace sss {
 
 // Walks are compiled once per pair of sizes (build.py).
-#define SSS_LA_EXTERN(E, F) extern template hipError_t la_run<E, F>(LaMode, bool, const LaWalk&, unsigned, hipStream_t);
+#define SSS_LA_EXTERN(E, F)                                                                                          \
+  extern template hipError_t la_run<E, F>(LaMode, bool, const LaWalk&, unsigned, hipStream_t);                       \
+  extern template hipError_t la_run_folds<E, F>(bool, const LaWalk&, const LaWalk&, unsigned, hipStream_t);          \
+  extern template hipError_t la_run_grads<E, F>(bool, const LaWalk&, const LaWalk&, const LaWalk&, unsigned, hipStream_t);
 #define SSS_LA_SIZES(CALL) \
   CALL(64, 64) CALL(64, 128) CALL(64, 256) CALL(128, 64) CALL(128, 128) CALL(128, 256) CALL(256, 64) CALL(256, 128) CALL(256, 256)
 SSS_LA_SIZES(SSS_LA_EXTERN)
 #undef SSS_LA_EXTERN
 
-hipError_t la_launch(int E, int F, LaMode mode, bool bf16, const LaWalk& g, unsigned grid, hipStream_t stream) {
-#define SSS_LA_CALL(E_, F_) \
-  if (E == E_ && F == F_) return la_run<E_, F_>(mode, bf16, g, grid, stream);
-  SSS_LA_SIZES(SSS_LA_CALL)
-#undef SSS_LA_CALL
-  return hipErrorInvalidValue;
-}
+#define SSS_LA_PICK(NAME, ...)                                      \
+  do {                                                              \
+    if (E == 64 && F == 64) return NAME<64, 64>(__VA_ARGS__);       \
+    if (E == 64 && F == 128) return NAME<64, 128>(__VA_ARGS__);     \
+    if (E == 64 && F == 256) return NAME<64, 256>(__VA_ARGS__);     \
+    if (E == 128 && F == 64) return NAME<128, 64>(__VA_ARGS__);     \
+    if (E == 128 && F == 128) return NAME<128, 128>(__VA_ARGS__);   \
+    if (E == 128 && F == 256) return NAME<128, 256>(__VA_ARGS__);   \
+    if (E == 256 && F == 64) return NAME<256, 64>(__VA_ARGS__);     \
+    if (E == 256 && F == 128) return NAME<256, 128>(__VA_ARGS__);   \
+    if (E == 256 && F == 256) return NAME<256, 256>(__VA_ARGS__);   \
+    return hipErrorInvalidValue;                                    \
+  } while (0)
 
-// One thread per element of the heads' states, over the segments in turn, the loads of eight at once.
-constexpr int kLaCarryBatch = 8;
-static __global__ __launch_bounds__(256) void la_carry_kernel(const float* __restrict__ end, const float* __restrict__ sum,
-                                                              const int32_t* __restrict__ flag, float* __restrict__ enter,
-                                                              int64_t hs, int H, int nseg, int rev) {
+hipError_t la_launch(int E, int F, LaMode mode, bool bf16, const LaWalk& g, unsigned grid, hipStream_t stream) {
+  SSS_LA_PICK(la_run, mode, bf16, g, grid, stream);
+}
+hipError_t la_launch_folds(int E, int F, bool bf16, const LaWalk& fwd, const LaWalk& rev, unsigned n, hipStream_t stream) {
+  SSS_LA_PICK(la_run_folds, bf16, fwd, rev, n, stream);
+}
+hipError_t la_launch_grads(int E, int F, bool bf16, const LaWalk& dq, const LaWalk& dk, const LaWalk& dv, unsigned n,
+                           hipStream_t stream) {
+  SSS_LA_PICK(la_run_grads, bf16, dq, dk, dv, n, stream);
+}
+#undef SSS_LA_PICK
+
+// One thread per element of the heads' states, over the segments in turn, the loads of sixteen at once (without
+// regard to the flags, which come with them: where one is 0 nothing was written, and nothing is used).  Lanes of
+// a wave whose elements are of one head share a decay.  blockIdx.y 1: backwards.
+constexpr int kLaCarryBatch = 16;
+static __global__ __launch_bounds__(256) void la_carry_kernel(LaCarry fwd, LaCarry back, int64_t hs, int H, int nseg) {
+  const bool rev = blockIdx.y != 0;
+  const float* const end = rev ? back.end : fwd.end;
+  const float* const sum = rev ? back.sum : fwd.sum;
+  const int32_t* const flag = rev ? back.flag : fwd.flag;
+  float* const enter = rev ? back.enter : fwd.enter;
   const int64_t per = hs * H, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= per) return;
   const int h = (int)(i / hs), last = nseg - 1;  // segments 0 .. nseg - 2, or backwards nseg - 1 .. 1
-  auto seg = [&](int n) { return rev ? last - n : n; };
   float v = 0.0f;
   for (int n0 = 0; n0 < last; n0 += kLaCarryBatch) {
     float e[kLaCarryBatch], d[kLaCarryBatch];
     int fl[kLaCarryBatch];
 #pragma unroll
-    for (int q = 0; q < kLaCarryBatch; ++q) fl[q] = n0 + q < last ? flag[seg(n0 + q)] : 0;
-#pragma unroll
     for (int q = 0; q < kLaCarryBatch; ++q) {
-      e[q] = d[q] = 0.0f;
-      if (fl[q] != 0) {  // else nothing was written
-        e[q] = end[seg(n0 + q) * per + i];
-        d[q] = sum[(int64_t)seg(n0 + q) * H + h];
-      }
+      const int n = min(n0 + q, last - 1), c = rev ? last - n : n;
+      fl[q] = flag[c];
+      e[q] = end[c * per + i];
+      d[q] = sum[(int64_t)c * H + h];
     }
 #pragma unroll
     for (int q = 0; q < kLaCarryBatch; ++q) {
-      if (fl[q] == 0) continue;
+      if (n0 + q >= last || fl[q] == 0) continue;
+      const int n = n0 + q;
       v = fl[q] == 2 ? e[q] : __builtin_fmaf(fast_exp2(d[q]), v, e[q]);
-      enter[(int64_t)(rev ? seg(n0 + q) - 1 : seg(n0 + q) + 1) * per + i] = v;
+      enter[(int64_t)(rev ? last - n - 1 : n + 1) * per + i] = v;
     }
   }
 }
 
-hipError_t la_carry(const float* end, const float* sum, const int32_t* flag, float* enter, int64_t hs, int H, int nseg, bool rev,
-                    hipStream_t stream) {
-  hipLaunchKernelGGL(la_carry_kernel, dim3((unsigned)((hs * H + 255) / 256)), dim3(256), 0, stream, end, sum, flag, enter, hs, H,
-                     nseg, rev ? 1 : 0);
+hipError_t la_carry(const LaCarry& fwd, const LaCarry* rev, int64_t hs, int H, int nseg, hipStream_t stream) {
+  hipLaunchKernelGGL(la_carry_kernel, dim3((unsigned)((hs * H + 255) / 256), rev != nullptr ? 2 : 1), dim3(256), 0, stream, fwd,
+                     rev != nullptr ? *rev : fwd, hs, H, nseg);
   return hipGetLastError();
 }
 
@@ -74,7 +96,8 @@ static __global__ __launch_bounds__(64) void la_finish_kernel(LaFinish a) {
   const int lane = threadIdx.x;
   const int h = (int)(blockIdx.x % (unsigned)a.H), seg = (int)(blockIdx.x / (unsigned)a.H);
   const int c0 = seg * a.K, tend = min(c0 + a.K, a.tokens);
-  const int lo = min(max(a.cu[0], 0), a.tokens), hi = min(max(a.cu[a.nseq], 0), a.tokens);
+  const LaBounds cu(a.cu, a.nseq, lane);
+  const int lo = min(max(cu.at(0), 0), a.tokens), hi = min(max(cu.at(a.nseq), 0), a.tokens);
   const int64_t H = a.H;
   double sum = 0.0;
   auto clear = [&](int b, int e) {
@@ -88,9 +111,9 @@ static __global__ __launch_bounds__(64) void la_finish_kernel(LaFinish a) {
   const int gap = min(t, tend);
   clear(c0, gap);
   clear(max(max(stop, c0), gap), tend);
-  int s = t < stop ? min(max(__builtin_amdgcn_readfirstlane(find_seq(a.cu, a.nseq, t, lane)), 0), a.nseq - 1) : 0;
+  int s = t < stop ? cu.find(t) : 0;
   while (t < stop) {
-    const int end = min(a.cu[s + 1], hi);
+    const int end = min(cu.at(s + 1), hi);
     if (end <= t) {
       if (++s >= a.nseq) break;
       continue;
