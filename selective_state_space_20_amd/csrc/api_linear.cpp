@@ -66,13 +66,16 @@ struct Plan {
   size_t total;
 };
 
-// Segments: one round of the workgroups that the GPU holds at a time (two per CU; 32768 tokens x 16 heads of 128 x 128:
-// 271 us in 32 segments, one round, 283-296 in 16, 24 or 48), each of a tile of fp32 at least (1001 tokens x 6 heads,
-// gradients: 98 us in 32 segments, 182 in 4).
+// Segments: one round of the workgroups that the GPU holds at a time, two per CU, over the walks of the last launch
+// (forward one; gradients dq and dk, and dv where it joins them), each segment of a tile of fp32 at least.  Forward,
+// 32768 tokens x 16 heads of 128 x 128: 268 us in 32 segments, one round, 302-365 in 16 or 12.  Gradients, 8192 tokens
+// of these: 242-250 us in 10 segments, one round, 246 in 16, 272 in 32, 424 in 4; 1001 tokens x 6 heads of 64 x 50 in
+// fp32: 55 us in 32, 56 in 16, 65 in 8, 93 in 4.
 Plan plan(int64_t tokens, int64_t nseq, int64_t heads, int64_t q_heads, int64_t k_heads, int64_t dk, int64_t dv, bool grads,
           int cus) {
   Plan p{};
-  const int64_t round = std::max<int64_t>(1, (int64_t)cus * 2 / heads);
+  const int64_t walks = !grads ? 1 : pad(dk) == pad(dv) ? 3 : 2;
+  const int64_t round = std::max<int64_t>(1, (int64_t)cus * 2 / (walks * heads));
   int64_t S = std::min<int64_t>(round, (tokens + kLaTile / 2 - 1) / (kLaTile / 2));
   const int forced = env_int("SSS_FORCE_SEGMENTS", 0);
   if (forced > 0) S = std::min<int64_t>(forced, tokens);
@@ -423,10 +426,10 @@ int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_
     c.sf = 1;
     e = la_launch_grads(ev, ek, bf16, a, b, c, grid, s);
     if (e == hipSuccess && ek != ev) e = la_launch(ek, ev, kLaDv, bf16, c, grid, s);
-    if (e == hipSuccess && q_heads < heads)
-      e = la_sum_heads(at(p.dq), dq, tokens, H, (int)(heads / q_heads), (int)dk, bf16, s);
-    if (e == hipSuccess && k_heads < heads)
-      e = la_sum_heads(at(p.dk), dk_out, tokens, H, (int)(heads / k_heads), (int)dk, bf16, s);
+    const LaSum of_q{at(p.dq), dq, (int)(heads / q_heads)}, of_k{at(p.dk), dk_out, (int)(heads / k_heads)};
+    const bool sum_q = q_heads < heads, sum_k = k_heads < heads;
+    if (e == hipSuccess && (sum_q || sum_k))
+      e = la_sum_heads(sum_q ? of_q : of_k, sum_q && sum_k ? &of_k : nullptr, tokens, H, (int)dk, bf16, s);
   }
   if (e == hipSuccess) {
     LaFinish a{};

@@ -99,8 +99,13 @@ struct LaFinish {
 };
 hipError_t la_finish(const LaFinish& a, hipStream_t stream);
 
-// out (tokens, heads / rep, d) = sums of rep adjacent heads of part (tokens, heads, d)
-hipError_t la_sum_heads(const float* part, void* out, int64_t tokens, int heads, int rep, int d, bool bf16, hipStream_t stream);
+// out (tokens, heads / rep, d) = sums of rep adjacent heads of part (tokens, heads, d); of a second set, if any, too
+struct LaSum {
+  const float* part;
+  void* out;
+  int rep;
+};
+hipError_t la_sum_heads(const LaSum& a, const LaSum* b, int64_t tokens, int heads, int d, bool bf16, hipStream_t stream);
 // dinitial = dfinal (or zero) of the sequences without tokens
 hipError_t la_empty(const int32_t* cu, const float* dfinal, float* dinitial, int nseq, int tokens, int64_t per, hipStream_t stream);
 

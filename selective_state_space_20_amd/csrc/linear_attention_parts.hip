@@ -172,9 +172,12 @@ hipError_t la_finish(const LaFinish& a, hipStream_t stream) {
 }
 
 template <bool BF16>
-static __global__ __launch_bounds__(256) void la_sum_heads_kernel(const float* __restrict__ part, char* __restrict__ out, int64_t n,
-                                                                  int rep, int d) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // an element of out
+static __global__ __launch_bounds__(256) void la_sum_heads_kernel(LaSum a, LaSum b, int64_t tokens, int heads, int d) {
+  const bool second = blockIdx.y != 0;
+  const float* const part = second ? b.part : a.part;
+  char* const out = (char*)(second ? b.out : a.out);
+  const int rep = second ? b.rep : a.rep;
+  const int64_t n = tokens * (heads / rep) * d, i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // an element of out
   if (i >= n) return;
   const int64_t row = i / d;
   const float* p = part + row * rep * d + (i - row * d);
@@ -184,11 +187,12 @@ static __global__ __launch_bounds__(256) void la_sum_heads_kernel(const float* _
   else ((float*)out)[i] = s;
 }
 
-hipError_t la_sum_heads(const float* part, void* out, int64_t tokens, int heads, int rep, int d, bool bf16, hipStream_t stream) {
+hipError_t la_sum_heads(const LaSum& a, const LaSum* b, int64_t tokens, int heads, int d, bool bf16, hipStream_t stream) {
+  const int rep = b != nullptr ? std::min(a.rep, b->rep) : a.rep;
   const int64_t n = tokens * (heads / rep) * d;
-  const dim3 grid((unsigned)((n + 255) / 256));
-  if (bf16) hipLaunchKernelGGL(la_sum_heads_kernel<true>, grid, dim3(256), 0, stream, part, (char*)out, n, rep, d);
-  else hipLaunchKernelGGL(la_sum_heads_kernel<false>, grid, dim3(256), 0, stream, part, (char*)out, n, rep, d);
+  const dim3 grid((unsigned)((n + 255) / 256), b != nullptr ? 2 : 1);
+  if (bf16) hipLaunchKernelGGL(la_sum_heads_kernel<true>, grid, dim3(256), 0, stream, a, b != nullptr ? *b : a, tokens, heads, d);
+  else hipLaunchKernelGGL(la_sum_heads_kernel<false>, grid, dim3(256), 0, stream, a, b != nullptr ? *b : a, tokens, heads, d);
   return hipGetLastError();
 }
 
