@@ -41,81 +41,100 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float* lds, int& tu
 struct LNormGeo {
   int64_t sx, sr;  // elements between rows of x and of the residual
   int64_t rows;
+  int64_t step;  // forward: between the rows of a lane
   int G, groups, nblk;
   float eps, inv_g;
 };
 
 // residual may be residual_out itself: every element is read by the lane that writes it, before the sums that
 // precede the writes.
-template <bool XB, bool HB, int V, int TPR, int M>
+// R: rows of a lane, `step` apart, so that one load of weight and bias serves all of them.
+template <bool XB, bool HB, int V, int TPR, int M, int R>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void layer_norm_fwd_kernel(
     const char* __restrict__ x, const char* residual, const float* __restrict__ w, const float* __restrict__ b,
     char* __restrict__ out, char* residual_out, float* __restrict__ mean_out, float* __restrict__ rstd_out, LNormGeo g) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
   constexpr int XS = XB ? 2 : 4, HS = HB ? 2 : 4;
+  static_assert(R == 1 || RPB > 1, "no barrier between the rows of a lane");
   __shared__ float lds[2 * 16];
-  const int64_t vr = (int64_t)blockIdx.x * RPB + (RPB > 1 ? (int)(threadIdx.x / TPR) : 0);
-  if (RPB > 1 && vr >= g.rows * g.groups) return;  // all lanes of the row; no barrier where a workgroup has many
-  const int64_t row = vr / g.groups, D = (int64_t)g.G * g.groups;
-  const int c0 = (int)(vr - row * g.groups) * g.G;
+  // the division in 64 bits once for the workgroup
+  const int64_t first = (int64_t)blockIdx.x * RPB, row_first = first / g.groups;
+  const unsigned at = (unsigned)(first - row_first * g.groups) + (RPB > 1 ? threadIdx.x / TPR : 0);
+  const unsigned down = RPB > 1 ? at / (unsigned)g.groups : 0, grp = at - down * (unsigned)g.groups;
+  const int64_t row0 = row_first + down, D = (int64_t)g.G * g.groups;
+  if (RPB > 1 && row0 >= g.step) return;  // all lanes of the row; no barrier where a workgroup has many
+  const int c0 = (int)grp * g.G;
   const Pieces<V, TPR, M> pc(g.G);
-  Vec<XB, V> xr[M];
-  Vec<HB, V> hr[M];
+  Vec<XB, V> xr[R][M];
+  Vec<HB, V> hr[R][M];
   Vec<false, V> wr[M], br[M];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = R > 1 ? min(row0 + r * g.step, g.rows - 1) : row0;  // past the last: loaded, not used
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      xr[r][m].template load<true>(x + (row * g.sx + c0 + pc.at[m]) * XS);
+      if (residual != nullptr) hr[r][m].template load<true>(residual + (row * g.sr + c0 + pc.at[m]) * HS);
+    }
+  }
 #pragma unroll
   for (int m = 0; m < M; ++m) {
     if (!pc.live(m)) continue;
-    xr[m].template load<true>(x + (row * g.sx + c0 + pc.at[m]) * XS);
-    if (residual != nullptr) hr[m].template load<true>(residual + (row * g.sr + c0 + pc.at[m]) * HS);
     if (w != nullptr) wr[m].load(w + c0 + pc.at[m]);
     if (b != nullptr) br[m].load(b + c0 + pc.at[m]);
   }
-  float h[M][V], s = 0.0f;
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    if (!pc.live(m)) continue;
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      h[m][c] = xr[m].get(c);
-      if (residual != nullptr) h[m][c] += hr[m].get(c);
-      s += c < pc.skip[m] ? 0.0f : h[m][c];
-    }
-  }
   int turn = 0;
-  const float mean = row_sum<TPR>(s, lds, turn) * g.inv_g;
-  s = 0.0f;
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    if (!pc.live(m)) continue;
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = row0 + r * g.step;
+    if (R > 1 && row >= g.rows) break;
+    float h[M][V], s = 0.0f;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float d = h[m][c] - mean;
-      s += c < pc.skip[m] ? 0.0f : d * d;
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        h[m][c] = xr[r][m].get(c);
+        if (residual != nullptr) h[m][c] += hr[r][m].get(c);
+        s += c < pc.skip[m] ? 0.0f : h[m][c];
+      }
     }
-  }
-  const float rstd = __builtin_amdgcn_rsqf(row_sum<TPR>(s, lds, turn) * g.inv_g + g.eps);
-  if ((threadIdx.x & (TPR - 1)) == 0) {
-    if (mean_out != nullptr) mean_out[vr] = mean;
-    if (rstd_out != nullptr) rstd_out[vr] = rstd;
-  }
+    const float mean = row_sum<TPR>(s, lds, turn) * g.inv_g;
+    s = 0.0f;
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    if (!pc.live(m)) continue;
-    if (residual_out != nullptr) {
-      Vec<HB, V> r;
-      r.set(h[m]);
-      r.template store_from<false>(residual_out + (row * D + c0 + pc.at[m]) * HS, pc.skip[m]);
-    }
-    float o[V];
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {  // of h before it is rounded
-      o[c] = (h[m][c] - mean) * rstd;
-      if (w != nullptr) o[c] *= wr[m].get(c);
-      if (b != nullptr) o[c] += br[m].get(c);
+      for (int c = 0; c < V; ++c) {
+        const float d = h[m][c] - mean;
+        s += c < pc.skip[m] ? 0.0f : d * d;
+      }
     }
-    Vec<XB, V> r;
-    r.set(o);
-    r.template store_from<true>(out + (row * D + c0 + pc.at[m]) * XS, pc.skip[m]);
+    const float rstd = __builtin_amdgcn_rsqf(row_sum<TPR>(s, lds, turn) * g.inv_g + g.eps);
+    if ((threadIdx.x & (TPR - 1)) == 0) {
+      if (mean_out != nullptr) mean_out[row * g.groups + grp] = mean;
+      if (rstd_out != nullptr) rstd_out[row * g.groups + grp] = rstd;
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (!pc.live(m)) continue;
+      if (residual_out != nullptr) {
+        Vec<HB, V> v;
+        v.set(h[m]);
+        v.template store_from<false>(residual_out + (row * D + c0 + pc.at[m]) * HS, pc.skip[m]);
+      }
+      float o[V];
+#pragma unroll
+      for (int c = 0; c < V; ++c) {  // of h before it is rounded
+        o[c] = (h[m][c] - mean) * rstd;
+        if (w != nullptr) o[c] *= wr[m].get(c);
+        if (b != nullptr) o[c] += br[m].get(c);
+      }
+      Vec<XB, V> v;
+      v.set(o);
+      v.template store_from<true>(out + (row * D + c0 + pc.at[m]) * XS, pc.skip[m]);
+    }
   }
 }
 
@@ -213,18 +232,31 @@ static LNormGeo layer_geo(const LayerNormArgs& a) {
   return g;
 }
 
+// Where a row's lanes are a part of a wave, four rows per lane, from 512 workgroups of them on: weight and bias are twice
+// the bytes of a bf16 x each, and came from the caches once per element.  bf16 in groups of 64: 16384 x 5120
+// 82 -> 64 us (5.3 TB/s), 1024 x 5120 (640 workgroups) 7.3 -> 6.4, but 256 x 5120 (160) 2.9 -> 3.9; 250 x 40 of 8192
+// rows 95 -> 76; groups of 128, 4096 x 16 (1024 workgroups) 9.1 -> 8.6, 1024 x 16 (256) 3.6 -> 4.4.
+constexpr int layer_rows(int tpr) { return tpr < 64 ? 4 : 1; }
+
 template <bool XB, bool HB>
 static hipError_t layer_fwd(const LayerNormArgs& a, hipStream_t stream) {
-  const LNormGeo g = layer_geo(a);
+  LNormGeo g = layer_geo(a);
   const NormShape sh = norm_shape(a.group, !XB || !HB);
-  const int64_t vrows = a.rows * a.groups;
-#define CALL(V, TPR, M)                                                                                        \
-  hipLaunchKernelGGL((layer_norm_fwd_kernel<XB, HB, V, TPR, M>),                                               \
-                     dim3((unsigned)((vrows + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1))), \
-                     dim3(TPR < 256 ? 256 : TPR), 0, stream, (const char*)a.x, (const char*)a.residual, a.w, a.b, \
-                     (char*)a.out, (char*)a.residual_out, a.mean, a.rstd, g)
+  const int64_t rpb = sh.tpr < 256 ? 256 / sh.tpr : 1;
+  const int64_t R = layer_rows(sh.tpr);
+  const bool many = R > 1 && a.rows * a.groups >= R * rpb * 512;
+  g.step = many ? (a.rows + R - 1) / R : a.rows;
+  const dim3 grid((unsigned)((g.step * a.groups + rpb - 1) / rpb));
+#define CALL_R(V, TPR, M, R)                                                                                       \
+  hipLaunchKernelGGL((layer_norm_fwd_kernel<XB, HB, V, TPR, M, R>), grid, dim3(TPR < 256 ? 256 : TPR), 0, stream,  \
+                     (const char*)a.x, (const char*)a.residual, a.w, a.b, (char*)a.out, (char*)a.residual_out, a.mean, \
+                     a.rstd, g)
+#define CALL(V, TPR, M)                                \
+  if (many) CALL_R(V, TPR, M, layer_rows(TPR));        \
+  else CALL_R(V, TPR, M, 1)
   SSS_NORM_SHAPES(CALL, !XB || !HB);
 #undef CALL
+#undef CALL_R
   return hipGetLastError();
 }
 

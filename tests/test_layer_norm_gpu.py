@@ -159,3 +159,23 @@ def test_rows_apart_and_none():
     out, mean, rstd = sss.layer_norm_fwd(none, return_stats=True)
     g = sss.layer_norm_bwd(none, none, torch.ones(64, device=DEV), mean=mean, rstd=rstd, bias=True)
     assert out.shape == (0, 64) and bool((g["dweight"] == 0).all()) and bool((g["dbias"] == 0).all())
+
+
+@pytest.mark.parametrize("types", ["fp32", "bf16", "bf16 stream fp32"])
+@pytest.mark.parametrize("rows, group, groups", [(3279, 20, 40), (3277, 64, 40), (4099, 100, 16), (4097, 250, 8), (32769, 130, 1)])
+def test_many_rows_of_small_groups(rows, group, groups, types):
+    """Where a lane takes four rows: none is left out, also where four does not divide them."""
+    import torch
+    import selective_state_space_20_amd as sss
+    dt = torch.float32 if types == "fp32" else torch.bfloat16
+    dim = group * groups
+    x = rnd(1, rows, dim + 8, dtype=dt, shift=1.0)[:, :dim]
+    res = rnd(2, rows, dim) if "stream" in types else None
+    w, b = rnd(3, dim), rnd(4, dim)
+    xd, rd = x.to(DEV), None if res is None else res.to(DEV)
+    if dim % 8 == 0:
+        xd = torch.empty(rows, dim + 8, dtype=dt, device=DEV)[:, :dim].copy_(x)
+    got = sss.layer_norm_fwd(xd, w.to(DEV), b.to(DEV), rd, residual_out=rd, group_size=group, return_stats=True)
+    ref = reference(x, res, w, b, 1e-5, groups)
+    for n, t in zip(("out", "mean", "rstd") if res is None else ("out", "h", "mean", "rstd"), got):
+        check(t, ref, n)
