@@ -63,8 +63,8 @@
  *  - The library allocates no device memory and keeps no state between calls other
  *    than a per-device cache of the compute-unit count.  Calls are thread-safe.
  *  - Environment: SSS_FORCE_SEGMENTS=<S> forces the number of time segments (the
- *    two-pass split; of the packed scan the chunks, of the convolution's gradients the
- *    segments) for testing; SSS_LOG=1 prints the chosen launch plan to stderr;
+ *    two-pass split; of the packed scan the chunks, of the convolution's gradients and of linear
+ *    attention the segments) for testing; SSS_LOG=1 prints the chosen launch plan to stderr;
  *    SSS_WAVES_PER_SIMD / SSS_CONV_WAVES_PER_CU override the occupancy targets the
  *    selective-scan and convolution plans aim at, SSS_EW_CPL (1, 2 or 4) the channels per
  *    lane of the elementwise scan (tuning only).  SSS_CHUNKED=1 runs the plain time-major

@@ -22,9 +22,26 @@
 // segment and head.  The state that enters a segment comes from a first pass (kLaFold*: the update of M
 // alone, for the one sequence that runs across the segment's edge) and a sum over the segments.
 //
-// Sums, decays (64-bit) and M are fp32 or more.  What is rounded to bf16 on the way to a bf16 result:
-// scores and M.  What goes into fp32 results (the states, and the parts of dg, db that come from other
-// tiles) takes M and the weighted z as the sum of two or three bf16 parts, 16 or 24 bits of them.
+// Sums, decays (64-bit) and M are fp32 or more.  What is rounded to bf16 on the way to a bf16 result: the
+// scores, and M as an operand of the outputs and of dv.  What goes into fp32 results (the states, and the parts of
+// dg, db that come from other tiles) takes M and the weighted z as the sum of three bf16 parts, 24 bits of them;
+// dv's walk, whose only result is bf16, takes the weighted z as two.  Two parts in dq and dk would save 4%
+// (301 -> 289 us below) and leave 6e-6 of dg's norm instead of 3e-7.
+//
+// What bounds it.  The bytes are few (16384 tokens x 80 heads of 128 x 64: 449 MB, 85 us at a copy's rate) and so is
+// the arithmetic (0.1 TFLOP with the extra parts, 75 us at a large product's rate); what is left is the chain of a
+// tile: loads to LDS, barrier, scores, barrier, the products that need them and M, with two workgroups of four waves
+// per CU (LDS and the registers of M) to fill each other's gaps.  So a tile is as long as LDS allows, its loads are
+// in flight during the tile before, without branches, the scores' triangle is shared evenly by the waves, and the
+// segments are one round of workgroups: a second would pay another fold and carry.
+//   16384 x 80 x 128 x 64, q and k shared, prompts   335 us (fold 45, carry 9, walk 285)
+//   32768 x 16 x 128 x 128, prompts                  258 us (fold 73, carry 12, walk 165: 3.4 TB/s)
+//   8192 x 16 x 128 x 128, gradients                 247 us (folds 55, carry 11, dq dk dv 177); in launches of
+//                                                    their own, each a round of workgroups, 298
+//   1001 x 6 x 64 x 50 fp32, gradients                56 us (folds 9, carry 5, dq dk dv 27, sums 15); apart 96
+// Measured and no better: eight waves for 128 columns, swizzled rows instead of padded ones, rows without any bank
+// conflict (half of them gone, the same time), three smaller workgroups per CU, scores dealt tile by tile to the
+// waves, two heads per workgroup where they share q and k, nontemporal loads.
 #include "linear_attention.h"
 
 #include "seq_walk.h"

@@ -278,3 +278,14 @@ def test_offsets_past_32_bits():
     g = sss.layer_norm_bwd(x, x, w, mean=mean, rstd=rstd)
     g3 = sss.layer_norm_bwd(x[-3:].clone(), x[-3:].clone(), w, mean=m3, rstd=r3)
     assert torch.equal(g["dx"][-3:], g3["dx"])
+
+
+@pytest.mark.parametrize("sequences", [62, 63, 64, 65, 130])
+@pytest.mark.parametrize("segments", [None, 7])
+def test_many_sequences(sequences, segments, monkeypatch):
+    """As many boundaries and slots as a wave has lanes, fewer and more."""
+    from . import test_linear_attention_gpu as base
+    monkeypatch.setitem(base.LENGTHS, "many", [(5 * i) % 9 for i in range(sequences)])
+    for bf16 in (False, True):
+        base.check_prompts((2, 1, 1, 48, 36), bf16, segments, "many", "gate", monkeypatch)
+        base.check_gradients((2, 1, 1, 48, 36), bf16, segments, "many", "gate", True, monkeypatch)
