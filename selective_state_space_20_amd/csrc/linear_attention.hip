@@ -428,19 +428,24 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
     LaLoad<BF16, C, F, NT> rz, rw;
     float rg = 0.0f, rb = 0.0f;
     const int ntile = (e - a + C - 1) / C;
-    auto fetch = [&](int tid, int m) __attribute__((always_inline)) {
+    // Parts: 1, the decays and x; 2, y; 4, z and w.  Asked for at three points of the tile before, so that none of them
+    // waits for room among the loads in flight: at one point, 349 us in place of 343 for prompts of 16384 x 80 x 128 x 64,
+    // 248 in place of 239 for the gradients of 8192 x 16 x 128 x 128.
+    auto fetch = [&](int tid, int m, int part) __attribute__((always_inline)) {
       const int lane = tid & 63;
       const int t = a + m * C, nr = min(C, e - t);
       // first, so that waiting for them does not wait for the tiles: vector loads return in order
       const int r = t + min(lane, nr - 1);
-      rg = gp[r * g.g_st];
-      rb = bp != nullptr ? bp[r * g.beta_st] : 1.0f;
-      if constexpr (kOut) rx.load(tid, xp, t, g.x.st, nr, Ew);
-      ry.load(tid, yp, t, g.y.st, nr, Ew);
-      rz.load(tid, zp, t, g.z.st, nr, Fw);
-      if constexpr (kDots) rw.load(tid, wp, t, g.w.st, nr, Fw);
+      if (part & 1) {
+        rg = gp[r * g.g_st];
+        rb = bp != nullptr ? bp[r * g.beta_st] : 1.0f;
+      }
+      if (kOut && (part & 1)) rx.load(tid, xp, t, g.x.st, nr, Ew);
+      if (part & 2) ry.load(tid, yp, t, g.y.st, nr, Ew);
+      if (part & 4) rz.load(tid, zp, t, g.z.st, nr, Fw);
+      if (kDots && (part & 4)) rw.load(tid, wp, t, g.w.st, nr, Fw);
     };
-    fetch((int)threadIdx.x, kRev ? ntile - 1 : 0);
+    fetch((int)threadIdx.x, kRev ? ntile - 1 : 0, 7);
     for (int k = 0; k < ntile; ++k) {
       const int m = kRev ? ntile - 1 - k : k;
       const int t0 = a + m * C, nr = min(C, e - t0);
@@ -470,7 +475,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
       }
       if constexpr (kDots) rw.store(tid, lw, wp, t0, g.w.st, nr, Fw);
       la_barrier();
-      if (k + 1 < ntile) fetch(tid, kRev ? m - 1 : m + 1);
+      if (k + 1 < ntile) fetch(tid, kRev ? m - 1 : m + 1, kOut ? 1 : 7);
       if constexpr (MODE == kLaDq) {
         if (k + 1 == ntile) {
           through = 0.0f;
@@ -555,6 +560,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
             }
           }
         }
+        if (k + 1 < ntile) fetch(tid, kRev ? m - 1 : m + 1, 2);
         // x M, transposed: the lane has row i of the tokens, columns f + r
         la_f4 o[TI][NF];
 #pragma unroll
@@ -602,6 +608,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
             if (l4 == 0) lrr[wave * C + 16 * t + l16] = dot;
           }
         }
+        if (k + 1 < ntile) fetch(tid, kRev ? m - 1 : m + 1, 4);
         take_z();
         if (threadIdx.x == 0) lwild[turn ^ 1] = 0;  // last read before this tile
         la_barrier();  // the scores are there
