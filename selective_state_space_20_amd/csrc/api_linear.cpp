@@ -69,7 +69,7 @@ struct Plan {
 // Segments: one round of the workgroups that the GPU holds at a time, two per CU, over the walks of the last launch
 // (forward one; gradients dq and dk, and dv where it joins them), each segment of a tile of fp32 at least.  Forward,
 // 32768 tokens x 16 heads of 128 x 128: 268 us in 32 segments, one round, 302-365 in 16 or 12.  Gradients, 8192 tokens
-// of these: 242-250 us in 10 segments, one round, 246 in 16, 272 in 32, 424 in 4; 1001 tokens x 6 heads of 64 x 50 in
+// of these: 236-250 us in 10 segments, one round, 246 in 16, 272 in 32, 424 in 4; 1001 tokens x 6 heads of 64 x 50 in
 // fp32: 55 us in 32, 56 in 16, 65 in 8, 93 in 4.
 Plan plan(int64_t tokens, int64_t nseq, int64_t heads, int64_t q_heads, int64_t k_heads, int64_t dk, int64_t dv, bool grads,
           int cus) {

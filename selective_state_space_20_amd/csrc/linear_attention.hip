@@ -26,7 +26,7 @@
 // scores, and M as an operand of the outputs and of dv.  What goes into fp32 results (the states, and the parts of
 // dg, db that come from other tiles) takes M and the weighted z as the sum of three bf16 parts, 24 bits of them;
 // dv's walk, whose only result is bf16, takes the weighted z as two.  Two parts in dq and dk would save 4%
-// (301 -> 289 us below) and leave 6e-6 of dg's norm instead of 3e-7.
+// (301 -> 289 us of the gradients below, as they were) and leave 6e-6 of dg's norm instead of 3e-7.
 //
 // What bounds it.  The bytes are few (16384 tokens x 80 heads of 128 x 64: 449 MB, 85 us at a copy's rate) and so is
 // the arithmetic (0.1 TFLOP with the extra parts, 75 us at a large product's rate); what is left is the chain of a
@@ -34,11 +34,11 @@
 // per CU (LDS and the registers of M) to fill each other's gaps.  So a tile is as long as LDS allows, its loads are
 // in flight during the tile before, without branches, the scores' triangle is shared evenly by the waves, and the
 // segments are one round of workgroups: a second would pay another fold and carry.
-//   16384 x 80 x 128 x 64, q and k shared, prompts   335 us (fold 45, carry 9, walk 285)
-//   32768 x 16 x 128 x 128, prompts                  258 us (fold 73, carry 12, walk 165: 3.4 TB/s)
-//   8192 x 16 x 128 x 128, gradients                 247 us (folds 55, carry 11, dq dk dv 177); in launches of
+//   16384 x 80 x 128 x 64, q and k shared, prompts   335 us (fold 43, carry 11, walk 280-290)
+//   32768 x 16 x 128 x 128, prompts                  256 us (fold 76, carry 15, walk 165: 3.3 TB/s)
+//   8192 x 16 x 128 x 128, gradients                 236 us (folds 54, carry 11, dq dk dv 163); in launches of
 //                                                    their own, each a round of workgroups, 298
-//   1001 x 6 x 64 x 50 fp32, gradients                56 us (folds 9, carry 5, dq dk dv 27, sums 15); apart 96
+//   1001 x 6 x 64 x 50 fp32, gradients                55 us (folds 9, carry 5, dq dk dv 28, sums 12); apart 96
 // Measured and no better: eight waves for 128 columns, swizzled rows instead of padded ones, rows without any bank
 // conflict (half of them gone, the same time), three smaller workgroups per CU, scores dealt tile by tile to the
 // waves, two heads per workgroup where they share q and k, nontemporal loads.
