@@ -440,8 +440,13 @@ int layer_norm_bwd(const void* dout, const void* dresidual_out, const void* x, i
  * (SSS_ERR_UNSUPPORTED otherwise), heads up to 65536.  Packed prompts, cache slots, alignment and
  * overlap as above.  Results are deterministic.
  *
+ * Log decays are meant to be zero or less.  Larger ones are taken as they are, and states that grow past
+ * float32 become infinities or no numbers, at the latest where those of 64 tokens add up to 88.
+ *
  * A value that is not finite reaches the results that it is a part of, as an infinity or as no number,
- * and no others: nothing of tokens before it, of other sequences or heads. */
+ * and no others: nothing of tokens before it, of other sequences or heads.  Two exceptions among the
+ * gradients: dlog_decay is formed from sums over a sequence, and may have it for every token of its
+ * sequence and head; and of a log decay that is no number or +inf, those of up to 63 tokens behind it. */
 
 /* Bytes of workspace linear_attention_packed_fwd needs on `device` (0 on invalid sizes, and where
  * none is needed); it does not depend on the sequences. */
