@@ -64,7 +64,8 @@ def _run(cmd):
 def build(verbose: bool = False, jobs: int = 0) -> str:
     os.makedirs(OBJ, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    work = compile_jobs()
+    # the scan's kernels first: those of 64 states take minutes, all others together little more
+    work = sorted(compile_jobs(), key=lambda job: "selective_scan" not in job[0])
     cmds = [["hipcc", *FLAGS, *extra, *inc, "-c", src, "-o", obj] for obj, extra, src in work]
     workers = jobs or max(1, min(len(cmds), os.cpu_count() or 1, 16))
     probe_cmd = ["hipcc", *FLAGS, "-shared", PROBE_SRC, "-o", PROBE_LIB + ".tmp"]
