@@ -66,16 +66,20 @@ struct Plan {
   size_t total;
 };
 
-// Segments: one round of the workgroups that the GPU holds at a time, two per CU, over the walks of the last launch
-// (forward one; gradients dq and dk, and dv where it joins them), each segment of a tile of fp32 at least.  Forward,
-// 32768 tokens x 16 heads of 128 x 128: 268 us in 32 segments, one round, 302-365 in 16 or 12.  Gradients, 8192 tokens
-// of these: 236-250 us in 10 segments, one round, 246 in 16, 272 in 32, 424 in 4; 1001 tokens x 6 heads of 64 x 50 in
-// fp32: 55 us in 32, 56 in 16, 65 in 8, 93 in 4.
+// Segments: one round of the workgroups that the GPU holds at a time, two per CU, one where a side of the states is above
+// 128 (LDS); of the gradients' walks one round of dq and dk, and dv, where it is in their launch, follows into the places
+// that dk leaves, half as long.  Each segment is of a tile of fp32 at least.  Measured, 8192 tokens where not said,
+// prompts: 32768 x 16 heads of 128 x 128 268 us in 32 segments, one round, 302-365 in 16 or 12; 8 heads of
+// 256 x 256 132 in 32, 157 in 16, 209 in 64; 8 of 128 x 256 78, 103 and 105.  Gradients: 16 heads of 64 x 64 94 us in 16,
+// 134 in 10, 114 in 21, 97 in 32; 16 of 128 x 128 241 in 16 as in 10, 272 in 32, 424 in 4; 16 of 128 x 64 182 in 16,
+// 259 in 10, 235 in 21; 8 of 128 x 256 241 in 16, 364 in 10, 253 in 32; 8 of 256 x 256 437 in 16, 550 in 10, 526 in
+// 32; 1001 tokens x 6 heads of 64 x 50 in fp32 55 us in 32, 56 in 16, 65 in 8, 93 in 4.  The other way: 8 fp32 heads of
+// 128 x 128 284 in 32, 276 in 21.
 Plan plan(int64_t tokens, int64_t nseq, int64_t heads, int64_t q_heads, int64_t k_heads, int64_t dk, int64_t dv, bool grads,
           int cus) {
   Plan p{};
-  const int64_t walks = !grads ? 1 : pad(dk) == pad(dv) ? 3 : 2;
-  const int64_t round = std::max<int64_t>(1, (int64_t)cus * 2 / (walks * heads));
+  const int64_t walks = grads ? 2 : 1, per_cu = std::max(dk, dv) > 128 ? 1 : 2;
+  const int64_t round = std::max<int64_t>(1, cus * per_cu / (walks * heads));
   int64_t S = std::min<int64_t>(round, (tokens + kLaTile / 2 - 1) / (kLaTile / 2));
   const int forced = env_int("SSS_FORCE_SEGMENTS", 0);
   if (forced > 0) S = std::min<int64_t>(forced, tokens);
