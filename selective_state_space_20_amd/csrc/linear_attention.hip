@@ -36,9 +36,9 @@
 // segments are one round of workgroups: a second would pay another fold and carry.
 //   16384 x 80 x 128 x 64, q and k shared, prompts   335 us (fold 43, carry 11, walk 280-290)
 //   32768 x 16 x 128 x 128, prompts                  256 us (fold 76, carry 15, walk 165: 3.3 TB/s)
-//   8192 x 16 x 128 x 128, gradients                 236 us (folds 54, carry 11, dq dk dv 163); in launches of
+//   8192 x 16 x 128 x 128, gradients                 234 us (folds 45, carry 14, dq dk dv 177); in launches of
 //                                                    their own, each a round of workgroups, 298
-//   1001 x 6 x 64 x 50 fp32, gradients                55 us (folds 9, carry 5, dq dk dv 28, sums 12); apart 96
+//   1001 x 6 x 64 x 50 fp32, gradients                55 us (folds 9, carry 8, dq dk dv 24, sums 11); apart 96
 // Measured and no better: eight waves for 128 columns, swizzled rows instead of padded ones, rows without any bank
 // conflict (half of them gone, the same time), three smaller workgroups per CU, scores dealt tile by tile to the
 // waves, two heads per workgroup where they share q and k, nontemporal loads.

@@ -48,8 +48,8 @@ hipError_t la_launch_grads(int E, int F, bool bf16, const LaWalk& dq, const LaWa
 // One thread per element of the heads' states, over the segments in turn, the loads of sixteen at once (without
 // regard to the flags, which come with them: where one is 0 nothing was written, and nothing is used).  Lanes of
 // a wave whose elements are of one head share a decay.  blockIdx.y 1: backwards.  Bound by latency, a trip to
-// memory per sixteen segments: both directions of 10 segments x 16 heads x 128 x 128 take 11 us (31 MB), of 16 segments
-// x 6 x 64 x 50 5 us; with eight loads at once and a launch for each direction they took 34 (32 segments) and 20.
+// memory per sixteen segments: both directions of 16 segments x 16 heads x 128 x 128 take 14 us (63 MB), of 32 segments
+// x 6 x 64 x 50 8 us; with eight loads at once and a launch for each direction 34 (32 segments) and 20.
 constexpr int kLaCarryBatch = 16;
 static __global__ __launch_bounds__(256) void la_carry_kernel(LaCarry fwd, LaCarry back, int64_t hs, int H, int nseg) {
   const bool rev = blockIdx.y != 0;
@@ -94,7 +94,7 @@ hipError_t la_carry(const LaCarry& fwd, const LaCarry* rev, int64_t hs, int H, i
 // segment's part of a sequence starts that sum with a `through` of its own, formed without a difference.  (Whole dq
 // and dk would do as well, but roundings of pairs that cancel would be carried over the segment: 3e-5 of dg's norm in
 // place of 3e-7.)  A wave per segment and head; the sums are 64-bit.  Bound by the latency of a wave's tiles in turn:
-// 8192 tokens x 16 heads in 10 segments 14 us, 1001 x 6 5 us.
+// 8192 tokens x 16 heads in 16 segments 11 us, 1001 x 6 in 32 4 us.
 static __global__ __launch_bounds__(64) void la_finish_kernel(LaFinish a) {
   const int lane = threadIdx.x;
   const int h = (int)(blockIdx.x % (unsigned)a.H), seg = (int)(blockIdx.x / (unsigned)a.H);
