@@ -34,8 +34,8 @@
 // per CU (LDS and the registers of M) to fill each other's gaps.  So a tile is as long as LDS allows, its loads are
 // in flight during the tile before, without branches, the scores' triangle is shared evenly by the waves, and the
 // segments are one round of workgroups: a second would pay another fold and carry.
-//   16384 x 80 x 128 x 64, q and k shared, prompts   335 us (fold 43, carry 11, walk 280-290)
-//   32768 x 16 x 128 x 128, prompts                  256 us (fold 76, carry 15, walk 165: 3.3 TB/s)
+//   16384 x 80 x 128 x 64, q and k shared, prompts   332 us (fold 43, carry 11, walk 275-285)
+//   32768 x 16 x 128 x 128, prompts                  254 us (fold 76, carry 15, walk 160: 3.4 TB/s)
 //   8192 x 16 x 128 x 128, gradients                 234 us (folds 45, carry 14, dq dk dv 177); in launches of
 //                                                    their own, each a round of workgroups, 298
 //   1001 x 6 x 64 x 50 fp32, gradients                55 us (folds 9, carry 8, dq dk dv 24, sums 11); apart 96
@@ -454,6 +454,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
       int tid = (int)threadIdx.x, wave = wave_id;
       asm volatile("" : "+v"(tid), "+s"(wave));
       const int lane = tid & 63, l16 = tid & 15, l4 = lane >> 4, f0 = wave * (16 * NF);
+      if constexpr (MODE == kLaFwd) __builtin_amdgcn_s_setprio(0);
       la_barrier();  // the tile before has been read
       const bool alive = lane < nr;
       const double x = la_prefix(la_log2_decay(alive ? rg : 0.0f)), tot = la_lane(x, 63);
@@ -561,6 +562,9 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
           }
         }
         if (k + 1 < ntile) fetch(tid, kRev ? m - 1 : m + 1, 2);
+        // The outputs' products before what the CU's other workgroup does between them (16384 x 80 x 128 x 64 339 -> 332 us;
+        // the gradients, whose three walks share the GPU, were 3% slower with it).
+        if constexpr (MODE == kLaFwd) __builtin_amdgcn_s_setprio(1);
         // x M, transposed: the lane has row i of the tokens, columns f + r
         la_f4 o[TI][NF];
 #pragma unroll
