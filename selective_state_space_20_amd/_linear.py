@@ -8,14 +8,20 @@ from ._block import _cache, _code, _dense, _keep, _library, _new, _out, _refuse,
 from ._lib import SSSError, load
 
 
-def _heads(t, name, dtype, rows, heads, dim, index):
+def _three_d(t, name):
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be (tokens, heads, head size), got shape {tuple(shape)}")
+    return shape
+
+
+# Each attribute of a tensor is asked for once: the step on small batches is as long as its call.
+def _heads(t, name, shape, dtype, rows, heads, dim, index):
     """Checks a (rows, heads, dim) tensor, tokens and heads of any stride; returns (pointer, strides, heads)."""
-    if t.ndim != 3:
-        raise ValueError(f"{name} must be (tokens, heads, head size), got shape {tuple(t.shape)}")
-    n = t.shape[1]
+    r, n, d = shape
     if n < 1 or heads % n != 0:
         raise ValueError(f"{name}: its {n} heads must divide the call's {heads}")
-    if t.dtype is not dtype or t.shape != (rows, n, dim) or t.get_device() != index or index < 0:
+    if r != rows or d != dim or t.dtype is not dtype or t.get_device() != index or index < 0:
         _refuse(t, name, dtype, (rows, n, dim), index)
     st, sh, s1 = t.stride()
     if s1 != 1 and dim != 1:
@@ -27,24 +33,23 @@ def _heads(t, name, dtype, rows, heads, dim, index):
 def _operands(q, k, v, log_decay, beta, D, scale):
     """The checked operands as the leading arguments of the C calls, and the sizes."""
     torch = torch_()
-    gpu = v.get_device()
-    if v.ndim != 3:
-        raise ValueError(f"v must be (tokens, heads, head size), got shape {tuple(v.shape)}")
-    rows, heads, dv = v.shape
-    code = _code(v.dtype, "v")
+    f32, gpu, dtype = torch.float32, v.get_device(), v.dtype
+    of_v = _three_d(v, "v")
+    rows, heads, dv = of_v
+    code = _code(dtype, "v")
     if heads < 1 or dv < 1:
-        raise ValueError(f"v must have heads and elements, got shape {tuple(v.shape)}")
-    if q.ndim != 3:
-        raise ValueError(f"q must be (tokens, heads, head size), got shape {tuple(q.shape)}")
-    dk = q.shape[2]
-    qp, kp = (_heads(t, n, v.dtype, rows, heads, dk, gpu) for t, n in ((q, "q"), (k, "k")))
-    vp = _heads(v, "v", v.dtype, rows, heads, dv, gpu)[:3]
+        raise ValueError(f"v must have heads and elements, got shape {tuple(of_v)}")
+    of_q = _three_d(q, "q")
+    dk = of_q[2]
+    qp = _heads(q, "q", of_q, dtype, rows, heads, dk, gpu)
+    kp = _heads(k, "k", _three_d(k, "k"), dtype, rows, heads, dk, gpu)
+    vp = _heads(v, "v", of_v, dtype, rows, heads, dv, gpu)[:3]
     if log_decay.ndim == 1:  # one for each head
-        gp, gs = _dense(log_decay, "log_decay", torch.float32, (heads,), gpu), 0
+        gp, gs = _dense(log_decay, "log_decay", f32, (heads,), gpu), 0
     else:
-        gp, gs = _rows(log_decay, "log_decay", torch.float32, rows, heads, gpu)
-    bp, bs = _rows(beta, "beta", torch.float32, rows, heads, gpu) if beta is not None else (0, 0)
-    Dp = _dense(D, "D", torch.float32, (heads,), gpu)
+        gp, gs = _rows(log_decay, "log_decay", f32, rows, heads, gpu)
+    bp, bs = _rows(beta, "beta", f32, rows, heads, gpu) if beta is not None else (0, 0)
+    Dp = _dense(D, "D", f32, (heads,), gpu)
     return (*qp, *kp, *vp, gp, gs, bp, bs, Dp, float(scale)), rows, heads, qp[3], kp[3], dk, dv, code, gpu
 
 
