@@ -14,18 +14,19 @@
 //   dq       forwards     do  v   k    S^T
 //   dk       backwards    v   do  q    R^T  (j >= i, and e^(G_C - G_i), e^(G_j) for the two weights)
 //   dv       backwards    k   q   do   R
-// The scores of a tile go through LDS once (bf16: rounded to bf16 there, an operand like the
-// others); M never leaves the registers of the wave that has its columns: a wave's accumulators of two
-// 16-row tiles are, rounded, the operand of 32 rows of the next product as they lie.
+// The scores of a tile go through LDS once; M never leaves the registers of the wave that has its columns: a wave's
+// accumulators of two 16-row tiles are, in parts, the operand of 32 rows of the next product as they lie.
 //
 // The packed axis is cut in segments of K tokens, whatever the sequences; a workgroup takes one
 // segment and head.  The state that enters a segment comes from a first pass (kLaFold*: the update of M
 // alone, for the one sequence that runs across the segment's edge) and a sum over the segments.
 //
-// Sums, decays (64-bit) and M are fp32 or more.  What is rounded to bf16 on the way to a bf16 result: the
-// scores, and M as an operand of the outputs and of dv.  What goes into fp32 results (the states, and the parts of
-// dg, db that come from other tiles) takes M and the weighted z as the sum of three bf16 parts, 24 bits of them;
-// dv's walk, whose only result is bf16, takes the weighted z as two.  Two parts in dq and dk would save 4%
+// Sums, decays (64-bit) and M are fp32 or more, and no operand that is formed here is rounded to one bf16.  What ends in
+// bf16 results takes the scores and M (the outputs, dv), and dv's walk the weighted z, as the sum of two bf16 parts: 16
+// bits, so that a bf16 result is a value in fp32 precision, rounded once.  (One part each left 0.0024 of the results' norm
+// in place of the rounding's own 0.0017; prompts of 16384 x 80 x 128 x 64 took 325 us, of 32768 x 16 x 128 x 128 245, the
+// gradients below 229.)  What goes into fp32 results (the states, and the parts of dg, db that come from other tiles)
+// takes M and the weighted z as the sum of three, 24 bits of them.  Two parts in dq and dk would save 4%
 // (301 -> 289 us of the gradients below, as they were) and leave 6e-6 of dg's norm instead of 3e-7.
 //
 // What bounds it.  The bytes are few (16384 tokens x 80 heads of 128 x 64: 449 MB, 85 us at a copy's rate) and so is
@@ -34,9 +35,9 @@
 // per CU (LDS and the registers of M) to fill each other's gaps.  So a tile is as long as LDS allows, its loads are
 // in flight during the tile before, without branches, the scores' triangle is shared evenly by the waves, and the
 // segments are one round of workgroups: a second would pay another fold and carry.
-//   16384 x 80 x 128 x 64, q and k shared, prompts   332 us (fold 43, carry 11, walk 275-285)
-//   32768 x 16 x 128 x 128, prompts                  254 us (fold 76, carry 15, walk 160: 3.4 TB/s)
-//   8192 x 16 x 128 x 128, gradients                 234 us (folds 45, carry 14, dq dk dv 177); in launches of
+//   16384 x 80 x 128 x 64, q and k shared, prompts   353 us (of it the fold 43, carry 11)
+//   32768 x 16 x 128 x 128, prompts                  259 us (of it the fold 76, carry 15)
+//   8192 x 16 x 128 x 128, gradients                 234 us (of it the folds 45, carry 14); in launches of
 //                                                    their own, each a round of workgroups, 298
 //   1001 x 6 x 64 x 50 fp32, gradients                55 us (folds 9, carry 8, dq dk dv 24, sums 11); apart 96
 // Measured and no better: eight waves for 128 columns, swizzled rows instead of padded ones, rows without any bank
@@ -171,6 +172,62 @@ struct LaTile {
   }
 };
 
+// A tile's scores in LDS: the 16 x 16 tiles on and below the diagonal (REV: above) and no others, bf16 as the sum of two
+// parts.  A tile is pieces of 16 bytes of a row, the same piece of its 16 rows side by side, so that 16 lanes meet 256
+// adjacent bytes.  (Rows as long as the tile, padded, took 9216 bytes for one part of 64 tokens: with two, a CU would
+// hold one workgroup of the gradients in place of two.  This takes 10240 for both.)
+template <bool BF16, int C, bool REV>
+struct LaScores {
+  static constexpr int ES = BF16 ? 2 : 4, VE = 16 / ES, PARTS = BF16 ? 2 : 1, TI = C / 16, TILE = 256 * ES;
+  static constexpr int PART = TI * (TI + 1) / 2 * TILE, kBytes = PARTS * PART;
+  static __device__ __forceinline__ int tile(int it, int jt) {
+    const int big = REV ? TI - 1 - it : it, small = REV ? TI - 1 - jt : jt;
+    return (big * (big + 1) / 2 + small) * TILE;
+  }
+  // row l % 16 of row tile it, columns 32 ks + 8 (l / 16) + 0..7; the half of them that lies across the diagonal is zero
+  static __device__ __forceinline__ LaFrag<BF16> rows(const char* part, int it, int ks, int lane) {
+    const int l = lane & 15, g = lane >> 4;
+    const bool half = REV ? 2 * ks < it : 2 * ks + 1 > it;  // one of the two tiles is not there
+    const int only = REV ? 1 : 0;
+    const int step = REV ? -TILE : TILE;  // to the next columns' tile
+    const char* const p = part + tile(it, 2 * ks + (half ? only : 0)) + (half ? 0 : (g >> 1) * step) + (g & 1) * (8 / VE * 256) + l * 16;
+    const bool in = !half || (g >> 1) == only;
+    LaFrag<BF16> f;
+    if constexpr (BF16) {
+      f.u = *(const la_u4*)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.u[i] = in ? f.u[i] : 0u;
+    } else {
+      const la_f4 a = *(const la_f4*)p, b = *(const la_f4*)(p + 256);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.f[i] = in ? a[i] : 0.0f, f.f[4 + i] = in ? b[i] : 0.0f;
+    }
+    return f;
+  }
+  // row l % 16, columns 4 (l / 16) + 0..3 of a tile
+  static __device__ __forceinline__ void put(char* t, int it, int jt, int lane, const float (&v)[4]) {
+    const int l = lane & 15, g = lane >> 4;
+    char* const p = t + tile(it, jt) + l * 16;
+    if constexpr (BF16) {
+      typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+      const u2 hi = {vec_bf16_pair(v[0], v[1]), vec_bf16_pair(v[2], v[3])};
+      const u2 lo = {vec_bf16_pair(v[0] - __builtin_bit_cast(float, hi[0] << 16), v[1] - __builtin_bit_cast(float, hi[0] & 0xFFFF0000u)),
+                     vec_bf16_pair(v[2] - __builtin_bit_cast(float, hi[1] << 16), v[3] - __builtin_bit_cast(float, hi[1] & 0xFFFF0000u))};
+      char* const q = p + (g >> 1) * 256 + 8 * (g & 1);
+      *(u2*)q = hi;
+      *(u2*)(q + PART) = lo;
+    } else {
+      *(la_f4*)(p + g * 256) = la_f4{v[0], v[1], v[2], v[3]};
+    }
+  }
+  static __device__ __forceinline__ float get(const char* t, int i, int j) {
+    const char* const p = t + tile(i >> 4, j >> 4) + ((j & 15) / VE) * 256 + (i & 15) * 16 + (j % VE) * ES;
+    float v = la_get<BF16>(p);
+    if constexpr (BF16) v += la_get<BF16>(p + PART);
+    return v;
+  }
+};
+
 // A tile on its way from memory to LDS, in registers of NT threads: pieces of 16 bytes, all loaded without a
 // branch, so that they are in flight together.  Where a piece would lie outside the tile, the nearest one inside is
 // loaded; what does not belong there is cleared when the tile is stored.
@@ -280,7 +337,7 @@ struct LaShape {
   static constexpr bool kRev = MODE == kLaFoldRev || MODE == kLaDk || MODE == kLaDv;
   static constexpr bool kOut = MODE >= kLaFwd;
   static constexpr bool kDots = MODE == kLaDq || MODE == kLaDk;
-  static constexpr int XM = BF16 && kDots ? 3 : 1;                                 // parts of M as an operand
+  static constexpr int XM = !BF16 ? 1 : kDots ? 3 : 2;          // parts of M as an operand
   static constexpr int UP = !BF16 ? 1 : MODE == kLaDv ? 2 : 3;  // of the weighted z
   static constexpr int NW = F == 256 ? 8 : 4, NT = NW * 64, NF = F / (16 * NW);
   static constexpr int C = BF16 ? kLaTile : kLaTile / 2, TI = C / 16, KS = C / 32;
@@ -288,7 +345,7 @@ struct LaShape {
   // LDS: the tiles x, y, z, w and scores, weights of y z^T, beta, sums of the columns' waves, two flags
   static constexpr int ROWX = LaTile<BF16, E>::LD * (BF16 ? 2 : 4) * C, ROWZ = LaTile<BF16, F>::LD * (BF16 ? 2 : 4) * C;
   static constexpr int kY = kOut ? ROWX : 0, kZ = kY + ROWX, kW = kZ + ROWZ, kP = kW + (kDots ? ROWZ : 0);
-  static constexpr int kU = kP + (kOut ? LaTile<BF16, C>::LD * (BF16 ? 2 : 4) * C : 0), kB = kU + 4 * C, kR = kB + 4 * C;
+  static constexpr int kU = kP + (kOut ? LaScores<BF16, C, kRev>::kBytes : 0), kB = kU + 4 * C, kR = kB + 4 * C;
   static constexpr int kWild = kR + (kDots ? 4 * NW * C : 0), kBytes = kWild + 16;
 };
 
@@ -301,7 +358,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
   constexpr int ES = BF16 ? 2 : 4;
   using TX = LaTile<BF16, E>;
   using TZ = LaTile<BF16, F>;
-  using TP = LaTile<BF16, C>;
+  using TP = LaScores<BF16, C, kRev>;
   char* const lx = smem;
   char* const ly = smem + S::kY;
   char* const lz = smem + S::kZ;
@@ -532,21 +589,8 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
             }
             if constexpr (MODE == kLaFwd || MODE == kLaDv) p[r] += j + r == i ? skip : 0.0f;
           }
-          auto put = [&](int tile, const float (&v)[4]) __attribute__((always_inline)) {
-            char* const to_p = lp + (i * TP::LD + 16 * tile + 4 * l4) * ES;
-            if constexpr (BF16) {
-              typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-              *(u2*)to_p = u2{vec_bf16_pair(v[0], v[1]), vec_bf16_pair(v[2], v[3])};
-            } else {
-              *(la_f4*)to_p = la_f4{v[0], v[1], v[2], v[3]};
-            }
-          };
-          put(jt, p);
-          if (it == jt && (kRev ? it & 1 : !(it & 1))) {  // the other half of the product's 32 columns
-            const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            put(it ^ 1, none);
-          }
-          if constexpr (MODE == kLaDq) {  // sums over the tile's columns and rows, kept between the rows of x and of the scores
+          TP::put(lp, it, jt, lane, p);
+          if constexpr (MODE == kLaDq) {  // sums over the tile's columns and rows, kept between the rows of x and of w
             ri += __shfl_xor(ri, 16);
             ri += __shfl_xor(ri, 32);
             if (l4 == 0) *(float*)(lx + (i * TX::LD + E) * ES + 4 * jt) = ri;
@@ -557,7 +601,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
               v += la_dpp32<0x4E>(v);   // quad_perm [2,3,0,1]
               v += la_dpp32<0x141>(v);  // row_half_mirror
               v += la_dpp32<0x140>(v);  // row_mirror
-              if (l16 == 0) *(float*)(lp + ((j + r) * TP::LD + C) * ES + 4 * it) = v;
+              if (l16 == 0) *(float*)(lw + ((j + r) * TZ::LD + F) * ES + 4 * it) = v;
             }
           }
         }
@@ -581,14 +625,15 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
             for (int r = 0; r < 4; ++r) v[r] = M[2 * s][nf][r], v[4 + r] = M[2 * s + 1][nf][r];
             la_split<S::XM>(v, mf[nf]);
           }
+          LaFrag<BF16> xf[TI];
 #pragma unroll
-          for (int t = 0; t < TI; ++t) {
-            const LaFrag<BF16> xf = TX::rows(lx, 16 * t, 32 * s, lane);
+          for (int t = 0; t < TI; ++t) xf[t] = TX::rows(lx, 16 * t, 32 * s, lane);
 #pragma unroll
-            for (int nf = 0; nf < NF; ++nf)
+          for (int q = S::XM - 1; q >= 0; --q)
 #pragma unroll
-              for (int q = S::XM - 1; q >= 0; --q) o[t][nf] = la_mma(mf[nf][q], xf, o[t][nf]);
-          }
+            for (int t = 0; t < TI; ++t)
+#pragma unroll
+              for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_mma(mf[nf][q], xf[t], o[t][nf]);
         }
 #pragma unroll
         for (int t = 0; t < TI; ++t) {
@@ -631,7 +676,7 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
 #pragma unroll
               for (int q = 0; q < TI; ++q) {
                 rs += q <= i2 / 16 ? *(const float*)(lx + (i2 * TX::LD + E) * ES + 4 * q) : 0.0f;
-                cs += q >= i2 / 16 ? *(const float*)(lp + (i2 * TP::LD + C) * ES + 4 * q) : 0.0f;
+                cs += q >= i2 / 16 ? *(const float*)(lw + (i2 * TZ::LD + F) * ES + 4 * q) : 0.0f;
               }
               float n = lane < C ? rs - lbeta[i2] * cs : 0.0f;
 #pragma unroll
@@ -649,24 +694,30 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
         const bool wide = !BF16 || (kDots && g.out_f32);
         const uint32_t out_es = wide ? 4 : 2, out_row = (uint32_t)g.out_st * out_es;
         const row_ptr to_out = row_at(g.out, ((int64_t)t0 * g.out_st + h * g.out_sh) * out_es);
+        if (!wild) {
+          // the rows' products in turn, so that none waits for the one before (16384 x 80 x 128 x 64: 373 us row by row, 361 in
+          // turn, 353 with those of x M in turn as well)
 #pragma unroll
-        for (int t = 0; t < TI; ++t) {
-          const int i2 = 16 * t + l16;
-          if (!wild) {
+          for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              if (kRev ? 2 * ks + 1 < t : 2 * ks > t) continue;
-              const LaFrag<BF16> pf = TP::rows(lp, 16 * t, 32 * ks, lane);
+            for (int q = TP::PARTS - 1; q >= 0; --q)
 #pragma unroll
-              for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_mma(zf[ks][nf], pf, o[t][nf]);
-            }
-          } else {
-            // a score of zero times an infinity or no number of a token that this row does not see would be no number:
-            // the products that count, one by one
+              for (int t = 0; t < TI; ++t) {
+                if (kRev ? 2 * ks + 1 < t : 2 * ks > t) continue;
+                const LaFrag<BF16> pf = TP::rows(lp + q * TP::PART, t, ks, lane);
+#pragma unroll
+                for (int nf = 0; nf < NF; ++nf) o[t][nf] = la_mma(zf[ks][nf], pf, o[t][nf]);
+              }
+        } else {
+          // a score of zero times an infinity or no number of a token that this row does not see would be no number:
+          // the products that count, one by one
+#pragma unroll
+          for (int t = 0; t < TI; ++t) {
+            const int i2 = 16 * t + l16;
 #pragma unroll 1
             for (int j = 0; j < C; ++j) {
               if (kRev ? j < i2 : j > i2) continue;
-              const float p = la_get<BF16>(lp + (i2 * TP::LD + j) * ES);
+              const float p = TP::get(lp, i2, j);
 #pragma unroll
               for (int nf = 0; nf < NF; ++nf)
 #pragma unroll
@@ -674,6 +725,10 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
                   o[t][nf][r] = __builtin_fmaf(p, la_get<BF16>(lz + (j * TZ::LD + f0 + 16 * nf + 4 * l4 + r) * ES), o[t][nf][r]);
             }
           }
+        }
+#pragma unroll
+        for (int t = 0; t < TI; ++t) {
+          const int i2 = 16 * t + l16;
           if (i2 >= nr) continue;
 #pragma unroll
           for (int nf = 0; nf < NF; ++nf) {
