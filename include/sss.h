@@ -436,7 +436,8 @@ int layer_norm_bwd(const void* dout, const void* dresidual_out, const void* x, i
  * heads, adjacent heads share one.  log_decay (tokens, heads) float32 with decay_stride, or
  * (heads) with decay_stride 0: one decay for each head.  beta (tokens, heads) float32 with
  * beta_stride, nullable; D_skip (heads) float32, nullable.  A log decay of -1e4 or less, -inf
- * included, leaves nothing of the state.  state (slots, heads, dk, dv) float32.  dk and dv up to 256
+ * included, leaves nothing of the state; its gradient is zero, and finite values on either side of it do not reach
+ * the gradients on the other.  state (slots, heads, dk, dv) float32.  dk and dv up to 256
  * (SSS_ERR_UNSUPPORTED otherwise), heads up to 65536.  Packed prompts, cache slots, alignment and
  * overlap as above.  Results are deterministic.
  *

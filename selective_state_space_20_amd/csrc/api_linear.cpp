@@ -443,6 +443,8 @@ int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_
     a.within = at(p.within);
     a.edge = at(p.edge);
     a.last = at(p.last);
+    a.g = log_decay;
+    a.g_st = decay_stride;
     a.beta = beta;
     a.beta_st = beta_stride;
     a.cu = cu_seqlens;

@@ -11,6 +11,7 @@
 namespace sss {
 
 constexpr int kLaTile = 64;  // tokens of a tile (bf16); fp32 takes 32
+constexpr float kLaCut = -1e4f;  // a log decay up to this leaves nothing of the state, whatever those beside it
 
 // One operand of (tokens, heads, width): elements between tokens and between heads, and how many
 // of the call's heads share one of its heads.
@@ -87,6 +88,8 @@ struct LaFinish {
   const float* within;
   const float* edge;
   const float* last;
+  const float* g;
+  int64_t g_st;
   const float* beta;
   int64_t beta_st;
   const int32_t* cu;

@@ -328,9 +328,9 @@ __device__ __forceinline__ double la_lane(double v, int l) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// log decays below this leave nothing of a state in fp32; kept finite, so that differences of
+// log decays up to kLaCut leave nothing of a state in fp32; kept finite, so that differences of
 // their sums are numbers (a NaN stays one)
-__device__ __forceinline__ double la_log2_decay(float g) { return (g < -1e4f ? -1e4 : (double)g) * 1.4426950408889634074; }
+__device__ __forceinline__ double la_log2_decay(float g) { return (double)(g < kLaCut ? kLaCut : g) * 1.4426950408889634074; }
 
 template <bool BF16, int E, int F, int MODE>
 struct LaShape {
@@ -517,6 +517,8 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
       const double x = la_prefix(la_log2_decay(alive ? rg : 0.0f)), tot = la_lane(x, 63);
       const float b = alive ? rb : 0.0f, keep = fast_exp2((float)tot);
       if constexpr (!kOut) total += tot;
+      // the tokens that nothing before them reaches
+      const uint64_t cuts = MODE == kLaDq ? __builtin_amdgcn_ballot_w64(alive && rg <= kLaCut) : 0;
       if (wave == 0 && lane < C) {
         const float in = fast_exp2((float)x), out = fast_exp2((float)(tot - x));
         *lg(lane) = x;
@@ -678,11 +680,14 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
                 rs += q <= i2 / 16 ? *(const float*)(lx + (i2 * TX::LD + E) * ES + 4 * q) : 0.0f;
                 cs += q >= i2 / 16 ? *(const float*)(lw + (i2 * TZ::LD + F) * ES + 4 * q) : 0.0f;
               }
+              // Summed from the right.  Tokens behind a cut add up to zero, but in their roundings alone, which would reach the
+              // tokens before it: none is taken from lanes that have one between.
               float n = lane < C ? rs - lbeta[i2] * cs : 0.0f;
+              const uint64_t behind = cuts >> lane >> 1;
 #pragma unroll
               for (int d = 1; d < C; d *= 2) {
                 const float up = __shfl_down(n, d);
-                if (lane + d < C) n += up;
+                if (lane + d < C && (behind & (((uint64_t)1 << d) - 1)) == 0) n += up;
               }
               if (in) {
                 g.within[at] = n;

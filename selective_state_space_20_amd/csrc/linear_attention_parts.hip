@@ -93,8 +93,9 @@ hipError_t la_carry(const LaCarry& fwd, const LaCarry* rev, int64_t hs, int H, i
 // outside (through) the sum of r of all tiles to the right less that of c from the tile on.  The last tile of a
 // segment's part of a sequence starts that sum with a `through` of its own, formed without a difference.  (Whole dq
 // and dk would do as well, but roundings of pairs that cancel would be carried over the segment: 3e-5 of dg's norm in
-// place of 3e-7.)  A wave per segment and head; the sums are 64-bit.  Bound by the latency of a wave's tiles in turn:
-// 8192 tokens x 16 heads in 16 segments 11 us, 1001 x 6 in 32 4 us.
+// place of 3e-7.)  Nothing passes a token whose decay is a cut (kLaCut): its dg is zero, and so is a tile's `through` that
+// has one, exactly, where the difference would leave roundings of however large sums behind it.  A wave per segment and head; the sums are 64-bit.  Bound by the latency of a wave's tiles in turn:
+// 8192 tokens x 16 heads in 16 segments 10 us, 1001 x 6 in 32 4 us.
 static __global__ __launch_bounds__(64) void la_finish_kernel(LaFinish a) {
   const int lane = threadIdx.x;
   const int h = (int)(blockIdx.x % (unsigned)a.H), seg = (int)(blockIdx.x / (unsigned)a.H);
@@ -124,18 +125,25 @@ static __global__ __launch_bounds__(64) void la_finish_kernel(LaFinish a) {
     const int e = min(end, tend);
     double through = end > tend ? a.edge[seg * H + h] : a.last[s * H + h], x = 0.0;
     const int last = (e - t - 1) / a.tile;
+    // a tile's values, asked for during the tile before (the decays, which lie apart, cost 2 us of 8192 tokens x 16 heads otherwise)
+    float next[6];
+    auto fetch = [&](int m) {
+      const int at = min(t + a.tile * m + lane, e - 1);
+      const int64_t p = (int64_t)h * a.tokens + at;
+      next[0] = a.rows[p];
+      next[1] = a.cols2[p];
+      next[2] = a.within[p];
+      next[3] = a.dbeta != nullptr ? a.cols[p] : 0.0f;
+      next[4] = a.beta != nullptr ? a.beta[at * a.beta_st + h] : 1.0f;
+      next[5] = a.g[at * a.g_st + h];
+    };
+    fetch(last);
     for (int m = last; m >= 0; --m) {
       const int at = t + a.tile * m + lane;
-      const bool in = lane < a.tile && at < e;
-      float r = 0.0f, c = 0.0f, w = 0.0f;
-      if (in) {
-        const int64_t p = (int64_t)h * a.tokens + at;
-        r = a.rows[p];
-        c = a.cols2[p];
-        w = a.within[p];
-        if (a.dbeta != nullptr) a.dbeta[at * H + h] = a.cols[p] + c;
-        if (a.beta != nullptr) c *= a.beta[at * a.beta_st + h];
-      }
+      const bool in = lane < a.tile && at < e, cut = in && next[5] <= kLaCut;
+      const float r = in ? next[0] : 0.0f, w = next[2], c0 = next[1], k = next[3], c = in ? c0 * next[4] : 0.0f;
+      if (m > 0) fetch(m - 1);
+      if (in && a.dbeta != nullptr) a.dbeta[at * H + h] = k + c0;
       double rs = (double)r, cs = (double)c;  // from the lane on; up to the lane
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
@@ -144,9 +152,10 @@ static __global__ __launch_bounds__(64) void la_finish_kernel(LaFinish a) {
         if (lane >= d) cs += dn;
       }
       if (m != last) through = x - __shfl(cs, 63);
+      if (__builtin_amdgcn_ballot_w64(cut) != 0) through = 0.0;
       x = through + __shfl(rs, 0);
       if (in) {
-        const double v = through + rs + (cs - (double)c) + (double)w;
+        const double v = cut ? 0.0 : through + rs + (cs - (double)c) + (double)w;
         if (a.part == nullptr) a.dg[at * H + h] = (float)v;
         else sum += v;
       }
@@ -253,7 +262,7 @@ static __global__ __launch_bounds__(256) void la_step_kernel(LaStep a) {
     lk[tid] = la_get<BF16>(k, tid) * (a.beta != nullptr ? a.beta[b * a.beta_st + h] : 1.0f);
   }
   const float gv = a.g[b * a.g_st + h];
-  const float decay = fast_exp2((float)((double)(gv < -1e4f ? -1e4f : gv) * 1.4426950408889634074));
+  const float decay = fast_exp2((float)((double)(gv < kLaCut ? kLaCut : gv) * 1.4426950408889634074));
   const char* const vp = a.v.p + ((h / a.v.rep) * a.v.sh + b * a.v.st) * ES;
   float v[V], o[V];
 #pragma unroll
