@@ -343,8 +343,7 @@ int linear_attention_packed_bwd(const void* q, int64_t q_stride, int64_t q_head_
   const int cus = current_device_cus();
   if (cus <= 0) return SSS_ERR_HIP;
   const Plan p = plan(tokens, nseq, heads, q_heads, k_heads, dk, dv, true, cus);
-  if (!launch_ok(3 * p.nseg * heads) || !launch_ok(nseq) || (double)tokens * (double)heads * (double)dk + 256.0 > kMaxThreads)
-    return SSS_ERR_BAD_DIM;
+  if (!launch_ok(3 * p.nseg * heads)) return SSS_ERR_BAD_DIM;
   if (p.total > 0) {
     if (workspace == nullptr || workspace_bytes < p.total) return SSS_ERR_WORKSPACE;
     r.output(workspace, (int64_t)p.total, 16);

@@ -183,26 +183,29 @@ hipError_t la_finish(const LaFinish& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// A thread per element, up to 2^30 threads: a launch counts them in 32 bits.
+constexpr int64_t kLaSumBlocks = (int64_t)1 << 22;
 template <bool BF16>
 static __global__ __launch_bounds__(256) void la_sum_heads_kernel(LaSum a, LaSum b, int64_t tokens, int heads, int d) {
   const bool second = blockIdx.y != 0;
   const float* const part = second ? b.part : a.part;
   char* const out = (char*)(second ? b.out : a.out);
   const int rep = second ? b.rep : a.rep;
-  const int64_t n = tokens * (heads / rep) * d, i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // an element of out
-  if (i >= n) return;
-  const int64_t row = i / d;
-  const float* p = part + row * rep * d + (i - row * d);
-  float s = 0.0f;
-  for (int r = 0; r < rep; ++r) s += p[(int64_t)r * d];
-  if constexpr (BF16) ((uint16_t*)out)[i] = (uint16_t)vec_bf16_pair(s, 0.0f);
-  else ((float*)out)[i] = s;
+  const int64_t n = tokens * (heads / rep) * d;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {  // an element of out
+    const int64_t row = i / d;
+    const float* p = part + row * rep * d + (i - row * d);
+    float s = 0.0f;
+    for (int r = 0; r < rep; ++r) s += p[(int64_t)r * d];
+    if constexpr (BF16) ((uint16_t*)out)[i] = (uint16_t)vec_bf16_pair(s, 0.0f);
+    else ((float*)out)[i] = s;
+  }
 }
 
 hipError_t la_sum_heads(const LaSum& a, const LaSum* b, int64_t tokens, int heads, int d, bool bf16, hipStream_t stream) {
   const int rep = b != nullptr ? std::min(a.rep, b->rep) : a.rep;
   const int64_t n = tokens * (heads / rep) * d;
-  const dim3 grid((unsigned)((n + 255) / 256), b != nullptr ? 2 : 1);
+  const dim3 grid((unsigned)std::min((n + 255) / 256, kLaSumBlocks), b != nullptr ? 2 : 1);
   if (bf16) hipLaunchKernelGGL(la_sum_heads_kernel<true>, grid, dim3(256), 0, stream, a, b != nullptr ? *b : a, tokens, heads, d);
   else hipLaunchKernelGGL(la_sum_heads_kernel<false>, grid, dim3(256), 0, stream, a, b != nullptr ? *b : a, tokens, heads, d);
   return hipGetLastError();
@@ -210,14 +213,15 @@ hipError_t la_sum_heads(const LaSum& a, const LaSum* b, int64_t tokens, int head
 
 static __global__ __launch_bounds__(256) void la_empty_kernel(const int32_t* __restrict__ cu, const float* __restrict__ dfinal,
                                                               float* __restrict__ dinitial, int nseq, int tokens, int64_t per) {
-  const int64_t s = blockIdx.x;
   const int lo = min(max(cu[0], 0), tokens), hi = min(max(cu[nseq], 0), tokens);
-  if (min(cu[s + 1], hi) > max(cu[s], lo)) return;
-  for (int64_t i = threadIdx.x; i < per; i += 256) dinitial[s * per + i] = dfinal != nullptr ? dfinal[s * per + i] : 0.0f;
+  for (int64_t s = blockIdx.x; s < nseq; s += gridDim.x) {
+    if (min(cu[s + 1], hi) > max(cu[s], lo)) continue;
+    for (int64_t i = threadIdx.x; i < per; i += 256) dinitial[s * per + i] = dfinal != nullptr ? dfinal[s * per + i] : 0.0f;
+  }
 }
 
 hipError_t la_empty(const int32_t* cu, const float* dfinal, float* dinitial, int nseq, int tokens, int64_t per, hipStream_t stream) {
-  hipLaunchKernelGGL(la_empty_kernel, dim3((unsigned)nseq), dim3(256), 0, stream, cu, dfinal, dinitial, nseq, tokens, per);
+  hipLaunchKernelGGL(la_empty_kernel, dim3((unsigned)std::min(nseq, 1 << 22)), dim3(256), 0, stream, cu, dfinal, dinitial, nseq, tokens, per);
   return hipGetLastError();
 }
 
