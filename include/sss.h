@@ -404,7 +404,7 @@ int rms_norm_residual_bwd(const void* dout, const void* dresidual_out, const voi
  * x (rows, dim) and out (contiguous) in io_dtype; residual and residual_out (contiguous: h) in
  * residual_dtype (ignored where neither is given); weight, bias (dim) float32; mean, rstd (rows,
  * dim / group) float32: outputs for the gradients call.  Nullable: residual (zero), weight (one), bias (zero), residual_out, mean, rstd.
- * out is of h before it is rounded to residual_dtype.  residual_out may be residual itself
+ * out, mean and rstd are of h before it is rounded to residual_dtype.  residual_out may be residual itself
  * (contiguous), no other overlap.  Required: x, out. */
 int layer_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const float* weight,
                    const float* bias, void* out, void* residual_out, float* mean, float* rstd, int64_t rows, int64_t dim,
@@ -415,7 +415,8 @@ size_t layer_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group, i
 
 /* Its gradients for L = sum(dout * out) + sum(dresidual_out * residual_out) (dresidual_out nullable:
  * zero).  x (rows, dim) in x_dtype is what was normed: the forward call's x, or its residual_out; mean, rstd as
- * it left them.  dout and dx (rows, dim) in io_dtype, dresidual_out and dresidual (nullable) in x_dtype, all
+ * it left them (of a bf16 residual_out, those of the sum before it was rounded: the gradient is then that of the norm of the
+ * sum, but for half a step of the stream in each of its values).  dout and dx (rows, dim) in io_dtype, dresidual_out and dresidual (nullable) in x_dtype, all
  * contiguous; dx and dresidual are the same gradient (of x and of the residual).  dweight (dim), required
  * with weight, and dbias (dim), nullable, float32, are summed over the rows in a fixed order; with no
  * rows they are zero. */

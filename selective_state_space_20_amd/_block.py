@@ -549,7 +549,7 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, *, group_size=None,
     x (rows, dim) float32 or bfloat16, residual (rows, dim) float32 or bfloat16, rows may be strided;
     weight, bias (dim) float32.  Returns out in x's dtype; with a residual (or residual_out) also
     residual_out = h in its dtype, which may be the residual itself; and with return_stats the (rows,
-    groups) float32 mean and rstd that layer_norm_bwd takes."""
+    groups) float32 mean and rstd that layer_norm_bwd takes, like out of h before it is rounded to its dtype."""
     torch = torch_()
     gpu = x.get_device()
     rows, dim = _two_d(x, "x")
