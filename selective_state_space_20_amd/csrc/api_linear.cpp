@@ -121,8 +121,8 @@ Plan plan(int64_t tokens, int64_t nseq, int64_t heads, int64_t q_heads, int64_t 
   return p;
 }
 
-// workgroups of the walks have at most 512 threads
-bool launch_ok(int64_t groups) { return (double)groups * 512.0 <= kMaxThreads; }
+// workgroups of the walks have at most 512 threads, of the step 256
+bool launch_ok(int64_t groups, int threads = 512) { return (double)groups * (double)threads <= kMaxThreads; }
 
 struct Fwd {
   Side q, k, v;
@@ -275,7 +275,7 @@ int linear_attention_update_slots(const void* q, int64_t q_stride, int64_t q_hea
   r.output(out, batch * heads * dv * es, es);
   if (!r.aligned) return SSS_ERR_UNSUPPORTED;
   if (!r.ok()) return SSS_ERR_ALIAS;
-  if (!launch_ok(batch * heads)) return SSS_ERR_BAD_DIM;
+  if (!launch_ok(batch * heads, 256)) return SSS_ERR_BAD_DIM;
   if (batch == 0) return SSS_OK;
   LaStep a{};
   a.q = f.q.on(heads);
