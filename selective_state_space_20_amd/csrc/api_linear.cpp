@@ -33,6 +33,7 @@ int dims_status(int64_t tokens, int64_t nseq, int64_t slots, int64_t heads, int6
       heads > kMaxHeads || q_heads < 1 || k_heads < 1 || heads % q_heads != 0 || heads % k_heads != 0 || dk < 1 || dv < 1)
     return SSS_ERR_BAD_DIM;
   if (dk > kMaxHeadDim || dv > kMaxHeadDim) return SSS_ERR_UNSUPPORTED;
+  if ((double)slots * (double)heads * (double)(dk * dv) > 1.0e18) return SSS_ERR_BAD_DIM;  // bytes in 64 bits
   return SSS_OK;
 }
 

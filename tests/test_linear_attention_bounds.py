@@ -2,13 +2,22 @@
 addresses, never met), and the step's launch is counted in the threads that it has."""
 import pytest
 
-from .test_linear_attention_refusals import BAD_DIM, P, step
+from .test_linear_attention_refusals import BAD_DIM, P, attention, grads, step
 
 
 def test_a_step_of_too_many_workgroups_is_refused():
     for batch, heads in ((1 << 24, 1), (1 << 18, 64)):  # 2^32 threads
         assert step(batch=batch, heads=heads, q_heads=1, k_heads=1, slots=1, idx=6 * P + (P >> 1), dk=1, dv=1, gs=heads, bs=heads,
                     vs=heads) == BAD_DIM
+
+
+HUGE = dict(heads=1 << 16, q_heads=1, k_heads=1, gs=1 << 16, bs=1 << 16, vs=1 << 24, dk=256, dv=256, vh=256)
+
+
+@pytest.mark.parametrize("call, count", [(attention, "slots"), (step, "slots"), (grads, "nseq")])
+def test_states_of_more_bytes_than_64_bits_count(call, count):
+    for n in (1 << 28, 1 << 29, 1 << 30):  # 2^62, 2^63 and 2^64 bytes
+        assert call(**HUGE, **{count: n}) == BAD_DIM, n
 
 
 @pytest.mark.gpu
