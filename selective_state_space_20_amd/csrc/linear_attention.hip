@@ -756,7 +756,8 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
       }
 
       if constexpr (!kOut) take_z();
-      // M <- e^(G_C) M + sum_j weight_j y_j z_j^T
+      // M <- e^(G_C) M + sum_j weight_j y_j z_j^T; of the parts of a product none waits for the one before, as above
+      // (16384 x 80 x 128 x 64 315 -> 307 us, gradients of 8192 x 16 x 128 x 128 216 -> 211)
 #pragma unroll
       for (int t = 0; t < ET; ++t)
 #pragma unroll
@@ -774,12 +775,16 @@ __device__ __forceinline__ void la_walk(const LaWalk& g, char* smem, unsigned id
           la_split<S::UP>(v, wz[nf]);
         }
 #pragma unroll
-        for (int t = 0; t < ET; ++t) {
-          const LaFrag<BF16> yf = TX::template cols<8>(ly, 32 * ks, 32 * (t >> 1) + 4 * (t & 1), lane);
+        for (int t = 0; t < ET; t += 4) {
+          LaFrag<BF16> yf[4];
 #pragma unroll
-          for (int nf = 0; nf < NF; ++nf)
+          for (int i = 0; i < 4; ++i) yf[i] = TX::template cols<8>(ly, 32 * ks, 32 * ((t + i) >> 1) + 4 * ((t + i) & 1), lane);
 #pragma unroll
-            for (int q = S::UP - 1; q >= 0; --q) M[t][nf] = la_mma(yf, wz[nf][q], M[t][nf]);
+          for (int q = S::UP - 1; q >= 0; --q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int nf = 0; nf < NF; ++nf) M[t + i][nf] = la_mma(yf[i], wz[nf][q], M[t + i][nf]);
         }
       }
     }
