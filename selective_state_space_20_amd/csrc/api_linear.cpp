@@ -70,12 +70,13 @@ struct Plan {
 // Segments: one round of the workgroups that the GPU holds at a time, two per CU, one where a side of the states is above
 // 128 (LDS); of the gradients' walks one round of dq and dk, and dv, where it is in their launch, follows into the places
 // that dk leaves, half as long.  Each segment is of a tile of fp32 at least.  Measured, 8192 tokens where not said,
-// prompts: 32768 x 16 heads of 128 x 128 268 us in 32 segments, one round, 302-365 in 16 or 12; 8 heads of
-// 256 x 256 132 in 32, 157 in 16, 209 in 64; 8 of 128 x 256 78, 103 and 105.  Gradients: 16 heads of 64 x 64 94 us in 16,
-// 134 in 10, 114 in 21, 97 in 32; 16 of 128 x 128 241 in 16 as in 10, 272 in 32, 424 in 4; 16 of 128 x 64 182 in 16,
-// 259 in 10, 235 in 21; 8 of 128 x 256 241 in 16, 364 in 10, 253 in 32; 8 of 256 x 256 437 in 16, 550 in 10, 526 in
-// 32; 1001 tokens x 6 heads of 64 x 50 in fp32 55 us in 32, 56 in 16, 65 in 8, 93 in 4.  The other way: 8 fp32 heads of
-// 128 x 128 284 in 32, 276 in 21.
+// prompts: 32768 x 16 heads of 128 x 128 248 us in 32 segments, one round, 291-355 in 16 or 12; 8 heads of
+// 256 x 256 169 in 32, 208 in 16, 243 in 64; 8 of 128 x 256 85, 107 and 115.  Gradients: 16 heads of 64 x 64 93 us in 16,
+// 128 in 10, 114 in 21, 98 in 32; 16 of 128 x 128 209 in 16, 225 in 10, 236 in 32, 384 in 4; 16 of 128 x 64 161 in 16,
+// 233 in 10, 217 in 21; 8 of 128 x 256 236 in 16, 358 in 10, 258 in 32; 8 of 256 x 256 457 in 16, 545 in 10, 543 in
+// 32; 1001 tokens x 6 heads of 64 x 50 in fp32 46 us in 32, 46 in 16, 57 in 8, 85 in 4.  The other way: gradients of 8 fp32
+// heads of 128 x 128 288 in 32, 278 in 21; prompts of 300 heads of 64 x 64, for which a round is rounded down to one
+// segment, 481, 372 in two.
 Plan plan(int64_t tokens, int64_t nseq, int64_t heads, int64_t q_heads, int64_t k_heads, int64_t dk, int64_t dv, bool grads,
           int cus) {
   Plan p{};

@@ -30,16 +30,16 @@
 // (301 -> 289 us of the gradients below, as they were) and leave 6e-6 of dg's norm instead of 3e-7.
 //
 // What bounds it.  The bytes are few (16384 tokens x 80 heads of 128 x 64: 449 MB, 85 us at a copy's rate) and so is
-// the arithmetic (0.1 TFLOP with the extra parts, 75 us at a large product's rate); what is left is the chain of a
+// the arithmetic (0.15 TFLOP with the extra parts, 120 us at a large product's rate); what is left is the chain of a
 // tile: loads to LDS, barrier, scores, barrier, the products that need them and M, with two workgroups of four waves
 // per CU (LDS and the registers of M) to fill each other's gaps.  So a tile is as long as LDS allows, its loads are
 // in flight during the tile before, without branches, the scores' triangle is shared evenly by the waves, and the
 // segments are one round of workgroups: a second would pay another fold and carry.
-//   16384 x 80 x 128 x 64, q and k shared, prompts   353 us (of it the fold 43, carry 11)
-//   32768 x 16 x 128 x 128, prompts                  259 us (of it the fold 76, carry 15)
-//   8192 x 16 x 128 x 128, gradients                 234 us (of it the folds 45, carry 14); in launches of
-//                                                    their own, each a round of workgroups, 298
-//   1001 x 6 x 64 x 50 fp32, gradients                55 us (folds 9, carry 8, dq dk dv 24, sums 11); apart 96
+//   16384 x 80 x 128 x 64, q and k shared, prompts   333-352 us (fold 42, carry 11, walk 314, traced)
+//   32768 x 16 x 128 x 128, prompts                  246-262 us (fold 79, carry 15, walk 180: 3.0 TB/s)
+//   8192 x 16 x 128 x 128, gradients                 225-236 us (folds 43, carry 15, dq dk dv 176); in
+//                                                    launches of their own, each a round of workgroups, 298
+//   1001 x 6 x 64 x 50 fp32, gradients                50-54 us (folds 9, carry 8, dq dk dv 24, sums 11); apart 96
 // Measured and no better: eight waves for 128 columns, swizzled rows instead of padded ones, rows without any bank
 // conflict (half of them gone, the same time), three smaller workgroups per CU, scores dealt tile by tile to the
 // waves, two heads per workgroup where they share q and k, nontemporal loads.

@@ -48,7 +48,7 @@ hipError_t la_launch_grads(int E, int F, bool bf16, const LaWalk& dq, const LaWa
 // One thread per element of the heads' states, over the segments in turn, the loads of sixteen at once (without
 // regard to the flags, which come with them: where one is 0 nothing was written, and nothing is used).  Lanes of
 // a wave whose elements are of one head share a decay.  blockIdx.y 1: backwards.  Bound by latency, a trip to
-// memory per sixteen segments: both directions of 16 segments x 16 heads x 128 x 128 take 14 us (63 MB), of 32 segments
+// memory per sixteen segments: both directions of 16 segments x 16 heads x 128 x 128 take 15 us (63 MB), of 32 segments
 // x 6 x 64 x 50 8 us; with eight loads at once and a launch for each direction 34 (32 segments) and 20.
 constexpr int kLaCarryBatch = 16;
 static __global__ __launch_bounds__(256) void la_carry_kernel(LaCarry fwd, LaCarry back, int64_t hs, int H, int nseg) {

@@ -9,7 +9,8 @@ of values at the lower end of their binade, 2^-8 / sqrt(3) of their norm.  fp32 
 roundings in turn, of either sign and each uniform, leave sqrt(n / 3) eps of the norm, n the tokens of the longest
 sequence, each a product that is added to a state, and 500 for inner axes, tiles, weights and joins; twice that for
 the gradients of decays and weights, which two such sums make.  (333 tokens: 17 eps, 4500: 41 eps.)  The gradient of a head's one decay is a sum over all tokens whose parts cancel: its error is no more
-than the sum of theirs, sqrt(tokens) times the norm of these (Cauchy-Schwarz), of which each of them has its share."""
+than the sum of theirs, sqrt(tokens) times the norm of these (Cauchy-Schwarz), of which each of them has its share.
+One part of the scores or of the states as operands of bf16 results, two where fp32 results come of them, fail."""
 import pytest
 
 from . import linear_ref as ref
